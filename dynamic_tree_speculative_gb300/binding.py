@@ -17,13 +17,14 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libspec_tree.so")
 
-BF16, F32 = 0, 1
+BF16, F32, F16 = 0, 1, 2   # F16: key-value cache, queries and attention outputs only
 BUILDER_TOPR, BUILDER_SMART = 0, 1
 PROBE_FIRST, PROBE_LAST = 0, 1
 ROOT, DET, PROBE, FILL = 0, 1, 2, 3
 OK, E_PARAM, E_LAYOUT, E_CUDA = 0, -1, -3, -4
 S_NONFINITE_DRAFT, S_NONFINITE_TARGET, S_RESIDUAL_EMPTY = 1, 2, 4
 S_OVERFLOW, S_TIMEOUT, S_ROWS, S_LAYERS = 8, 16, 32, 64
+S_PAGES, S_NODES = 128, 256
 MAX_SUPPORT = 1024
 SUPPORT_DENSE = 0x40000000   # |S| = V for any vocabulary
 DENSE_MAX_K = 64
@@ -33,7 +34,8 @@ DEFAULT_SUPPORT = 128
 EXPORTS = ("spec_tree_rows_needed", "spec_tree_check_params", "spec_tree_select_expand", "spec_tree_rank",
            "spec_tree_build", "spec_tree_verify", "spec_tree_layer_state_bytes", "spec_tree_layer_rows",
            "spec_tree_layer", "spec_tree_finish", "spec_tree_layer_static", "spec_tree_smart_fit",
-           "spec_tree_wait_selftest", "spec_tree_verify_dense", "spec_tree_strerror")
+           "spec_tree_wait_selftest", "spec_tree_verify_dense", "spec_tree_kv_append", "spec_tree_attend",
+           "spec_tree_attend_workspace_bytes", "spec_tree_kv_commit", "spec_tree_strerror")
 
 
 class SpecTreeError(RuntimeError):
@@ -54,6 +56,23 @@ class c_tree(ctypes.Structure):
         "n_nodes", "sup_id", "sup_q", "sup_qT", "sup_z", "sup_zT", "probe_pos")] + [
         ("n_rows", ctypes.c_int32), ("max_nodes", ctypes.c_int32), ("sup_stride", ctypes.c_int32),
         ("sched", ctypes.c_void_p)]
+
+
+class c_kv(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "page_table", "seq_len")] + [
+        (n, ctypes.c_int64) for n in ("layer_stride", "page_stride", "token_stride", "head_stride")] + [
+        (n, ctypes.c_int32) for n in ("dtype", "n_layers", "n_pages", "page_size", "n_kv_heads", "head_dim",
+                                      "max_pages", "table_stride")]
+
+
+class c_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("tree_stride", "node_stride",
+                                                                            "head_stride")]
+
+
+class c_nodes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("parent", "depth", "n_nodes")] + [
+        (n, ctypes.c_int32) for n in ("stride", "begin", "count")]
 
 
 def _load():
@@ -77,10 +96,17 @@ def _load():
     dp = ctypes.POINTER(ctypes.c_double)
     lib.spec_tree_smart_fit.argtypes = [i32, dp, dp, dp, ctypes.c_double, dp, P, dp, dp]
     lib.spec_tree_wait_selftest.argtypes = [ctypes.c_uint32, vp, vp, vp]
+    KV, N, H = ctypes.POINTER(c_kv), ctypes.POINTER(c_nodes), ctypes.POINTER(c_heads)
+    lib.spec_tree_kv_append.argtypes = [i32, KV, i32, N, i32, H, H, H, H, vp, i32, i32, i32, vp, vp, ctypes.c_float,
+                                        vp, vp]
+    lib.spec_tree_attend.argtypes = [i32, KV, i32, N, i32, H, H, ctypes.c_float, vp, ctypes.c_size_t, vp, vp]
+    lib.spec_tree_attend_workspace_bytes.argtypes = [i32] * 5
+    lib.spec_tree_attend_workspace_bytes.restype = ctypes.c_size_t
+    lib.spec_tree_kv_commit.argtypes = [i32, KV, vp, vp, i32, vp, vp, vp]
     lib.spec_tree_strerror.argtypes = [i32]
     lib.spec_tree_strerror.restype = ctypes.c_char_p
     for name in EXPORTS:
-        if name not in ("spec_tree_strerror", "spec_tree_layer_state_bytes"):
+        if name not in ("spec_tree_strerror", "spec_tree_layer_state_bytes", "spec_tree_attend_workspace_bytes"):
             getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -341,3 +367,154 @@ def spec_tree_wait_selftest(polls: int, status: torch.Tensor, result: torch.Tens
     """Let one CTA-scope and one cluster-scope bounded wait run out (`polls` polls each) on a barrier
     nothing arrives on; result (4 x int32 on the device) = gave up / polls made, per CTA."""
     _check(_lib.spec_tree_wait_selftest(polls, _ptr(status), _ptr(result), _stream(stream)))
+
+
+# --------------------------------------------------- the model's side of a step ---
+
+_HALF = {torch.bfloat16: BF16, torch.float16: F16}
+
+
+class KVCache:
+    """A paged key-value cache (the spec_tree_kv_t of the C ABI).
+
+    k, v: [layers][pages][page_size][kv heads][head_dim], bf16 or f16, any strides with contiguous
+    head_dim (a [layers][pages][heads][page_size][head_dim] pool is passed transposed);
+    page_table: int32 [B][max_pages]; seq_len: int32 [B], committed tokens.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor):
+        if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+            raise SpecTreeError("k and v must be alike, [layers][pages][page_size][kv heads][head_dim]")
+        if k.dtype not in _HALF:
+            raise SpecTreeError(f"unsupported cache dtype {k.dtype}")
+        if k.stride(4) != 1:
+            raise SpecTreeError("head_dim must be contiguous")
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1:
+            raise SpecTreeError("page_table must be int32 [B][max_pages] with contiguous rows")
+        self.k, self.v, self.page_table, self.B = k, v, page_table, page_table.shape[0]
+        layers, pages, size, heads, dim = k.shape
+        c = c_kv(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), None, k.stride(0), k.stride(1), k.stride(2),
+                 k.stride(3), _HALF[k.dtype], layers, pages, size, heads, dim, page_table.shape[1],
+                 max(page_table.stride(0), page_table.shape[1]))
+        self._c = c
+        self.set_lengths(seq_len)
+
+    def set_lengths(self, seq_len: torch.Tensor):
+        """Committed tokens from now on, e.g. the new_len of spec_tree_kv_commit."""
+        _int_rows("seq_len", seq_len, (self.B,))
+        self.seq_len = seq_len
+        self._c.seq_len = seq_len.data_ptr()
+
+    def c(self) -> c_kv:
+        return self._c
+
+
+@dataclasses.dataclass
+class NodeArrays:
+    """Node arrays of a batch of trees where no TreeBuffers holds them (a drafter's frontiers, a chain with
+    n_nodes alone): int32 node_parent, node_depth [B][nodes] and n_nodes [B], each or None."""
+    node_parent: Optional[torch.Tensor] = None
+    node_depth: Optional[torch.Tensor] = None
+    n_nodes: Optional[torch.Tensor] = None
+
+
+def _int_rows(name: str, t: torch.Tensor, shape):
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise SpecTreeError(f"{name} must be contiguous int32 {list(shape)}")
+
+
+def _nodes(tree, B: int, begin: int, count: int) -> c_nodes:
+    """spec_tree_nodes_t of a TreeBuffers, a NodeArrays or None (a chain of which every node exists)."""
+    if tree is None:
+        return c_nodes(None, None, None, 0, begin, count)
+    parent, depth, n = tree.node_parent, tree.node_depth, tree.n_nodes
+    stride = 0
+    if parent is not None:
+        stride = parent.shape[1] if parent.dim() == 2 else 0
+        _int_rows("node_parent", parent, (B, stride))
+        if depth is not None:
+            _int_rows("node_depth", depth, (B, stride))
+    elif depth is not None:
+        raise SpecTreeError("node_depth without node_parent")
+    if n is not None:
+        _int_rows("n_nodes", n, (B,))
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    return c_nodes(at(parent), at(depth), at(n), stride, begin, count)
+
+
+def _heads(name: str, x: torch.Tensor, cache: KVCache, count: Optional[int] = None, heads: Optional[int] = None):
+    if x.dim() != 4 or x.dtype != cache.k.dtype or x.stride(3) != 1 or x.shape[0] != cache.B or \
+            x.shape[3] != cache.k.shape[4] or (count is not None and x.shape[1] != count) or \
+            (heads is not None and x.shape[2] != heads):
+        raise SpecTreeError(f"{name} must be [B][nodes][heads][head_dim] of the cache's dtype, head_dim contiguous")
+    return c_heads(x.data_ptr(), x.stride(0), x.stride(1), x.stride(2))
+
+
+def rope_table(rows: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Cosines and sines of positions 0 .. rows - 1, [rows][rot_dim] float32: row t holds cos(t f_j), then
+    sin(t f_j), f_j = base^(-2 j / rot_dim); the angles are taken in float64."""
+    half = rot_dim // 2
+    f = base ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
+    a = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+def spec_tree_kv_append(cache: KVCache, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        q_out: torch.Tensor, rope: Optional[torch.Tensor], status: torch.Tensor, tree=None,
+                        node_begin: int = 0, q_weight: Optional[torch.Tensor] = None,
+                        k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                        stream=None):
+    """Nodes node_begin .. node_begin + q.shape[1] - 1 of every tree: head norms (with weights), rotation
+    (with a rope table [rows][rot_dim]), keys and values into the cache, queries to q_out."""
+    n, dim = q.shape[1], cache.k.shape[4]
+    cq, ck, cv = _heads("q", q, cache), _heads("k", k, cache, n, cache.k.shape[3]), _heads("v", v, cache, n,
+                                                                                           cache.k.shape[3])
+    co = _heads("q_out", q_out, cache, n, q.shape[2])
+    rows = rot = 0
+    if rope is not None:
+        if rope.dim() != 2 or rope.dtype != torch.float32 or not rope.is_contiguous():
+            raise SpecTreeError("rope must be contiguous float32 [rows][rot_dim]")
+        rows, rot = rope.shape
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and (w.dtype != cache.k.dtype or tuple(w.shape) != (dim,) or not w.is_contiguous()):
+            raise SpecTreeError(f"{name} must be [head_dim] of the cache's dtype")
+    nodes = _nodes(tree, cache.B, node_begin, n)
+    _check(_lib.spec_tree_kv_append(cache.B, ctypes.byref(cache.c()), layer, ctypes.byref(nodes), q.shape[2],
+                                    ctypes.byref(cq), ctypes.byref(ck), ctypes.byref(cv), ctypes.byref(co),
+                                    _ptr(rope), rows, rot, int(interleaved), _ptr(q_weight), _ptr(k_weight), eps,
+                                    _ptr(status), _stream(stream)))
+
+
+class AttendWorkspace:
+    """Workspace of spec_tree_attend for calls of up to B trees and `count` nodes (one call at a time)."""
+
+    def __init__(self, B: int, count: int, n_q_heads: int, n_kv_heads: int, head_dim: int, device="cuda"):
+        with torch.cuda.device(device):
+            n = _lib.spec_tree_attend_workspace_bytes(B, count, n_q_heads, n_kv_heads, head_dim)
+        if n == 0:
+            raise SpecTreeError("spec_tree_attend takes no such heads or nodes")
+        self.data = torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def spec_tree_attend(cache: KVCache, layer: int, q: torch.Tensor, out: torch.Tensor, workspace: AttendWorkspace,
+                     status: torch.Tensor, tree=None, node_begin: int = 0, scale: Optional[float] = None,
+                     stream=None):
+    """Nodes node_begin .. node_begin + q.shape[1] - 1 of every tree attend to the committed tokens, their
+    ancestors and themselves; scale defaults to head_dim ** -0.5."""
+    cq, co = _heads("q", q, cache), _heads("out", out, cache, q.shape[1], q.shape[2])
+    nodes = _nodes(tree, cache.B, node_begin, q.shape[1])
+    _check(_lib.spec_tree_attend(cache.B, ctypes.byref(cache.c()), layer, ctypes.byref(nodes), q.shape[2],
+                                 ctypes.byref(cq), ctypes.byref(co),
+                                 cache.k.shape[4] ** -0.5 if scale is None else scale, _ptr(workspace.data),
+                                 workspace.data.numel(), _ptr(status), _stream(stream)))
+
+
+def spec_tree_kv_commit(cache: KVCache, accept_len: torch.Tensor, out_node: torch.Tensor, new_len: torch.Tensor,
+                        status: torch.Tensor, stream=None):
+    """Move the accepted path (spec_tree_verify's accept_len and out_node) behind the committed tokens in
+    every layer; new_len [B] receives the new committed lengths (then cache.set_lengths(new_len))."""
+    _int_rows("accept_len", accept_len, (cache.B,))
+    _int_rows("new_len", new_len, (cache.B,))
+    _int_rows("out_node", out_node, (cache.B, out_node.shape[-1]))
+    _check(_lib.spec_tree_kv_commit(cache.B, ctypes.byref(cache.c()), _ptr(accept_len), _ptr(out_node),
+                                    out_node.shape[1], _ptr(new_len), _ptr(status), _stream(stream)))

@@ -9,8 +9,10 @@
 #include "st_kernels.h"
 
 namespace {
-
 constexpr int MAX_DEVICES = 64;
+}
+
+namespace st {
 
 int num_sms_of_current_device() {
   static int cache[MAX_DEVICES] = {0};
@@ -25,6 +27,12 @@ int num_sms_of_current_device() {
   }
   return cache[dev];
 }
+
+}  // namespace st
+
+namespace {
+
+using st::num_sms_of_current_device;
 
 // |S| = min(support, V); support 0 selects the pages' default of 128 tokens
 constexpr int DEFAULT_SUPPORT = 128;

@@ -67,6 +67,44 @@ struct VerifyLaunch {
   int64_t draft_row_stride;  // elements
 };
 
+struct AppendLaunch {
+  int B, layer, n_q_heads;
+  spec_tree_kv_t kv;
+  spec_tree_nodes_t nodes;
+  spec_tree_heads_t q, k, v, q_out;
+  const float* rope;
+  int rope_rows, rot_dim;
+  bool interleaved;
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  uint32_t* status;
+};
+
+struct AttendLaunch {
+  int B, layer, n_q_heads;
+  spec_tree_kv_t kv;
+  spec_tree_nodes_t nodes;
+  spec_tree_heads_t q, out;
+  float scale;
+  void* workspace;
+  uint32_t* status;
+  int num_sms;
+};
+
+struct CommitLaunch {
+  int B;
+  spec_tree_kv_t kv;
+  const int32_t* accept_len;
+  const int32_t* out_node;
+  int path_stride;
+  int32_t* new_len;
+  uint32_t* status;
+};
+
+// SMs of the current device, 0 if it cannot be asked
+int num_sms_of_current_device();
+
 size_t select_expand_smem_bytes();
 cudaError_t launch_select_expand(int dtype, const SelLaunch& L, cudaStream_t stream);
 // supports of 129 to 1024 tokens
@@ -84,5 +122,9 @@ cudaError_t launch_layer_topr(const RankLaunch& L, cudaStream_t stream);
 cudaError_t launch_layer_finish(const RankLaunch& L, cudaStream_t stream);
 cudaError_t launch_verify(const VerifyLaunch& L, cudaStream_t stream);
 cudaError_t launch_verify_dense(const VerifyLaunch& L, cudaStream_t stream);
+cudaError_t launch_kv_append(const AppendLaunch& L, cudaStream_t stream);
+cudaError_t launch_kv_commit(const CommitLaunch& L, cudaStream_t stream);
+size_t attend_workspace_bytes(int num_sms, int64_t rows, int head_dim);
+cudaError_t launch_attend(const AttendLaunch& L, cudaStream_t stream);
 
 }  // namespace st

@@ -54,6 +54,7 @@ typedef struct CUstream_st* spec_tree_stream_t;
 /* element types of logit rows */
 #define SPEC_TREE_BF16 0
 #define SPEC_TREE_F32 1
+#define SPEC_TREE_F16 2 /* key-value cache, queries and attention outputs only */
 
 /* tree builders */
 #define SPEC_TREE_BUILDER_TOPR 0  /* expand-then-rerank, frontier top-W, global top-R */
@@ -83,6 +84,8 @@ typedef struct CUstream_st* spec_tree_stream_t;
 #define SPEC_TREE_S_TIMEOUT 16u          /* a bounded wait on a bulk copy gave up */
 #define SPEC_TREE_S_ROWS 32u             /* a tree wanted more draft rows than n_rows */
 #define SPEC_TREE_S_LAYERS 64u           /* layer mode: a call out of order, or finish before the last layer */
+#define SPEC_TREE_S_PAGES 128u           /* a cached token whose page is not in the page table, or not in the pool */
+#define SPEC_TREE_S_NODES 256u           /* a parent, depth, path or length that no tree of this call can have */
 
 /* Limits of this build. */
 #define SPEC_TREE_MAX_SUPPORT 1024
@@ -426,6 +429,149 @@ int spec_tree_smart_fit(int npts, const double* n, const double* t_draft, const 
  * Returns SPEC_TREE_E_PARAM for a null pointer or polls out of range.
  */
 int spec_tree_wait_selftest(uint32_t polls, uint32_t* status, uint32_t* result, spec_tree_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The model's side of a step: a paged key-value cache, the attention of a
+ * tree's nodes over it, and the commit of the accepted path.  The pages have
+ * no counterpart (they take the logits as given); these are the operations
+ * that a target or draft model runs between spec_tree_build and
+ * spec_tree_verify, on the same node arrays:
+ *
+ *   spec_tree_kv_append   nodes' keys and values, rotated, into the cache
+ *   spec_tree_attend      nodes' queries over committed tokens and ancestors
+ *   (the rest of the layer; spec_tree_verify on the logits)
+ *   spec_tree_kv_commit   the accepted path's entries, moved into place
+ *
+ * A sequence of seq_len committed tokens keeps token t in slot t.  The nodes
+ * of its tree follow: node n (canonical index; the root, node 0, is the newest
+ * token, whose entries are not cached yet) lies in slot seq_len + n, at
+ * position seq_len + depth(n).  Slot s is entry s % page_size of page
+ * page_table[b][s / page_size].
+ * ------------------------------------------------------------------------ */
+
+/*
+ * A paged key-value cache of n_layers layers (device pointers, caller-owned).
+ * Element d of the key of slot entry o, page g, head h, layer l is
+ *   k[l * layer_stride + g * page_stride + o * token_stride + h * head_stride + d]
+ * (strides in elements, the same for v; head_dim elements are contiguous), so
+ * both [page][token][head] and [page][head][token] orders are served.
+ *   dtype       SPEC_TREE_BF16 or SPEC_TREE_F16;
+ *   head_dim    64 or 128;  n_kv_heads >= 1;
+ *   page_size   a power of two, 8 to 65536;
+ *   page_table  device [B][table_stride] int32, max_pages <= table_stride
+ *               entries used, each 0 .. n_pages - 1 where the sequence has
+ *               tokens (others are not read);
+ *   seq_len     device [B] int32 >= 0: committed tokens.
+ * k and v are 16-byte aligned and strides multiples of 8 elements, else
+ * SPEC_TREE_E_LAYOUT.
+ */
+typedef struct spec_tree_kv_t {
+  void* k;
+  void* v;
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  int64_t layer_stride, page_stride, token_stride, head_stride;
+  int32_t dtype, n_layers, n_pages, page_size, n_kv_heads, head_dim, max_pages, table_stride;
+} spec_tree_kv_t;
+
+/* Vectors of head_dim elements per (tree, node of the call, head): element d
+ * at data[b * tree_stride + i * node_stride + h * head_stride + d].  16-byte
+ * aligned, strides multiples of 8 elements. */
+typedef struct spec_tree_heads_t {
+  void* data;
+  int64_t tree_stride, node_stride, head_stride;
+} spec_tree_heads_t;
+
+/*
+ * The nodes a call works on: begin .. begin + count - 1 of every tree.
+ *   parent, depth: device [B][stride] int32, spec_tree_t's node_parent and
+ *     node_depth (any arrays with parent[n] < n and parent[0] = -1 will do,
+ *     such as a drafter's frontiers in the order they were expanded), or both
+ *     NULL: a chain, every node the child of the one before it (one node:
+ *     plain decoding; many: a chunk of a prompt).
+ *   n_nodes: device [B] int32, or NULL (all): nodes at index >= n_nodes[b] do
+ *     not exist.
+ * With parents, begin + count <= stride and <= SPEC_TREE_MAX_NODES; a chain
+ * has at most 2^20 nodes.
+ */
+typedef struct spec_tree_nodes_t {
+  const int32_t* parent;
+  const int32_t* depth;
+  const int32_t* n_nodes;
+  int32_t stride, begin, count;
+} spec_tree_nodes_t;
+
+/*
+ * Appends the nodes' keys and values to layer `layer` of the cache:
+ *   x' = x * rsqrt(mean(x^2) + eps) * weight   (queries with q_weight, keys
+ *        with k_weight; a NULL weight leaves them as they are),
+ *   rotated to position t = seq_len[b] + depth(n): each pair (x, y) becomes
+ *        (x c - y s, x s + y c), c = rope[t][j], s = rope[t][rot_dim / 2 + j];
+ *        pair j is elements (j, j + rot_dim / 2), or (2j, 2j + 1) when
+ *        `interleaved`; elements from rot_dim on keep their values,
+ * in float32, rounded once.  Keys and values (values unchanged) go to slot
+ * seq_len[b] + n, queries to q_out (which may be q itself).  A node that does
+ * not exist leaves the cache alone and gets zeros in q_out.
+ *   q, q_out: n_q_heads vectors per node; k, v: kv->n_kv_heads; all kv->dtype.
+ *   rope:     device float [rope_rows][rot_dim], 16-byte aligned; rot_dim a
+ *             multiple of 16 up to head_dim; NULL with rot_dim = 0: no rotation.
+ *   weights:  device, head_dim elements of kv->dtype, 16-byte aligned.
+ * A slot without a page sets SPEC_TREE_S_PAGES and is not written; a position
+ * outside the table sets SPEC_TREE_S_NODES, the node is then not rotated.
+ */
+int spec_tree_kv_append(int B, const spec_tree_kv_t* kv, int layer, const spec_tree_nodes_t* nodes, int n_q_heads,
+                        const spec_tree_heads_t* q, const spec_tree_heads_t* k, const spec_tree_heads_t* v,
+                        const spec_tree_heads_t* q_out, const float* rope, int rope_rows, int rot_dim,
+                        int interleaved, const void* q_weight, const void* k_weight, float eps, uint32_t* status,
+                        spec_tree_stream_t stream);
+
+/*
+ * Attention of the nodes over layer `layer` of the cache:
+ *   out_i = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale (q_i . k_t) - max_t),
+ * over the tokens t that node n = begin + i sees: the seq_len[b] committed
+ * ones, its ancestors and itself (all slots' entries must have been appended).
+ * Query head h reads key head h / (n_q_heads / n_kv_heads).  Products are
+ * summed, and the statistics of the softmax held, in float32; the weights are
+ * rounded to kv->dtype for their product with the values.  What a node does
+ * not see has no influence on it, whatever it holds (NaN and infinities
+ * included).  A node that does not exist, or that sees no score above -inf,
+ * gets zeros.
+ *   q, out: n_q_heads vectors per node of kv->dtype, n_q_heads a multiple of
+ *           n_kv_heads; out must not overlap q.
+ *   scale:  finite, usually head_dim^-0.5.
+ *   workspace: device, spec_tree_attend_workspace_bytes() bytes, 16-byte
+ *           aligned, zero before the first call that uses it; every call
+ *           leaves what the next one needs.  Calls that overlap on the GPU
+ *           must not share one.
+ * A slot without a page sets SPEC_TREE_S_PAGES and reads as zeros; a parent
+ * that does not precede its node sets SPEC_TREE_S_NODES and ends the walk.
+ * Results do not depend on timing: the same call on the same device gives the
+ * same bits.
+ */
+int spec_tree_attend(int B, const spec_tree_kv_t* kv, int layer, const spec_tree_nodes_t* nodes, int n_q_heads,
+                     const spec_tree_heads_t* q, const spec_tree_heads_t* out, float scale, void* workspace,
+                     size_t workspace_bytes, uint32_t* status, spec_tree_stream_t stream);
+
+/* Workspace of spec_tree_attend on the current device for calls of up to B
+ * trees and `count` nodes (0: bad arguments or no device). */
+size_t spec_tree_attend_workspace_bytes(int B, int count, int n_q_heads, int n_kv_heads, int head_dim);
+
+/*
+ * Commits the accepted path of spec_tree_verify in every layer: for
+ * j = 1 .. accept_len[b], slot seq_len[b] + j takes the entries of slot
+ * seq_len[b] + out_node[b][j - 1] (as they are: the node's depth is j, so its
+ * position stays the same), and new_len[b] = seq_len[b] + 1 + accept_len[b]
+ * (the root and the path are then committed; the bonus token is the next
+ * tree's root).
+ *   accept_len: device [B]; out_node: device [B][path_stride] as written by
+ *   spec_tree_verify (path_stride = depth + 1, 1 to 256); new_len: device [B],
+ *   not kv->seq_len (the caller swaps the two).
+ * A path whose j-th node is below j, or longer than path_stride, sets
+ * SPEC_TREE_S_NODES: that tree's cache is left alone and new_len[b] =
+ * seq_len[b].  A slot without a page sets SPEC_TREE_S_PAGES and is skipped.
+ */
+int spec_tree_kv_commit(int B, const spec_tree_kv_t* kv, const int32_t* accept_len, const int32_t* out_node,
+                        int path_stride, int32_t* new_len, uint32_t* status, spec_tree_stream_t stream);
 
 /* Message for a return code (static string). */
 const char* spec_tree_strerror(int code);
