@@ -30,7 +30,7 @@ int check_kv(int B, const spec_tree_kv_t* kv, int layer) {
   if (!aligned16(kv->k) || !aligned16(kv->v)) return SPEC_TREE_E_LAYOUT;
   const int64_t st[4] = {kv->layer_stride, kv->page_stride, kv->token_stride, kv->head_stride};
   for (int64_t x : st)
-    if (x < 0 || x % 8 != 0) return SPEC_TREE_E_LAYOUT;
+    if (x < 0 || x % 8 != 0 || x >= (1ll << 38)) return SPEC_TREE_E_LAYOUT;
   return SPEC_TREE_OK;
 }
 
@@ -112,7 +112,7 @@ int spec_tree_attend(int B, const spec_tree_kv_t* kv, int layer, const spec_tree
   if (rc) return rc;
   if ((rc = check_nodes(nodes, false))) return rc;
   if (n_q_heads < kv->n_kv_heads || n_q_heads > MAX_HEADS || n_q_heads % kv->n_kv_heads != 0 ||
-      static_cast<int64_t>(B) * nodes->count * n_q_heads > INT32_MAX)
+      static_cast<int64_t>(B) * nodes->count * n_q_heads > (1 << 30))
     return SPEC_TREE_E_PARAM;
   if ((rc = check_heads(q)) || (rc = check_heads(out))) return rc;
   if (!isfinite(scale) || workspace == nullptr || q->data == out->data) return SPEC_TREE_E_PARAM;

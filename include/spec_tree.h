@@ -543,8 +543,10 @@ int spec_tree_kv_append(int B, const spec_tree_kv_t* kv, int layer, const spec_t
  *           aligned, zero before the first call that uses it; every call
  *           leaves what the next one needs.  Calls that overlap on the GPU
  *           must not share one.
- * A slot without a page sets SPEC_TREE_S_PAGES and reads as zeros; a parent
- * that does not precede its node sets SPEC_TREE_S_NODES and ends the walk.
+ * A slot whose page is not in the pool sets SPEC_TREE_S_PAGES and reads as
+ * zeros; a tree with slots past the page table sets it too, one of negative
+ * length sets SPEC_TREE_S_NODES, and both get zeros; a parent that does not
+ * precede its node sets SPEC_TREE_S_NODES and ends the walk.
  * Results do not depend on timing: the same call on the same device gives the
  * same bits.
  */
