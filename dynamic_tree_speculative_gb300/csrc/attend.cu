@@ -44,6 +44,7 @@ constexpr int PANEL_BYTES = TILE * 128;         // 128 rows of 64 elements
 constexpr int MASKED_TILES = SPEC_TREE_MAX_NODES / TILE + 2;
 constexpr float LAZY = 8.0f;                    // log2 of what a weight may exceed its reference by
 constexpr int MAX_STAGES = 10;
+constexpr int SPINS = 64;                       // polls of a wait before it suspends the thread
 
 struct Plan {
   AttendLaunch L;
@@ -84,7 +85,7 @@ struct Layout {
 
 struct Control {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES];
-  uint64_t q_full, s_full[2], w_full[2], o_full[2], drain;
+  uint64_t q_full, s_full[2], w_full[2][2], o_full[2], drain;
   uint32_t tmem;
   int abort;
   int64_t scan[16];
@@ -198,8 +199,16 @@ struct Walk {
 // A wait that gives up when it, or another role of the CTA, has run out.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Control& C, uint32_t* status) {
   const uint32_t addr = smem_u32(bar);
+  uint32_t done;
+  for (int spin = 0; spin < SPINS; ++spin) {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
   for (uint32_t it = 0; it < WAIT_LIMIT; ++it) {
-    uint32_t done;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
@@ -211,6 +220,17 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Control& C,
   *reinterpret_cast<volatile int*>(&C.abort) = 1;
   set_status(status, SPEC_TREE_S_TIMEOUT);
   return false;
+}
+
+// The same for a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Control& C, uint32_t* status) {
+  return __all_sync(FULL, wait(bar, parity, C, status));
+}
+
+// One arrival for a whole warp, after what all its lanes did before.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
 
 // bit j: the row's node sees slot `base` + j of the 128 slots of a tile
@@ -282,7 +302,7 @@ __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* mk, 
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv, ++n) {
         const int st = n % Y::STAGES;
-        if (!__all_sync(FULL, wait(&C.empty[st], ((n / Y::STAGES) & 1) ^ 1, C, P.L.status))) {
+        if (!warp_wait(&C.empty[st], ((n / Y::STAGES) & 1) ^ 1, C, P.L.status)) {
           // copies in flight land before the CTA ends
           for (uint32_t o = n > Y::STAGES ? n - Y::STAGES : 0; o < n; ++o)
             mbar_wait(&C.full[o % Y::STAGES], (o / Y::STAGES) & 1);
@@ -301,14 +321,16 @@ __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* mk, 
   }
 }
 
-// One thread: the products.  The halves take turns, so that while one half's
+// One warp: the products.  The halves take turns, so that while one half's
 // weights are made the other half's products run.  False: a wait gave up.
 template <typename T, int D, int NH>
 __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t q_smem, uint32_t ring, int64_t my_tiles) {
   using Y = Layout<D, NH>;
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t ID_S = mma_descriptor(BF, TILE, false), ID_O = mma_descriptor(BF, D, true);
-  const uint32_t tmem = C.tmem;
+  constexpr int KV16 = Y::KV_BYTES / 16, PANEL16 = PANEL_BYTES / 16;  // descriptors count 16 bytes
+  const uint32_t tmem = uniform(C.tmem), q_low = smem_descriptor_low(q_smem, 0);
+  const uint32_t k_low = smem_descriptor_low(ring, 0), v_low = smem_descriptor_low(ring, PANEL_BYTES);
   Walk<NH> walk;
   walk.begin(P, C, my_tiles);
   Segment s;
@@ -316,44 +338,56 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
   uint32_t* status = P.L.status;
 
   auto scores = [&](int h, uint32_t stage) {
+    const uint32_t a = uniform(q_low) + h * KV16, b = uniform(k_low + stage * KV16);
+    if (elect()) {
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t at = (k / 4) * PANEL_BYTES + (k % 4) * 32;
-      mma_ss(tmem + h * TILE, smem_descriptor(q_smem + h * Y::KV_BYTES + at, 0),
-             smem_descriptor(ring + stage * Y::KV_BYTES + at, 0), ID_S, k > 0);
+      for (int k = 0; k < D / 16; ++k) {
+        const int at = (k / 4) * PANEL16 + (k % 4) * 2;
+        mma_ss(tmem + h * TILE, smem_descriptor(a + at), smem_descriptor(b + at), ID_S, k > 0);
+      }
+      mma_commit(&C.s_full[h]);
     }
-    mma_commit(&C.s_full[h]);
+    __syncwarp();
   };
 
   while (walk.next(P, s)) {
-    if (!wait(&C.q_full, segment & 1, C, status)) return false;
-    uint32_t ks = n % Y::STAGES;
-    if (!wait(&C.full[ks], (n / Y::STAGES) & 1, C, status)) return false;
+    const uint32_t ks = n % Y::STAGES;
+    if (!warp_wait(&C.q_full, segment & 1, C, status)) return false;
+    if (!warp_wait(&C.full[ks], (n / Y::STAGES) & 1, C, status)) return false;
     tmem_fence_after();
     for (int h = 0; h < NH; ++h) scores(h, ks);
-    mma_commit(&C.empty[ks]);
+    if (elect()) mma_commit(&C.empty[ks]);
     for (int t = s.first; t < s.last; ++t, n += 2, ++tile) {
       const uint32_t vs = (n + 1) % Y::STAGES, next = (n + 2) % Y::STAGES;
+      const uint32_t b = uniform(v_low + vs * KV16), add = uniform(t > s.first);
       const bool more = t + 1 < s.last;
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        if (!wait(&C.w_full[h], tile & 1, C, status)) return false;
-        if (h == 0 && !wait(&C.full[vs], ((n + 1) / Y::STAGES) & 1, C, status)) return false;
-        tmem_fence_after();
+        if (h == 0 && !warp_wait(&C.full[vs], ((n + 1) / Y::STAGES) & 1, C, status)) return false;
 #pragma unroll
-        for (int k = 0; k < TILE / 16; ++k)
-          mma_ts(tmem + NH * TILE + h * D, tmem + h * TILE + k * 8,
-                 smem_descriptor(ring + vs * Y::KV_BYTES + k * 16 * 128, PANEL_BYTES), ID_O, t > s.first || k > 0);
+        for (int part = 0; part < 2; ++part) {
+          if (!warp_wait(&C.w_full[h][part], tile & 1, C, status)) return false;
+          tmem_fence_after();
+          if (elect()) {
+#pragma unroll
+            for (int k = part * TILE / 32; k < (part + 1) * TILE / 32; ++k)
+              mma_ts(tmem + NH * TILE + h * D, tmem + h * TILE + k * 8, smem_descriptor(b + k * (16 * 128 / 16)), ID_O,
+                     k > 0 || add);
+            if (part == 1 && !more) mma_commit(&C.o_full[h]);
+          }
+          __syncwarp();
+        }
         if (more) {
-          if (h == 0 && !wait(&C.full[next], ((n + 2) / Y::STAGES) & 1, C, status)) return false;
+          if (h == 0 && !warp_wait(&C.full[next], ((n + 2) / Y::STAGES) & 1, C, status)) return false;
           tmem_fence_after();
           scores(h, next);
-        } else {
-          mma_commit(&C.o_full[h]);
         }
       }
-      mma_commit(&C.empty[vs]);
-      if (more) mma_commit(&C.empty[next]);
+      if (elect()) {
+        mma_commit(&C.empty[vs]);
+        if (more) mma_commit(&C.empty[next]);
+      }
+      __syncwarp();
     }
     ++segment;
   }
@@ -401,7 +435,7 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
       *reinterpret_cast<uint4*>(smem + half * Y::KV_BYTES + (ch / 8) * PANEL_BYTES + r * 128 + (((ch % 8) ^ (r % 8)) * 16)) = x;
     }
     fence_proxy_async_smem();
-    mbar_arrive(&C.q_full);
+    warp_arrive(&C.q_full);
     if (P.L.nodes.parent) named_barrier(1, NH * TILE);
 
     const int row = s.row0 + half * TILE + t;
@@ -417,7 +451,7 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
       if (masked && half == 0) {
         // values of this tile: zero those past the end, and what is not finite
         const uint32_t v = 2 * tile + 1;
-        ok = ok && __all_sync(FULL, wait(&C.full[v % Y::STAGES], (v / Y::STAGES) & 1, C, status));
+        ok = ok && warp_wait(&C.full[v % Y::STAGES], (v / Y::STAGES) & 1, C, status);
         uint8_t* rowp = ring + (v % Y::STAGES) * Y::KV_BYTES + t * 128;
         bool odd = false;
         const bool past = base + t >= s.end || !ok;
@@ -445,7 +479,7 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
         if (lane == 0) C.odd[(j - first_masked) * (TILE / 32) + warp] = word;
         fence_proxy_async_smem();
       }
-      ok = ok && __all_sync(FULL, wait(&C.s_full[half], tile & 1, C, status));
+      ok = ok && warp_wait(&C.s_full[half], tile & 1, C, status);
       if (warp_live && ok) {
         tmem_fence_after();
         uint32_t x[TILE];
@@ -458,10 +492,14 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
           for (int c = 0; c < TILE; ++c)
             if (!((v.w[c / 32] >> (c % 32)) & 1)) x[c] = 0xff800000u;
         }
-        float top = -INFINITY;
+        float top8[8];
 #pragma unroll
-        for (int c = 0; c < TILE; ++c) top = fmaxf(top, __uint_as_float(x[c]));
-        top *= P.scale2;
+        for (int c = 0; c < 8; ++c) top8[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+#pragma unroll
+        for (int c = 16; c < TILE; c += 2)
+          top8[c / 2 % 8] = max3(top8[c / 2 % 8], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+        const float top = P.scale2 * fmaxf(max3(max3(top8[0], top8[1], top8[2]), top8[3], top8[4]),
+                                           max3(top8[5], top8[6], top8[7]));
         const bool grow = live && top > ref + LAZY;
         if (j == s.first) {
           ref = top;
@@ -480,24 +518,36 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
           }
         }
         const float sub = ref == -INFINITY ? 0.0f : ref - SHIFT;
-        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const F2 scale2(P.scale2, P.scale2), shift2(-sub, -sub);
+        F2 part[4];
 #pragma unroll
-        for (int c = 0; c < TILE; c += 2) {
-          const float a = ex2(fmaf(__uint_as_float(x[c]), P.scale2, -sub));
-          const float b = ex2(fmaf(__uint_as_float(x[c + 1]), P.scale2, -sub));
-          part[(c / 2) % 4] += a + b;
-          x[c / 2] = Pair<T>::pack(a, b);
+        for (int c = 0; c < 4; ++c) part[c] = F2(0.0f, 0.0f);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {  // the product starts on the first half of the weights
+#pragma unroll
+          for (int c = p * TILE / 2; c < (p + 1) * TILE / 2; c += 2) {
+            float a, b;
+            fma2(F2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, shift2).get(a, b);
+            a = ex2(a);
+            b = ex2(b);
+            part[c / 2 % 4] = add2(part[c / 2 % 4], F2(a, b));
+            x[c / 2] = Pair<T>::pack(a, b);
+          }
+          tmem_st32(tm_s + p * 32, x + p * 32);
+          tmem_wait_st();
+          tmem_fence_before();
+          if (p == 0) warp_arrive(&C.w_full[half][0]);
         }
-        sum += (part[0] + part[1]) + (part[2] + part[3]);
-        tmem_st32(tm_s, x);
-        tmem_st32(tm_s + 32, x + 32);
-        tmem_wait_st();
-        tmem_fence_before();
+        float a, b;
+        add2(add2(part[0], part[1]), add2(part[2], part[3])).get(a, b);
+        sum += a + b;
+      } else {
+        warp_arrive(&C.w_full[half][0]);
       }
-      mbar_arrive(&C.w_full[half]);
+      warp_arrive(&C.w_full[half][1]);
     }
 
-    ok = ok && __all_sync(FULL, wait(&C.o_full[half], segment & 1, C, status));
+    ok = ok && warp_wait(&C.o_full[half], segment & 1, C, status);
     ++segment;
     if (!ok) continue;
     if (!warp_live && s.row0 + half * TILE + warp * 32 >= P.rows) continue;
@@ -580,17 +630,18 @@ __global__ void __launch_bounds__(Layout<D, NH>::THREADS, 1)
   uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* ring = smem + Y::Q_BYTES;
   Control& C = *reinterpret_cast<Control*>(ring + Y::STAGES * Y::KV_BYTES);
-  const int warp = threadIdx.x / 32;
+  const int warp = __shfl_sync(FULL, threadIdx.x / 32, 0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < Y::STAGES; ++i) {
       mbar_init(&C.full[i], 1);
       mbar_init(&C.empty[i], 1);
     }
-    mbar_init(&C.q_full, NH * TILE);
+    mbar_init(&C.q_full, NH * 4);
     mbar_init(&C.drain, 1);
     for (int h = 0; h < NH; ++h) {
       mbar_init(&C.s_full[h], 1);
-      mbar_init(&C.w_full[h], TILE);
+      mbar_init(&C.w_full[h][0], 4);
+      mbar_init(&C.w_full[h][1], 4);
       mbar_init(&C.o_full[h], 1);
     }
     C.abort = 0;
@@ -659,9 +710,9 @@ __global__ void __launch_bounds__(Layout<D, NH>::THREADS, 1)
     softmax_role<T, D, NH>(P, C, smem, ring, to - from, cta, ctas, warp / 4);
   } else if (warp == NH * 4) {
     load_role<D, NH>(P, &mk, &mv, C, smem_u32(ring), to - from);
-  } else if (warp == NH * 4 + 1 && threadIdx.x % 32 == 0) {
+  } else if (warp == NH * 4 + 1) {
     if (!product_role<T, D, NH>(P, C, smem_u32(smem), smem_u32(ring), to - from)) {
-      mma_commit(&C.drain);  // products in flight end before their memory is given back
+      if (elect()) mma_commit(&C.drain);  // products in flight end before their memory is given back
       mbar_wait(&C.drain, 0);
     }
   }

@@ -65,10 +65,28 @@ __host__ __device__ constexpr uint32_t mma_descriptor(bool bf16, int n, bool b_n
 // Shared-memory operand of 128-byte swizzled rows: 8 rows of 128 bytes are a
 // 1024-byte group (aligned to it), groups follow each other.  `panel`: bytes
 // between blocks of 64 elements of N in an N-major operand.
-__device__ __forceinline__ uint64_t smem_descriptor(uint32_t addr, uint32_t panel) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>((panel >> 4) & 0x3fff) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+__device__ __forceinline__ uint32_t smem_descriptor_low(uint32_t addr, uint32_t panel) {
+  return ((addr >> 4) & 0x3fff) | (((panel >> 4) & 0x3fff) << 16);
 }
+
+// `low` may have been moved on by multiples of 16 bytes: the address does not
+// leave its field.
+__device__ __forceinline__ uint64_t smem_descriptor(uint32_t low) {
+  return low | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// One lane of a converged warp.  Products are issued under it, with operands
+// that the compiler can see to be uniform (uniform()): issued by `lane == 0`,
+// each costs several vector instructions for which the warp queues behind the
+// softmax warps of its scheduler (measured beside two warps of FMAs per
+// scheduler: 98 against 67 cycles per product of 64 cycles).
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(FULL, x, 0); }
 
 // D[tmem] (+)= A[smem] B[smem], K = 16; issued by one thread.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -112,6 +130,32 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// Pairs of float32 that one instruction works on.
+struct F2 {
+  uint64_t v;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ void get(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+};
+
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 y;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return y;
+}
+
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 y;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y.v) : "l"(a.v), "l"(b.v));
+  return y;
 }
 
 __device__ __forceinline__ float ex2(float x) {
