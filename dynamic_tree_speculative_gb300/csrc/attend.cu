@@ -49,8 +49,9 @@ constexpr int SPINS = 64;                       // polls of a wait before it sus
 struct Plan {
   AttendLaunch L;
   int group, rows, row_tiles, page_shift, box, ws_rows;
-  float scale2;   // |scale| log2(e)
-  uint32_t flip;  // sign bits to flip in queries (negative scale)
+  uint32_t group_inv;  // ceil(2^32 / group), 0 for a group of one
+  float scale2;        // |scale| log2(e)
+  bool negative;       // scale < 0: the products take -Q
 };
 
 // What a range has left in the workspace for the item it ends in, when others
@@ -62,14 +63,14 @@ struct JoinRecord {
 struct Workspace {
   JoinRecord* records;  // [CTA]
   float2* sums;         // [CTA][2][ws_rows]: (reference, sum)
-  float* out;           // [CTA][2][ws_rows][D]
+  float4* out;          // [CTA][2][D / 4][ws_rows]: neighbouring rows are neighbours in memory
 };
 
 __host__ __device__ inline Workspace workspace_of(void* ws, int num_sms, int ws_rows) {
   Workspace w;
   w.records = static_cast<JoinRecord*>(ws);
   w.sums = reinterpret_cast<float2*>(w.records + num_sms);
-  w.out = reinterpret_cast<float*>(w.sums + static_cast<size_t>(num_sms) * 2 * ((ws_rows + 1) / 2 * 2));
+  w.out = reinterpret_cast<float4*>(w.sums + static_cast<size_t>(num_sms) * 2 * ws_rows);
   return w;
 }
 
@@ -84,17 +85,15 @@ struct Layout {
 };
 
 struct Control {
-  uint64_t full[MAX_STAGES], empty[MAX_STAGES];
-  uint64_t q_full, s_full[2], w_full[2][2], o_full[2], drain;
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES], clean[MAX_STAGES];
+  uint64_t q_full, q_empty, s_full[2], w_full[2][2], o_full[2], drain;
   uint32_t tmem;
   int abort;
   int64_t scan[16];
-  int64_t start;                          // first tile of this CTA's range
   int64_t total;
-  int first_b;
-  int64_t first_tile;                     // of the range, counted from tree first_b
-  uint32_t odd[MASKED_TILES * (TILE / 32)];  // tokens with a value that is not finite
-  uint16_t parent[SPEC_TREE_MAX_NODES];
+  int b, rt, head, at;                       // where this CTA's range begins
+  uint32_t odd[3][MASKED_TILES * (TILE / 32)];  // tokens with a value that is not finite, by segment modulo 3
+  uint16_t parent[2][SPEC_TREE_MAX_NODES];      // by segment modulo 2
 };
 
 // A consecutive piece of an item's tiles: what one CTA does at a time.
@@ -152,23 +151,13 @@ struct Walk {
   int len, cnt;
 
   __device__ __forceinline__ void begin(const Plan& P, const Control& C, int64_t tiles) {
-    b = C.first_b;
     left = tiles;
-    rt = head = at = 0;
     if (left <= 0) return;
+    b = C.b;
+    rt = C.rt;
+    head = C.head;
+    at = C.at;
     tree_of(P, b, len, cnt);
-    int64_t skip = C.first_tile;
-    for (;; ++rt) {
-      int end, n;
-      item_tiles<NH>(P, len, cnt, rt, end, n);
-      const int64_t all = static_cast<int64_t>(n) * P.L.kv.n_kv_heads;
-      if (skip < all) {
-        head = static_cast<int>(skip / n);
-        at = static_cast<int>(skip % n);
-        break;
-      }
-      skip -= all;
-    }
   }
 
   __device__ __forceinline__ bool next(const Plan& P, Segment& s) {
@@ -193,6 +182,20 @@ struct Walk {
       }
     }
     return true;
+  }
+};
+
+// Row `row0` + r of an item: node i0 + (rem + r) / group of the call, head
+// (rem + r) % group.  rem + r < 2^15, so the product with the rounded-up
+// inverse is exact.
+struct Rows {
+  int i0, rem;
+  __device__ __forceinline__ Rows(const Plan& P, int row0) : i0(row0 / P.group), rem(row0 - row0 / P.group * P.group) {}
+  __device__ __forceinline__ void get(const Plan& P, int r, int& i, int& g) const {
+    const int x = rem + r;
+    const int n = P.group_inv ? static_cast<int>(__umulhi(x, P.group_inv)) : x;
+    i = i0 + n;
+    g = x - n * P.group;
   }
 };
 
@@ -242,7 +245,8 @@ __device__ __forceinline__ uint32_t below(int n) {  // the n lowest bits, n clam
   return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
 }
 
-__device__ __forceinline__ Seen seen_of(const Plan& P, const Control& C, const Segment& s, int node, int base) {
+template <typename Parent>  // Parent(n): -1 for none
+__device__ __forceinline__ Seen seen_of(const Plan& P, const Segment& s, int node, int base, Parent parent) {
   Seen v;
   const int off = base - s.len;  // node index of the tile's first slot
   const int prefix = P.L.nodes.parent ? -off : node + 1 - off;
@@ -255,8 +259,7 @@ __device__ __forceinline__ Seen seen_of(const Plan& P, const Control& C, const S
 #pragma unroll
       for (int i = 0; i < TILE / 32; ++i)
         if ((j >> 5) == i) v.w[i] |= 1u << (j & 31);
-      const int up = C.parent[at];
-      at = up == 0xffff ? -1 : up;
+      at = parent(at);
     }
   }
   return v;
@@ -337,13 +340,16 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
   uint32_t n = 0, segment = 0, tile = 0;  // loads, segments, tiles so far
   uint32_t* status = P.L.status;
 
+  const uint32_t id_s = uniform(P.negative ? ID_S | MMA_NEGATE_A : ID_S);
+  uint32_t clean = 0;  // bit i: parity of slot i's next cleaning
+
   auto scores = [&](int h, uint32_t stage) {
     const uint32_t a = uniform(q_low) + h * KV16, b = uniform(k_low + stage * KV16);
     if (elect()) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const int at = (k / 4) * PANEL16 + (k % 4) * 2;
-        mma_ss(tmem + h * TILE, smem_descriptor(a + at), smem_descriptor(b + at), ID_S, k > 0);
+        mma_ss(tmem + h * TILE, smem_descriptor(a + at), smem_descriptor(b + at), id_s, k > 0);
       }
       mma_commit(&C.s_full[h]);
     }
@@ -356,14 +362,24 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
     if (!warp_wait(&C.full[ks], (n / Y::STAGES) & 1, C, status)) return false;
     tmem_fence_after();
     for (int h = 0; h < NH; ++h) scores(h, ks);
-    if (elect()) mma_commit(&C.empty[ks]);
+    if (elect()) {
+      mma_commit(&C.empty[ks]);
+      if (s.first + 1 == s.last) mma_commit(&C.q_empty);
+    }
+    __syncwarp();
     for (int t = s.first; t < s.last; ++t, n += 2, ++tile) {
       const uint32_t vs = (n + 1) % Y::STAGES, next = (n + 2) % Y::STAGES;
       const uint32_t b = uniform(v_low + vs * KV16), add = uniform(t > s.first);
       const bool more = t + 1 < s.last;
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        if (h == 0 && !warp_wait(&C.full[vs], ((n + 1) / Y::STAGES) & 1, C, status)) return false;
+        if (h == 0) {
+          if (!warp_wait(&C.full[vs], ((n + 1) / Y::STAGES) & 1, C, status)) return false;
+          if ((t + 1) * TILE > s.clear) {
+            if (!warp_wait(&C.clean[vs], (clean >> vs) & 1, C, status)) return false;
+            clean ^= 1u << vs;
+          }
+        }
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           if (!warp_wait(&C.w_full[h][part], tile & 1, C, status)) return false;
@@ -386,6 +402,7 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
       if (elect()) {
         mma_commit(&C.empty[vs]);
         if (more) mma_commit(&C.empty[next]);
+        if (t + 2 == s.last) mma_commit(&C.q_empty);
       }
       __syncwarp();
     }
@@ -394,52 +411,101 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
   return true;
 }
 
-// 128 threads, one row each: queries into shared memory, weights, the running
-// reference and sum, and the output.
+// Two warps, ahead of the softmax: an item's queries and its nodes' parents
+// into shared memory, and the values of tiles that not every row sees whole:
+// those past the item's end and those that are not finite become zeros.
 template <typename T, int D, int NH>
-__device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t* smem, uint8_t* ring, int64_t my_tiles,
-                                             int cta, int ctas, int half) {
+__device__ __forceinline__ void side_role(const Plan& P, Control& C, uint32_t q_smem, uint8_t* ring, int64_t my_tiles) {
   using Y = Layout<D, NH>;
+  constexpr int CHUNKS = D / 8, THREADS = 64;
+  const int t = threadIdx.x % THREADS;
+  uint32_t* status = P.L.status;
+  Walk<NH> walk;
+  walk.begin(P, C, my_tiles);
+  Segment s;
+  uint32_t segment = 0, tile = 0;
+  for (; walk.next(P, s); ++segment, tile += s.last - s.first) {
+    const Rows rows(P, s.row0);
+    if (!warp_wait(&C.q_empty, (segment & 1) ^ 1, C, status)) return;
+    const int n = min(NH * TILE, P.rows - s.row0), ch = t % CHUNKS;
+    const T* from = static_cast<const T*>(P.L.q.data) + s.b * P.L.q.tree_stride +
+                    static_cast<int64_t>(s.head) * P.group * P.L.q.head_stride + ch * 8;
+    for (int r = t / CHUNKS; r < n; r += THREADS / CHUNKS) {
+      int i, g;
+      rows.get(P, r, i, g);
+      const bool live = P.L.nodes.begin + i < s.cnt;
+      async_copy16(q_smem + (r / TILE) * Y::KV_BYTES + (ch / 8) * PANEL_BYTES + (r % TILE) * 128 + (((ch % 8) ^ (r % 8)) * 16),
+                   live ? from + i * P.L.q.node_stride + g * P.L.q.head_stride : from, !live);
+    }
+    if (P.L.nodes.parent) {
+      for (int i = t; i < s.cnt; i += THREADS) {
+        const int up = P.L.nodes.parent[static_cast<int64_t>(s.b) * P.L.nodes.stride + i];
+        C.parent[segment % 2][i] = static_cast<uint16_t>(up < 0 || up >= i ? 0xffff : up);
+        if (up >= i) set_status(status, SPEC_TREE_S_NODES);
+      }
+    }
+    async_copies_wait();
+    fence_proxy_async_smem();
+    warp_arrive(&C.q_full);
+
+    const int first_masked = s.clear / TILE;
+    for (int j = max(s.first, first_masked); j < s.last; ++j) {
+      const uint32_t v = 2 * (tile + j - s.first) + 1;
+      if (!warp_wait(&C.full[v % Y::STAGES], (v / Y::STAGES) & 1, C, status)) return;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const int row = part * 64 + t;  // a token
+        uint8_t* at = ring + (v % Y::STAGES) * Y::KV_BYTES + row * 128;
+        const bool past = j * TILE + row >= s.end;
+        bool odd = false;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+          uint4* w4 = reinterpret_cast<uint4*>(at + (c / 8) * PANEL_BYTES + (((c % 8) ^ (row % 8)) * 16));
+          if (past) {
+            *w4 = make_uint4(0, 0, 0, 0);
+          } else {
+            const uint4 x = *w4;
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            bool hit = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool lo = odd16<T>(w[e]), hi = odd16<T>(w[e] >> 16);
+              if (lo) w[e] &= 0xffff0000u;
+              if (hi) w[e] &= 0x0000ffffu;
+              hit |= lo || hi;
+            }
+            if (hit) *w4 = make_uint4(w[0], w[1], w[2], w[3]);
+            odd |= hit;
+          }
+        }
+        const uint32_t word = __ballot_sync(FULL, odd);
+        if (t % 32 == 0) C.odd[segment % 3][(j - first_masked) * (TILE / 32) + part * 2 + t / 32] = word;
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&C.clean[v % Y::STAGES]);
+    }
+  }
+}
+
+// 128 threads, one row each: weights, the running reference and sum, and the
+// output.
+template <typename T, int D, int NH>
+__device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int64_t my_tiles, int cta, int ctas, int half) {
   constexpr float SHIFT = std::is_same<T, __half>::value ? 7.0f : 0.0f;
-  constexpr int CHUNKS = D / 8;
-  const int t = threadIdx.x % TILE, warp = t / 32, lane = t % 32;
+  const int t = threadIdx.x % TILE, warp = t / 32;
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
   const uint32_t tm_s = C.tmem + half * TILE + lanes, tm_o = C.tmem + NH * TILE + half * D + lanes;
-  const Workspace ws = workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows);
   uint32_t* status = P.L.status;
   Walk<NH> walk;
   walk.begin(P, C, my_tiles);
   Segment s;
   uint32_t tile = 0, segment = 0;
-  bool ok = true;  // uniform over the warp; a role that has given up still meets the others at barriers
-  while (walk.next(P, s)) {
-    // the item's queries and, for a tree, its parents
-    named_barrier(1, NH * TILE);  // every thread has done with the item before
-    if (P.L.nodes.parent) {
-      for (int i = threadIdx.x; i < s.cnt; i += NH * TILE) {
-        const int up = P.L.nodes.parent[static_cast<int64_t>(s.b) * P.L.nodes.stride + i];
-        C.parent[i] = static_cast<uint16_t>(up < 0 || up >= i ? 0xffff : up);
-        if (up >= i) set_status(status, SPEC_TREE_S_NODES);
-      }
-    }
-    const int rows = min(TILE, P.rows - s.row0 - half * TILE);
-    for (int c = t; c < rows * CHUNKS; c += TILE) {
-      const int r = c / CHUNKS, ch = c % CHUNKS, row = s.row0 + half * TILE + r;
-      const int i = row / P.group, g = row - i * P.group;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (P.L.nodes.begin + i < s.cnt) {
-        x = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.L.q.data) + s.b * P.L.q.tree_stride +
-                                            i * P.L.q.node_stride + (s.head * P.group + g) * P.L.q.head_stride + ch * 8);
-        x.x ^= P.flip, x.y ^= P.flip, x.z ^= P.flip, x.w ^= P.flip;
-      }
-      *reinterpret_cast<uint4*>(smem + half * Y::KV_BYTES + (ch / 8) * PANEL_BYTES + r * 128 + (((ch % 8) ^ (r % 8)) * 16)) = x;
-    }
-    fence_proxy_async_smem();
-    warp_arrive(&C.q_full);
-    if (P.L.nodes.parent) named_barrier(1, NH * TILE);
-
-    const int row = s.row0 + half * TILE + t;
-    const int i = row / P.group, node = P.L.nodes.begin + i;
+  bool ok = true;  // uniform over the warp
+  for (; walk.next(P, s); ++segment) {
+    const int local = half * TILE + t, row = s.row0 + local;
+    int i, g;
+    Rows(P, s.row0).get(P, local, i, g);
+    const int node = P.L.nodes.begin + i;
     const bool live = row < P.rows && node < s.cnt;
     const bool warp_live = __any_sync(FULL, live);
     const int first_masked = s.clear / TILE;  // tiles from here on are not seen whole by every row
@@ -448,37 +514,6 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
     for (int j = s.first; j < s.last; ++j, ++tile) {
       const int base = j * TILE;
       const bool masked = base + TILE > s.clear;
-      if (masked && half == 0) {
-        // values of this tile: zero those past the end, and what is not finite
-        const uint32_t v = 2 * tile + 1;
-        ok = ok && warp_wait(&C.full[v % Y::STAGES], (v / Y::STAGES) & 1, C, status);
-        uint8_t* rowp = ring + (v % Y::STAGES) * Y::KV_BYTES + t * 128;
-        bool odd = false;
-        const bool past = base + t >= s.end || !ok;
-#pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-          uint4* at = reinterpret_cast<uint4*>(rowp + (c / 8) * PANEL_BYTES + (((c % 8) ^ (t % 8)) * 16));
-          if (past) {
-            *at = make_uint4(0, 0, 0, 0);
-            continue;
-          }
-          uint4 x = *at;
-          uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-          bool hit = false;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool lo = odd16<T>(w[e]), hi = odd16<T>(w[e] >> 16);
-            if (lo) w[e] &= 0xffff0000u;
-            if (hi) w[e] &= 0x0000ffffu;
-            hit |= lo || hi;
-          }
-          if (hit) *at = x;
-          odd |= hit;
-        }
-        const uint32_t word = __ballot_sync(FULL, odd);
-        if (lane == 0) C.odd[(j - first_masked) * (TILE / 32) + warp] = word;
-        fence_proxy_async_smem();
-      }
       ok = ok && warp_wait(&C.s_full[half], tile & 1, C, status);
       if (warp_live && ok) {
         tmem_fence_after();
@@ -487,7 +522,8 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
         for (int c = 0; c < TILE / 32; ++c) tmem_ld32(tm_s + c * 32, x + c * 32);
         tmem_wait_ld();
         if (masked) {
-          const Seen v = seen_of(P, C, s, live ? node : -1, base);
+          const uint16_t* parent = C.parent[segment % 2];
+          const Seen v = seen_of(P, s, live ? node : -1, base, [&](int n) { return parent[n] == 0xffff ? -1 : parent[n]; });
 #pragma unroll
           for (int c = 0; c < TILE; ++c)
             if (!((v.w[c / 32] >> (c % 32)) & 1)) x[c] = 0xff800000u;
@@ -548,32 +584,31 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
     }
 
     ok = ok && warp_wait(&C.o_full[half], segment & 1, C, status);
-    ++segment;
-    if (!ok) continue;
-    if (!warp_live && s.row0 + half * TILE + warp * 32 >= P.rows) continue;
+    if (!ok || s.row0 + half * TILE + warp * 32 >= P.rows) continue;
     tmem_fence_after();
     const bool whole = s.first == 0 && s.last == s.tiles;
-    const int part = cta * 2 + (s.first == 0 ? 1 : 0);
-    const int ws_row = half * TILE + t;
-    const float inv = live && sum != 0.0f ? 1.0f / sum : 0.0f;
-    bool odd = false;
-    if (live && s.last > first_masked)
-      for (int j = max(s.first, first_masked); j < s.last; ++j)
-        for (int e = 0; e < TILE / 32; ++e) odd |= C.odd[(j - first_masked) * (TILE / 32) + e] != 0;
+    const Workspace ws = workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows);
+    const int64_t part = cta * 2 + (s.first == 0 ? 1 : 0);
+    const bool some = live && sum != 0.0f;
+    const float inv = some ? 1.0f / sum : 0.0f;
+    uint32_t odd = 0;
+    for (int j = max(s.first, first_masked); j < s.last; ++j)
+      for (int e = 0; e < TILE / 32; ++e) odd |= C.odd[segment % 3][(j - first_masked) * (TILE / 32) + e];
     T* out = static_cast<T*>(P.L.out.data) + s.b * P.L.out.tree_stride + i * P.L.out.node_stride +
-             (s.head * P.group + row - i * P.group) * P.L.out.head_stride;
-    float* partial = ws.out + (static_cast<int64_t>(part) * P.ws_rows + ws_row) * D;
+             (static_cast<int64_t>(s.head) * P.group + g) * P.L.out.head_stride;
+    float4* partial = ws.out + part * (D / 4) * P.ws_rows + local;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
       __syncwarp();
       tmem_ld32(tm_o + c * 32, o);
       tmem_wait_ld();
-      if (odd) {
+      if (odd && live) {  // rare: what the zeros in the values' place have left out
         for (int j = max(s.first, first_masked); j < s.last; ++j) {
-          const Seen v = seen_of(P, C, s, node, j * TILE);
+          const int32_t* parent = P.L.nodes.parent + static_cast<int64_t>(s.b) * P.L.nodes.stride;
+          const Seen v = seen_of(P, s, node, j * TILE, [&](int n) { return parent[n] < n ? parent[n] : -1; });
           for (int e = 0; e < TILE; ++e) {
-            if (!((C.odd[(j - first_masked) * (TILE / 32) + e / 32] >> (e % 32)) & 1)) continue;
+            if (!((C.odd[segment % 3][(j - first_masked) * (TILE / 32) + e / 32] >> (e % 32)) & 1)) continue;
             uint32_t word = v.w[0];
 #pragma unroll
             for (int k = 1; k < TILE / 32; ++k)
@@ -591,28 +626,26 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
           }
         }
       }
-      if (whole) {
-        if (row < P.rows) {
+      if (!whole) {
+        if (live) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float z = __uint_as_float(o[q * 8 + e]) * inv;
-              y[e] = live && sum != 0.0f ? z : 0.0f;
-            }
-            *reinterpret_cast<uint4*>(out + c * 32 + q * 8) = pack8<T>(y);
-          }
+          for (int q = 0; q < 8; ++q)
+            partial[(c * 8 + q) * P.ws_rows] = make_float4(__uint_as_float(o[q * 4]), __uint_as_float(o[q * 4 + 1]),
+                                                           __uint_as_float(o[q * 4 + 2]), __uint_as_float(o[q * 4 + 3]));
         }
-      } else if (live) {
+      } else if (row < P.rows) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<uint4*>(partial + c * 32 + q * 4) = make_uint4(o[q * 4], o[q * 4 + 1], o[q * 4 + 2], o[q * 4 + 3]);
+        for (int q = 0; q < 4; ++q) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = some ? __uint_as_float(o[q * 8 + e]) * inv : 0.0f;
+          *reinterpret_cast<uint4*>(out + c * 32 + q * 8) = pack8<T>(y);
+        }
       }
     }
-    if (!whole && live) ws.sums[static_cast<int64_t>(part) * P.ws_rows + ws_row] = make_float2(ref, sum);
+    if (!whole && live) ws.sums[part * P.ws_rows + local] = make_float2(ref, sum);
     tmem_fence_before();
-    if (!whole && s.first == 0 && half == 0 && t == 0) {
+    if (!whole && s.first == 0 && local == 0) {
       // the CTAs after this one whose ranges begin inside the item
       const int64_t end = range_start(C.total, cta + 1, ctas) + (s.tiles - s.last);
       int pieces = 1;
@@ -626,8 +659,7 @@ template <typename T, int D, int NH>
 __global__ void __launch_bounds__(Layout<D, NH>::THREADS, 1)
     attend_kernel(const __grid_constant__ Plan P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   using Y = Layout<D, NH>;
-  extern __shared__ uint8_t raw[];
-  uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  extern __shared__ __align__(1024) uint8_t smem[];  // nothing static, so it starts on a swizzle group
   uint8_t* ring = smem + Y::Q_BYTES;
   Control& C = *reinterpret_cast<Control*>(ring + Y::STAGES * Y::KV_BYTES);
   const int warp = __shfl_sync(FULL, threadIdx.x / 32, 0);
@@ -635,8 +667,10 @@ __global__ void __launch_bounds__(Layout<D, NH>::THREADS, 1)
     for (int i = 0; i < Y::STAGES; ++i) {
       mbar_init(&C.full[i], 1);
       mbar_init(&C.empty[i], 1);
+      mbar_init(&C.clean[i], 2);
     }
-    mbar_init(&C.q_full, NH * 4);
+    mbar_init(&C.q_full, 2);
+    mbar_init(&C.q_empty, 1);
     mbar_init(&C.drain, 1);
     for (int h = 0; h < NH; ++h) {
       mbar_init(&C.s_full[h], 1);
@@ -678,8 +712,22 @@ __global__ void __launch_bounds__(Layout<D, NH>::THREADS, 1)
     for (int b = b0; b < b1; ++b) {
       const int64_t n = tree_tiles<NH>(P, b);
       if (from < at + n) {
-        C.first_b = b;
-        C.first_tile = from - at;
+        int64_t skip = from - at;
+        int len, cnt;
+        tree_of(P, b, len, cnt);
+        for (int rt = 0;; ++rt) {
+          int end, tiles;
+          item_tiles<NH>(P, len, cnt, rt, end, tiles);
+          const int64_t all = static_cast<int64_t>(tiles) * P.L.kv.n_kv_heads;
+          if (skip < all) {
+            C.b = b;
+            C.rt = rt;
+            C.head = static_cast<int>(skip / tiles);
+            C.at = static_cast<int>(skip % tiles);
+            break;
+          }
+          skip -= all;
+        }
         break;
       }
       at += n;
@@ -707,7 +755,7 @@ __global__ void __launch_bounds__(Layout<D, NH>::THREADS, 1)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   }
   if (warp < NH * 4) {
-    softmax_role<T, D, NH>(P, C, smem, ring, to - from, cta, ctas, warp / 4);
+    softmax_role<T, D, NH>(P, C, to - from, cta, ctas, warp / 4);
   } else if (warp == NH * 4) {
     load_role<D, NH>(P, &mk, &mv, C, smem_u32(ring), to - from);
   } else if (warp == NH * 4 + 1) {
@@ -715,6 +763,8 @@ __global__ void __launch_bounds__(Layout<D, NH>::THREADS, 1)
       if (elect()) mma_commit(&C.drain);  // products in flight end before their memory is given back
       mbar_wait(&C.drain, 0);
     }
+  } else {
+    side_role<T, D, NH>(P, C, smem_u32(smem), ring, to - from);
   }
   __syncwarp();
   tmem_fence_before();
@@ -726,43 +776,47 @@ __global__ void __launch_bounds__(Layout<D, NH>::THREADS, 1)
 }
 
 // The rows of items whose tiles lie in several ranges: CTA x of grid.x looks
-// at what range x left, one warp per row.
+// at what range x left, one thread per 8 elements of a row.
+constexpr int JOIN_THREADS = 256;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ Plan P) {
+__global__ void __launch_bounds__(JOIN_THREADS) attend_join_kernel(const __grid_constant__ Plan P) {
   grid_dependency_wait();
   grid_dependents_launch();
   const Workspace ws = workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows);
   const int cta = blockIdx.x;
   const JoinRecord rec = ws.records[cta];
-  if (rec.pieces == 0) return;
-  const int r = blockIdx.y * 8 + threadIdx.x / 32, lane = threadIdx.x % 32, row = rec.row0 + r;
-  if (r >= P.ws_rows || row >= P.rows) return;
-  const int i = row / P.group, g = row - i * P.group;
+  const int idx = blockIdx.y * JOIN_THREADS + threadIdx.x, r = idx % P.ws_rows, q = idx / P.ws_rows;
+  if (rec.pieces == 0 || q >= D / 8 || rec.row0 + r >= P.rows) return;
+  int i, g;
+  Rows(P, rec.row0).get(P, r, i, g);
   int len, cnt;
   tree_of(P, rec.b, len, cnt);
-  constexpr int E = D / 32;
-  float acc[E], sum = 0.0f, top = -INFINITY;
+  float y[8], sum = 0.0f, top = -INFINITY;
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+  for (int e = 0; e < 8; ++e) y[e] = 0.0f;
   if (P.L.nodes.begin + i < cnt) {
-    for (int p = lane; p < rec.pieces; p += 32)
-      top = fmaxf(top, ws.sums[static_cast<int64_t>((cta + p) * 2 + (p == 0 ? 1 : 0)) * P.ws_rows + r].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+    // part p of the item: the end of range cta, then the starts of the next ones
+    auto part = [&](int p) { return static_cast<int64_t>(cta + p) * 2 + (p == 0 ? 1 : 0); };
+#pragma unroll 4
+    for (int p = 0; p < rec.pieces; ++p) top = fmaxf(top, ws.sums[part(p) * P.ws_rows + r].x);
     const float sub = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
     for (int p = 0; p < rec.pieces; ++p) {
-      const int64_t at = static_cast<int64_t>((cta + p) * 2 + (p == 0 ? 1 : 0)) * P.ws_rows + r;
-      const float2 ms = ws.sums[at];
+      const float2 ms = ws.sums[part(p) * P.ws_rows + r];
+      const float4* o = ws.out + (part(p) * (D / 4) + q * 2) * P.ws_rows + r;
+      const float4 a = o[0], b = o[P.ws_rows];
       const float f = ex2(ms.x - sub);
       sum += ms.y * f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += ws.out[at * D + lane * E + e] * f;
+      y[0] += a.x * f, y[1] += a.y * f, y[2] += a.z * f, y[3] += a.w * f;
+      y[4] += b.x * f, y[5] += b.y * f, y[6] += b.z * f, y[7] += b.w * f;
     }
   }
-  T* out = static_cast<T*>(P.L.out.data) + rec.b * P.L.out.tree_stride + i * P.L.out.node_stride +
-           (rec.head * P.group + g) * P.L.out.head_stride + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = T(sum == 0.0f ? 0.0f : acc[e] / sum);
+  for (int e = 0; e < 8; ++e) y[e] = sum == 0.0f ? 0.0f : y[e] / sum;
+  T* out = static_cast<T*>(P.L.out.data) + rec.b * P.L.out.tree_stride + i * P.L.out.node_stride +
+           (static_cast<int64_t>(rec.head) * P.group + g) * P.L.out.head_stride + q * 8;
+  *reinterpret_cast<uint4*>(out) = pack8<T>(y);
 }
 
 // -------------------------------------------------------------------- host ---
@@ -803,7 +857,7 @@ bool pool_map(CUtensorMap* map, const spec_tree_kv_t& kv, void* base, int layer,
 template <typename T, int D, int NH>
 cudaError_t attend(Plan& P, cudaStream_t stream) {
   using Y = Layout<D, NH>;
-  constexpr int SMEM = 1024 + Y::Q_BYTES + Y::STAGES * Y::KV_BYTES + static_cast<int>(sizeof(Control));
+  constexpr int SMEM = Y::Q_BYTES + Y::STAGES * Y::KV_BYTES + static_cast<int>(sizeof(Control));
   static_assert(SMEM <= 232448, "shared memory of one CTA");
   static_assert(NH * (TILE + D) <= Y::COLUMNS, "tensor memory");
   P.row_tiles = (P.rows + NH * TILE - 1) / (NH * TILE);
@@ -814,7 +868,8 @@ cudaError_t attend(Plan& P, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   err = launch_pdl(attend_kernel<T, D, NH>, dim3(P.L.num_sms), dim3(Y::THREADS), SMEM, stream, P, mk, mv);
   if (err != cudaSuccess) return err;
-  return launch_pdl(attend_join_kernel<T, D>, dim3(P.L.num_sms, (P.ws_rows + 7) / 8), dim3(256), 0, stream, P);
+  return launch_pdl(attend_join_kernel<T, D>, dim3(P.L.num_sms, (P.ws_rows * (D / 8) + JOIN_THREADS - 1) / JOIN_THREADS),
+                    dim3(JOIN_THREADS), 0, stream, P);
 }
 
 template <typename T, int D>
@@ -841,7 +896,8 @@ cudaError_t launch_attend(const AttendLaunch& L, cudaStream_t stream) {
   P.ws_rows = workspace_rows(P.rows);
   // a scale of zero would turn -inf into NaN: weights 2^(1e-30 S) are all one as well
   P.scale2 = fminf(fmaxf(fabsf(L.scale) * 1.4426950408889634f, 1e-30f), 3e38f);
-  P.flip = L.scale < 0.0f ? 0x80008000u : 0u;
+  P.negative = L.scale < 0.0f;
+  P.group_inv = P.group == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + P.group - 1) / P.group);
   if (L.kv.dtype == SPEC_TREE_BF16)
     return L.kv.head_dim == 128 ? attend_rows<__nv_bfloat16, 128>(P, stream) : attend_rows<__nv_bfloat16, 64>(P, stream);
   return L.kv.head_dim == 128 ? attend_rows<__half, 128>(P, stream) : attend_rows<__half, 64>(P, stream);

@@ -56,7 +56,9 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
 
 // Instruction descriptor of a 16-bit product with float32 sums: M = 128, N
 // columns; both operands of one type.  A is K-major; B K-major, or N-major
-// (b_n_major: rows of N elements, one per step of K).
+// (b_n_major: rows of N elements, one per step of K).  MMA_NEGATE_A: -A.
+constexpr uint32_t MMA_NEGATE_A = 1u << 13;
+
 __host__ __device__ constexpr uint32_t mma_descriptor(bool bf16, int n, bool b_n_major) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_n_major ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
@@ -124,12 +126,15 @@ __device__ __forceinline__ void tile_g2s(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+// 16 bytes global -> shared, or zeros; complete after async_copies_wait().
+__device__ __forceinline__ void async_copy16(uint32_t dst, const void* src, bool zeros) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(zeros ? 0 : 16) : "memory");
 }
 
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+__device__ __forceinline__ void async_copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
