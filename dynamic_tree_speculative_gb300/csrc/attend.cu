@@ -2,17 +2,27 @@
 //
 // Rows.  The query heads that share a key head, over all nodes of the call,
 // are the rows of one product: row r is node r / group, head r % group.  128
-// rows make a half; calls of more than 128 rows work on two halves at a time,
-// so that one half's softmax runs under the other half's products and keys
-// and values are loaded once for both.
+// rows fill the lanes of one accumulator ("half"); a CTA has two, so that one
+// half's softmax runs under the other half's products:
+//   - calls of more than 128 rows take 256 rows at a time, 128 in each half,
+//     and load keys and values once for both;
+//   - calls of up to 128 rows (PAIR) give both halves the same rows: one takes
+//     the even tiles of a segment, the other the odd ones, and their sums are
+//     put together at its end.
 //
 // Work.  An item is (tree, rows of 128 or 256, key head); its tokens are cut
-// into tiles of 128.  All items' tiles, one after the other, are dealt to the
-// CTAs (one per SM) in equal consecutive ranges, so a long cache is split over
-// the card and a batch of ragged ones is balanced by the same rule.  An item
-// whose tiles lie in one range is finished there; otherwise each range leaves
+// into tiles of 128.  The tiles are dealt to the CTAs (one per SM) in one of
+// two ways:
+//   - ranges: all items' tiles, one after the other, in equal consecutive
+//     ranges.  A long cache is split over the card and a ragged batch is
+//     balanced; a CTA begins and ends inside items;
+//   - pieces, where the items are fewer than the CTAs: each item cut into
+//     equal pieces, one per CTA, their length the least for which there are
+//     CTAs enough.  Taken where the length and one segment's fixed cost are
+//     below a range's length and two.
+// An item that one CTA has whole is finished there; otherwise each CTA leaves
 // its sums, their reference and its unnormalised output in the workspace, and
-// attend_join_kernel puts the parts together in order.
+// the parts are put together in order.
 //
 // Tile.  S = Q K^T in tensor memory (128 lanes: one row per softmax thread);
 // weights w = 2^(scale S - ref), rounded to the cache's type and stored over
@@ -44,13 +54,18 @@ constexpr int PANEL_BYTES = TILE * 128;         // 128 rows of 64 elements
 constexpr int MASKED_TILES = SPEC_TREE_MAX_NODES / TILE + 2;
 constexpr float LAZY = 8.0f;                    // log2 of what a weight may exceed its reference by
 constexpr int MAX_STAGES = 10;
-constexpr int SPINS = 64;                       // polls of a wait before it suspends the thread
+constexpr int THREADS = 3 * TILE;               // two softmax warpgroups and one of helpers
+constexpr int HELPERS = 2 * TILE / 32;          // the helpers' first warp
+constexpr int COLUMNS = 512;                    // tensor memory: S of both halves, then O of both
+constexpr int MAX_PIECE_ITEMS = 256;            // (tree, rows) of calls that may be dealt in pieces
+constexpr int SEGMENT_COST = 3;                 // fixed cost of a segment, in tiles
 
 struct Plan {
   AttendLaunch L;
   int group, rows, row_tiles, page_shift, box, ws_rows;
-  uint32_t group_inv;  // ceil(2^32 / group), 0 for a group of one
+  uint64_t group_inv;  // floor(2^64 / group) + 1, 0 for a group of one
   float scale2;        // |scale| log2(e)
+  bool may_piece;      // no more items than CTAs
   bool negative;       // scale < 0: the products take -Q
 };
 
@@ -74,26 +89,30 @@ __host__ __device__ inline Workspace workspace_of(void* ws, int num_sms, int ws_
   return w;
 }
 
-template <int D, int NH>
+template <int D, bool PAIR>
 struct Layout {
+  static constexpr int ROWS = PAIR ? TILE : 2 * TILE;  // rows of an item
   static constexpr int PANELS = D / PANEL;
   static constexpr int KV_BYTES = PANELS * PANEL_BYTES;
-  static constexpr int Q_BYTES = NH * KV_BYTES;
+  static constexpr int Q_BYTES = (ROWS / TILE) * KV_BYTES;
   static constexpr int STAGES = (7 * 32768 - Q_BYTES) / KV_BYTES < MAX_STAGES ? (7 * 32768 - Q_BYTES) / KV_BYTES : MAX_STAGES;
-  static constexpr int COLUMNS = NH * (TILE + D) > 256 ? 512 : 256;
-  static constexpr int THREADS = (NH + 1) * TILE;
 };
 
 struct Control {
-  uint64_t full[MAX_STAGES], empty[MAX_STAGES], clean[MAX_STAGES];
-  uint64_t q_full, q_empty, s_full[2], w_full[2][2], o_full[2], drain;
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES];
+  uint64_t q_full, q_empty, v_full, v_clean, s_full[2], w_full[2][2], o_full[2], drain;
   uint32_t tmem;
   int abort;
-  int64_t scan[16];
-  int64_t total;
-  int b, rt, head, at;                       // where this CTA's range begins
+  int64_t scan[THREADS / 32];
+  int64_t total, from, to;  // tiles of the call, and this CTA's range or piece of them
+  int pieces;               // pieces of this CTA's item, 0: ranges
+  int b, rt, head, at;      // where this CTA begins
   uint32_t odd[3][MASKED_TILES * (TILE / 32)];  // tokens with a value that is not finite, by segment modulo 3
-  uint16_t parent[2][SPEC_TREE_MAX_NODES];      // by segment modulo 2
+  uint8_t up[2][SPEC_TREE_MAX_NODES];           // node minus parent, by segment modulo 2; 0: none, 255: more
+  union {
+    float2 pair[TILE];         // the odd tiles' (reference, sum)
+    int tiles[MAX_PIECE_ITEMS];  // setup: tiles of (tree, rows)
+  };
 };
 
 // A consecutive piece of an item's tiles: what one CTA does at a time.
@@ -118,23 +137,28 @@ __device__ __forceinline__ uint32_t tree_of(const Plan& P, int b, int& len, int&
   return bad;
 }
 
-template <int NH>
+__device__ __forceinline__ int node_of_row(const Plan& P, int row) {  // row / group
+  return P.group_inv ? static_cast<int>(__umul64hi(row, P.group_inv)) : row;
+}
+
+template <int ROWS>
 __device__ __forceinline__ void item_tiles(const Plan& P, int len, int cnt, int rt, int& end, int& tiles) {
-  const int last_row = min((rt + 1) * NH * TILE, P.rows) - 1;
-  const int nodes = min(cnt, P.L.nodes.begin + last_row / P.group + 1);
-  const int first = P.L.nodes.begin + rt * NH * TILE / P.group;
+  const int last_row = min((rt + 1) * ROWS, P.rows) - 1;
+  const int nodes = min(cnt, P.L.nodes.begin + node_of_row(P, last_row) + 1);
+  const int first = P.L.nodes.begin + node_of_row(P, rt * ROWS);
   end = first < cnt ? len + nodes : 0;  // rows of nodes that do not exist read nothing
   tiles = end > 0 ? (end + TILE - 1) / TILE : 1;
 }
 
-template <int NH>
+template <int ROWS>
 __device__ __forceinline__ int64_t tree_tiles(const Plan& P, int b) {
   int len, cnt;
   tree_of(P, b, len, cnt);
   int64_t sum = 0;
+#pragma unroll 1
   for (int rt = 0; rt < P.row_tiles; ++rt) {
     int end, tiles;
-    item_tiles<NH>(P, len, cnt, rt, end, tiles);
+    item_tiles<ROWS>(P, len, cnt, rt, end, tiles);
     sum += tiles;
   }
   return sum * P.L.kv.n_kv_heads;
@@ -144,14 +168,14 @@ __device__ __forceinline__ int64_t range_start(int64_t total, int c, int ctas) {
 
 // The segments of a CTA's range, one after the other; every role walks them
 // for itself.
-template <int NH>
+template <int ROWS>
 struct Walk {
   int b, rt, head, at;
   int64_t left;
   int len, cnt;
 
-  __device__ __forceinline__ void begin(const Plan& P, const Control& C, int64_t tiles) {
-    left = tiles;
+  __device__ __forceinline__ void begin(const Plan& P, const Control& C) {
+    left = C.to - C.from;
     if (left <= 0) return;
     b = C.b;
     rt = C.rt;
@@ -164,11 +188,11 @@ struct Walk {
     if (left <= 0) return false;
     s.b = b;
     s.head = head;
-    s.row0 = rt * NH * TILE;
+    s.row0 = rt * ROWS;
     s.len = len;
     s.cnt = cnt;
-    item_tiles<NH>(P, len, cnt, rt, s.end, s.tiles);
-    s.clear = P.L.nodes.parent ? len : len + min(cnt, P.L.nodes.begin + s.row0 / P.group + 1);
+    item_tiles<ROWS>(P, len, cnt, rt, s.end, s.tiles);
+    s.clear = P.L.nodes.parent ? len : len + min(cnt, P.L.nodes.begin + node_of_row(P, s.row0) + 1);
     s.first = at;
     const int64_t n = min64(left, s.tiles - at);
     s.last = at + static_cast<int>(n);
@@ -185,33 +209,14 @@ struct Walk {
   }
 };
 
-// Row `row0` + r of an item: node i0 + (rem + r) / group of the call, head
-// (rem + r) % group.  rem + r < 2^15, so the product with the rounded-up
-// inverse is exact.
-struct Rows {
-  int i0, rem;
-  __device__ __forceinline__ Rows(const Plan& P, int row0) : i0(row0 / P.group), rem(row0 - row0 / P.group * P.group) {}
-  __device__ __forceinline__ void get(const Plan& P, int r, int& i, int& g) const {
-    const int x = rem + r;
-    const int n = P.group_inv ? static_cast<int>(__umulhi(x, P.group_inv)) : x;
-    i = i0 + n;
-    g = x - n * P.group;
-  }
-};
-
 // A wait that gives up when it, or another role of the CTA, has run out.
+// (The kernel's code is cold in the instruction cache when a CTA starts, so
+// what is not on the way of every tile is kept out of line or rolled.)
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Control& C, uint32_t* status) {
   const uint32_t addr = smem_u32(bar);
-  uint32_t done;
-  for (int spin = 0; spin < SPINS; ++spin) {
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(addr), "r"(parity)
-        : "memory");
-    if (done) return true;
-  }
+#pragma unroll 1
   for (uint32_t it = 0; it < WAIT_LIMIT; ++it) {
+    uint32_t done;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
@@ -236,9 +241,17 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
 
+// A barrier of some of the CTA's warps (converged: .aligned instructions of a
+// warp whose lanes have parted are undefined).
+__device__ __forceinline__ void warps_meet(int id, int threads) {
+  __syncwarp();
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // bit j: the row's node sees slot `base` + j of the 128 slots of a tile
 struct Seen {
   uint32_t w[TILE / 32];
+  __device__ __forceinline__ uint32_t get(int i) const { return i < 2 ? (i == 0 ? w[0] : w[1]) : (i == 2 ? w[2] : w[3]); }
 };
 
 __device__ __forceinline__ uint32_t below(int n) {  // the n lowest bits, n clamped to 0 .. 32
@@ -276,29 +289,31 @@ __device__ __forceinline__ bool odd16(uint32_t h) {  // infinity or NaN in the l
 // One warp: tokens' keys and values from their pages into the ring, K and V
 // of a tile one after the other.  Lane i copies the tile's i-th page (or its
 // 128 tokens of a larger one); pages past the item's end are not read.
-template <int D, int NH>
+template <int D, bool PAIR>
 __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* mk, const CUtensorMap* mv, Control& C,
-                                          uint32_t ring, int64_t my_tiles) {
-  using Y = Layout<D, NH>;
+                                          uint32_t ring) {
+  using Y = Layout<D, PAIR>;
   const int lane = threadIdx.x % 32;
   const int boxes = TILE / P.box;
-  Walk<NH> walk;
-  walk.begin(P, C, my_tiles);
+  Walk<Y::ROWS> walk;
+  walk.begin(P, C);
   Segment s;
   uint32_t n = 0;  // loads so far
   while (walk.next(P, s)) {
     const int32_t* table = P.L.kv.page_table + static_cast<int64_t>(s.b) * P.L.kv.table_stride;
+    auto entry = [&](int t) {  // the page of this lane's copy of tile t
+      const int slot = t * TILE + lane * P.box;
+      return t < s.last && lane < boxes && slot < s.end ? table[slot >> P.page_shift] : 0;
+    };
+    int next = entry(s.first);
     for (int t = s.first; t < s.last; ++t) {
       const int slot = t * TILE + lane * P.box;
       const bool mine = lane < boxes && slot < s.end;
-      int page = P.L.kv.n_pages;  // outside the pool: the copy fills zeros
-      if (mine) {
-        const int idx = slot >> P.page_shift;
-        const int got = idx < P.L.kv.max_pages ? table[idx] : -1;
-        if (got >= 0 && got < P.L.kv.n_pages)
-          page = got;
-        else
-          set_status(P.L.status, SPEC_TREE_S_PAGES);
+      int page = next;
+      next = entry(t + 1);
+      if (page < 0 || page >= P.L.kv.n_pages) {
+        set_status(P.L.status, SPEC_TREE_S_PAGES);
+        page = P.L.kv.n_pages;  // outside the pool: the copy fills zeros
       }
       const int off = slot & (P.L.kv.page_size - 1);
       const int used = s.end > 0 ? min(boxes, (s.end - t * TILE + P.box - 1) / P.box) : 0;
@@ -326,86 +341,124 @@ __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* mk, 
 
 // One warp: the products.  The halves take turns, so that while one half's
 // weights are made the other half's products run.  False: a wait gave up.
-template <typename T, int D, int NH>
-__device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t q_smem, uint32_t ring, int64_t my_tiles) {
-  using Y = Layout<D, NH>;
+template <typename T, int D, bool PAIR>
+__device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t q_smem, uint32_t ring) {
+  using Y = Layout<D, PAIR>;
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t ID_S = mma_descriptor(BF, TILE, false), ID_O = mma_descriptor(BF, D, true);
   constexpr int KV16 = Y::KV_BYTES / 16, PANEL16 = PANEL_BYTES / 16;  // descriptors count 16 bytes
-  const uint32_t tmem = uniform(C.tmem), q_low = smem_descriptor_low(q_smem, 0);
+  const uint32_t tmem = uniform(C.tmem), q_low = uniform(smem_descriptor_low(q_smem, 0));
   const uint32_t k_low = smem_descriptor_low(ring, 0), v_low = smem_descriptor_low(ring, PANEL_BYTES);
-  Walk<NH> walk;
-  walk.begin(P, C, my_tiles);
-  Segment s;
-  uint32_t n = 0, segment = 0, tile = 0;  // loads, segments, tiles so far
-  uint32_t* status = P.L.status;
-
   const uint32_t id_s = uniform(P.negative ? ID_S | MMA_NEGATE_A : ID_S);
-  uint32_t clean = 0;  // bit i: parity of slot i's next cleaning
+  uint32_t* status = P.L.status;
+  Walk<Y::ROWS> walk;
+  walk.begin(P, C);
+  Segment s = {};
+  uint32_t n = 0, segment = 0;   // loads, segments so far
+  uint32_t parity = 0;           // bit h: parity of half h's next weights
+  uint32_t cleaned = 0;          // tiles whose values were cleaned so far
 
-  auto scores = [&](int h, uint32_t stage) {
-    const uint32_t a = uniform(q_low) + h * KV16, b = uniform(k_low + stage * KV16);
+  auto ready = [&](uint32_t load) { return warp_wait(&C.full[load % Y::STAGES], (load / Y::STAGES) & 1, C, status); };
+  // S of half h from the keys of a load
+  auto scores = [&](int h, uint32_t load) {
+    const uint32_t a = uniform(q_low + (PAIR ? 0 : h * KV16)), b = uniform(k_low + load % Y::STAGES * KV16);
+    const uint32_t to = uniform(tmem + h * TILE);
     if (elect()) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const int at = (k / 4) * PANEL16 + (k % 4) * 2;
-        mma_ss(tmem + h * TILE, smem_descriptor(a + at), smem_descriptor(b + at), id_s, k > 0);
+        mma_ss(to, smem_descriptor(a + at), smem_descriptor(b + at), id_s, k > 0);
       }
       mma_commit(&C.s_full[h]);
     }
     __syncwarp();
   };
-
-  while (walk.next(P, s)) {
-    const uint32_t ks = n % Y::STAGES;
-    if (!warp_wait(&C.q_full, segment & 1, C, status)) return false;
-    if (!warp_wait(&C.full[ks], (n / Y::STAGES) & 1, C, status)) return false;
-    tmem_fence_after();
-    for (int h = 0; h < NH; ++h) scores(h, ks);
-    if (elect()) {
-      mma_commit(&C.empty[ks]);
-      if (s.first + 1 == s.last) mma_commit(&C.q_empty);
-    }
+  auto give_back = [&](uint64_t* bar) {
+    if (elect()) mma_commit(bar);
     __syncwarp();
-    for (int t = s.first; t < s.last; ++t, n += 2, ++tile) {
-      const uint32_t vs = (n + 1) % Y::STAGES, next = (n + 2) % Y::STAGES;
-      const uint32_t b = uniform(v_low + vs * KV16), add = uniform(t > s.first);
-      const bool more = t + 1 < s.last;
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        if (h == 0) {
-          if (!warp_wait(&C.full[vs], ((n + 1) / Y::STAGES) & 1, C, status)) return false;
-          if ((t + 1) * TILE > s.clear) {
-            if (!warp_wait(&C.clean[vs], (clean >> vs) & 1, C, status)) return false;
-            clean ^= 1u << vs;
-          }
-        }
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          if (!warp_wait(&C.w_full[h][part], tile & 1, C, status)) return false;
-          tmem_fence_after();
-          if (elect()) {
-#pragma unroll
-            for (int k = part * TILE / 32; k < (part + 1) * TILE / 32; ++k)
-              mma_ts(tmem + NH * TILE + h * D, tmem + h * TILE + k * 8, smem_descriptor(b + k * (16 * 128 / 16)), ID_O,
-                     k > 0 || add);
-            if (part == 1 && !more) mma_commit(&C.o_full[h]);
-          }
-          __syncwarp();
-        }
-        if (more) {
-          if (h == 0 && !warp_wait(&C.full[next], ((n + 2) / Y::STAGES) & 1, C, status)) return false;
-          tmem_fence_after();
-          scores(h, next);
-        }
-      }
+  };
+  // O of half h from the values of a load, as the weights' two parts come
+  auto output = [&](int h, uint32_t load, bool first, bool last) {
+    const uint32_t b = uniform(v_low + load % Y::STAGES * KV16), add = uniform(!first);
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+      if (!warp_wait(&C.w_full[h][part], (parity >> h) & 1, C, status)) return false;
+      tmem_fence_after();
+      const uint32_t to = uniform(tmem + 2 * TILE + h * D), from = uniform(tmem + h * TILE + part * (TILE / 4));
+      const uint32_t low = uniform(b + part * (64 * 128 / 16));
       if (elect()) {
-        mma_commit(&C.empty[vs]);
-        if (more) mma_commit(&C.empty[next]);
-        if (t + 2 == s.last) mma_commit(&C.q_empty);
+#pragma unroll
+        for (int k = 0; k < TILE / 32; ++k)
+          mma_ts(to, from + k * 8, smem_descriptor(low + k * (16 * 128 / 16)), ID_O, k > 0 || part || add);
+        if (part == 1 && last) mma_commit(&C.o_full[h]);
       }
       __syncwarp();
     }
+    parity ^= 1u << h;
+    return true;
+  };
+  // values of tile t, cleaned where not every row sees it whole: the side
+  // warps are told when they are there, as they do not follow the ring's phases
+  auto values = [&](int t, uint32_t load) {
+    if (!ready(load)) return false;
+    if ((t + 1) * TILE > s.clear) {
+      warp_arrive(&C.v_full);
+      if (!warp_wait(&C.v_clean, cleaned++ & 1, C, status)) return false;
+    }
+    return true;
+  };
+
+  while (walk.next(P, s)) {
+    const int count = s.last - s.first;
+    if (!warp_wait(&C.q_full, segment & 1, C, status) || !ready(n)) return false;
+    tmem_fence_after();
+#pragma unroll 1
+    for (int h = 0; h < 2 && (!PAIR || h < count); ++h) {
+      if (PAIR && h == 1 && !ready(n + 2)) return false;
+      scores(h, PAIR ? n + 2 * h : n);
+      if (PAIR) give_back(&C.empty[(n + 2 * h) % Y::STAGES]);
+    }
+    if (!PAIR) give_back(&C.empty[n % Y::STAGES]);
+    if (count <= (PAIR ? 2 : 1)) give_back(&C.q_empty);
+    if (PAIR) {
+      // tile x by half x % 2; its successor there is tile x + 2
+#pragma unroll 1
+      for (int x = 0; x < count; ++x) {
+        const uint32_t v = n + 2 * x + 1, k = n + 2 * (x + 2);
+        const bool more = x + 2 < count;
+        if (!values(s.first + x, v) || !output(x & 1, v, x < 2, !more)) return false;
+        give_back(&C.empty[v % Y::STAGES]);
+        if (more) {
+          if (!ready(k)) return false;
+          tmem_fence_after();
+          scores(x & 1, k);
+          give_back(&C.empty[k % Y::STAGES]);
+          if (x + 3 == count) give_back(&C.q_empty);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int x = 0; x < count; ++x) {
+        const uint32_t v = n + 2 * x + 1, k = v + 1;
+        const bool more = x + 1 < count;
+        if (!values(s.first + x, v)) return false;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (!output(h, v, x == 0, !more)) return false;
+          if (more) {
+            if (h == 0 && !ready(k)) return false;
+            tmem_fence_after();
+            scores(h, k);
+          }
+        }
+        give_back(&C.empty[v % Y::STAGES]);
+        if (more) {
+          give_back(&C.empty[k % Y::STAGES]);
+          if (x + 2 == count) give_back(&C.q_empty);
+        }
+      }
+    }
+    n += 2 * count;
     ++segment;
   }
   return true;
@@ -414,34 +467,50 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
 // Two warps, ahead of the softmax: an item's queries and its nodes' parents
 // into shared memory, and the values of tiles that not every row sees whole:
 // those past the item's end and those that are not finite become zeros.
-template <typename T, int D, int NH>
-__device__ __forceinline__ void side_role(const Plan& P, Control& C, uint32_t q_smem, uint8_t* ring, int64_t my_tiles) {
-  using Y = Layout<D, NH>;
-  constexpr int CHUNKS = D / 8, THREADS = 64;
-  const int t = threadIdx.x % THREADS;
+template <typename T, int D, bool PAIR>
+__device__ __forceinline__ void side_role(const Plan& P, Control& C, uint32_t q_smem, uint8_t* ring) {
+  using Y = Layout<D, PAIR>;
+  constexpr int CHUNKS = D / 8, SIDE = 64, STEP = SIDE / CHUNKS;
+  const int t = threadIdx.x % SIDE;
   uint32_t* status = P.L.status;
-  Walk<NH> walk;
-  walk.begin(P, C, my_tiles);
+  // what STEP rows on means in nodes and heads
+  const int step_i = node_of_row(P, STEP), step_g = STEP - step_i * P.group;
+  const int64_t step = step_i * P.L.q.node_stride + step_g * P.L.q.head_stride;
+  const int64_t wrap = P.L.q.node_stride - P.group * P.L.q.head_stride;
+  Walk<Y::ROWS> walk;
+  walk.begin(P, C);
   Segment s;
-  uint32_t segment = 0, tile = 0;
+  uint32_t segment = 0, tile = 0, cleaned = 0;
   for (; walk.next(P, s); ++segment, tile += s.last - s.first) {
-    const Rows rows(P, s.row0);
     if (!warp_wait(&C.q_empty, (segment & 1) ^ 1, C, status)) return;
-    const int n = min(NH * TILE, P.rows - s.row0), ch = t % CHUNKS;
-    const T* from = static_cast<const T*>(P.L.q.data) + s.b * P.L.q.tree_stride +
+    const int n = min(Y::ROWS, P.rows - s.row0), ch = t % CHUNKS;
+    const int row = s.row0 + t / CHUNKS;
+    int i = node_of_row(P, row), g = row - i * P.group;
+    const int nodes = s.cnt - P.L.nodes.begin;  // rows of later nodes are zeros
+    const T* base = static_cast<const T*>(P.L.q.data) + s.b * P.L.q.tree_stride +
                     static_cast<int64_t>(s.head) * P.group * P.L.q.head_stride + ch * 8;
-    for (int r = t / CHUNKS; r < n; r += THREADS / CHUNKS) {
-      int i, g;
-      rows.get(P, r, i, g);
-      const bool live = P.L.nodes.begin + i < s.cnt;
-      async_copy16(q_smem + (r / TILE) * Y::KV_BYTES + (ch / 8) * PANEL_BYTES + (r % TILE) * 128 + (((ch % 8) ^ (r % 8)) * 16),
-                   live ? from + i * P.L.q.node_stride + g * P.L.q.head_stride : from, !live);
+    const T* from = base + i * P.L.q.node_stride + g * P.L.q.head_stride;
+    const uint32_t to = q_smem + (ch / 8) * PANEL_BYTES;
+#pragma unroll 2
+    for (int r = t / CHUNKS; r < n; r += STEP) {
+      const bool live = i < nodes;
+      async_copy16(to + (r / TILE) * Y::KV_BYTES + (r % TILE) * 128 + (((ch % 8) ^ (r % 8)) * 16), live ? from : base, !live);
+      i += step_i;
+      g += step_g;
+      from += step;
+      if (g >= P.group) {
+        g -= P.group;
+        ++i;
+        from += wrap;
+      }
     }
     if (P.L.nodes.parent) {
-      for (int i = t; i < s.cnt; i += THREADS) {
-        const int up = P.L.nodes.parent[static_cast<int64_t>(s.b) * P.L.nodes.stride + i];
-        C.parent[segment % 2][i] = static_cast<uint16_t>(up < 0 || up >= i ? 0xffff : up);
-        if (up >= i) set_status(status, SPEC_TREE_S_NODES);
+      const int32_t* parent = P.L.nodes.parent + static_cast<int64_t>(s.b) * P.L.nodes.stride;
+#pragma unroll 2
+      for (int n = t; n < s.cnt; n += SIDE) {
+        const int up = parent[n];
+        C.up[segment % 2][n] = static_cast<uint8_t>(up < 0 || up >= n ? 0 : min(n - up, 255));
+        if (up >= n) set_status(status, SPEC_TREE_S_NODES);
       }
     }
     async_copies_wait();
@@ -451,8 +520,9 @@ __device__ __forceinline__ void side_role(const Plan& P, Control& C, uint32_t q_
     const int first_masked = s.clear / TILE;
     for (int j = max(s.first, first_masked); j < s.last; ++j) {
       const uint32_t v = 2 * (tile + j - s.first) + 1;
+      if (!warp_wait(&C.v_full, cleaned++ & 1, C, status)) return;
       if (!warp_wait(&C.full[v % Y::STAGES], (v / Y::STAGES) & 1, C, status)) return;
-#pragma unroll
+#pragma unroll 1
       for (int part = 0; part < 2; ++part) {
         const int row = part * 64 + t;  // a token
         uint8_t* at = ring + (v % Y::STAGES) * Y::KV_BYTES + row * 128;
@@ -482,52 +552,95 @@ __device__ __forceinline__ void side_role(const Plan& P, Control& C, uint32_t q_
         if (t % 32 == 0) C.odd[segment % 3][(j - first_masked) * (TILE / 32) + part * 2 + t / 32] = word;
       }
       fence_proxy_async_smem();
-      warp_arrive(&C.clean[v % Y::STAGES]);
+      warp_arrive(&C.v_clean);
+    }
+  }
+}
+
+// What the zeros in the place of values that are not finite have left out of a
+// row, added to what the row's thread has just written (`out`, or `partial` in
+// the workspace's order).
+template <typename T, int D>
+__device__ __noinline__ void add_odd(const Plan& P, const Segment& s, const uint32_t* odd, int from, int node, T* out,
+                                     float* partial) {
+  const int first_masked = s.clear / TILE;
+  const int32_t* parent = P.L.nodes.parent + static_cast<int64_t>(s.b) * P.L.nodes.stride;
+  for (int j = from; j < s.last; ++j) {
+    const Seen v = seen_of(P, s, node, j * TILE, [&](int n) { return parent[n] < n ? parent[n] : -1; });
+    for (int w = 0; w < TILE / 32; ++w) {
+      for (uint32_t left = odd[(j - first_masked) * (TILE / 32) + w] & v.get(w); left; left &= left - 1) {
+        const int64_t off = kv_slot_offset(P.L.kv, s.b, j * TILE + w * 32 + __ffs(left) - 1, P.page_shift);
+        if (off < 0) continue;
+        const T* value = static_cast<const T*>(P.L.kv.v) + P.L.layer * P.L.kv.layer_stride + off +
+                         s.head * P.L.kv.head_stride;
+#pragma unroll 1
+        for (int d = 0; d < D; ++d) {
+          const float x = static_cast<float>(value[d]);
+          if (isfinite(x)) continue;
+          if (out)
+            out[d] = T(static_cast<float>(out[d]) + x);
+          else
+            partial[static_cast<int64_t>(d / 4) * P.ws_rows * 4 + d % 4] += x;
+        }
+      }
     }
   }
 }
 
 // 128 threads, one row each: weights, the running reference and sum, and the
 // output.
-template <typename T, int D, int NH>
-__device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int64_t my_tiles, int cta, int ctas, int half) {
+template <typename T, int D, bool PAIR>
+__device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta, int ctas, int half) {
+  using Y = Layout<D, PAIR>;
+  constexpr int EACH = PAIR ? 2 : 1;  // a half takes every tile, or every other one
   constexpr float SHIFT = std::is_same<T, __half>::value ? 7.0f : 0.0f;
   const int t = threadIdx.x % TILE, warp = t / 32;
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-  const uint32_t tm_s = C.tmem + half * TILE + lanes, tm_o = C.tmem + NH * TILE + half * D + lanes;
+  const uint32_t tm_s = C.tmem + half * TILE + lanes, tm_o = C.tmem + 2 * TILE + half * D + lanes;
   uint32_t* status = P.L.status;
-  Walk<NH> walk;
-  walk.begin(P, C, my_tiles);
+  Walk<Y::ROWS> walk;
+  walk.begin(P, C);
   Segment s;
-  uint32_t tile = 0, segment = 0;
-  bool ok = true;  // uniform over the warp
+  uint32_t tile = 0, segment = 0, ends = 0;  // tiles of this half, segments, segments with a tile of this half so far
+  bool ok = true;  // uniform over the warp; a warp that has given up still meets the others at barriers
   for (; walk.next(P, s); ++segment) {
-    const int local = half * TILE + t, row = s.row0 + local;
-    int i, g;
-    Rows(P, s.row0).get(P, local, i, g);
+    const int local = (PAIR ? 0 : half * TILE) + t, row = s.row0 + local;
+    const int i = node_of_row(P, row), g = row - i * P.group;
     const int node = P.L.nodes.begin + i;
     const bool live = row < P.rows && node < s.cnt;
     const bool warp_live = __any_sync(FULL, live);
     const int first_masked = s.clear / TILE;  // tiles from here on are not seen whole by every row
     float ref = -INFINITY, sum = 0.0f;
 
-    for (int j = s.first; j < s.last; ++j, ++tile) {
+    for (int j = s.first + (PAIR ? half : 0); j < s.last; j += EACH, ++tile) {
       const int base = j * TILE;
       const bool masked = base + TILE > s.clear;
       ok = ok && warp_wait(&C.s_full[half], tile & 1, C, status);
       if (warp_live && ok) {
         tmem_fence_after();
         uint32_t x[TILE];
+        if (masked) {
+          const int32_t* parent = P.L.nodes.parent + static_cast<int64_t>(s.b) * P.L.nodes.stride;
+          const Seen v = seen_of(P, s, live ? node : -1, base, [&](int n) {
+            const int up = C.up[segment % 2][n];
+            return up == 0 ? -1 : (up == 255 ? parent[n] : n - up);
+          });
+#pragma unroll 1
+          for (int c = 0; c < TILE / 32; ++c) {
+            __syncwarp();
+            tmem_ld32(tm_s + c * 32, x);
+            tmem_wait_ld();
+            const uint32_t word = v.get(c);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((word >> e) & 1)) x[e] = 0xff800000u;
+            tmem_st32(tm_s + c * 32, x);
+          }
+          tmem_wait_st();
+        }
 #pragma unroll
         for (int c = 0; c < TILE / 32; ++c) tmem_ld32(tm_s + c * 32, x + c * 32);
         tmem_wait_ld();
-        if (masked) {
-          const uint16_t* parent = C.parent[segment % 2];
-          const Seen v = seen_of(P, s, live ? node : -1, base, [&](int n) { return parent[n] == 0xffff ? -1 : parent[n]; });
-#pragma unroll
-          for (int c = 0; c < TILE; ++c)
-            if (!((v.w[c / 32] >> (c % 32)) & 1)) x[c] = 0xff800000u;
-        }
         float top8[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) top8[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
@@ -537,13 +650,13 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int64_t 
         const float top = P.scale2 * fmaxf(max3(max3(top8[0], top8[1], top8[2]), top8[3], top8[4]),
                                            max3(top8[5], top8[6], top8[7]));
         const bool grow = live && top > ref + LAZY;
-        if (j == s.first) {
+        if (j < s.first + EACH) {
           ref = top;
         } else if (__any_sync(FULL, grow)) {
           const float f = grow ? ex2(ref - top) : 1.0f;
           if (grow) ref = top;
           sum *= f;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(tm_o + c * 32, o);
@@ -583,48 +696,58 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int64_t 
       warp_arrive(&C.w_full[half][1]);
     }
 
-    ok = ok && warp_wait(&C.o_full[half], segment & 1, C, status);
-    if (!ok || s.row0 + half * TILE + warp * 32 >= P.rows) continue;
+    const bool mine = s.first + (PAIR ? half : 0) < s.last;
+    if (mine) ok = ok && warp_wait(&C.o_full[half], ends++ & 1, C, status);
+    // PAIR: warp w + 4 hands its rows' statistics to warp w, which puts both
+    // outputs together, and goes on when warp w has read them
+    const bool both = PAIR && s.last - s.first > 1;
+    float f0 = 1.0f, f1 = 0.0f;
+    if (both) {
+      if (half == 1) {
+        C.pair[t] = make_float2(ref, sum);
+        tmem_fence_before();
+        warps_meet(1 + warp, 64);
+        warps_meet(5 + warp, 64);
+        tmem_fence_after();
+        continue;
+      }
+      warps_meet(1 + warp, 64);
+      const float2 other = C.pair[t];
+      const float top = fmaxf(ref, other.x), sub = top == -INFINITY ? 0.0f : top;
+      f0 = ex2(ref - sub);
+      f1 = ex2(other.x - sub);
+      sum = sum * f0 + other.y * f1;
+      ref = top;
+    } else if (PAIR && half == 1) {
+      continue;
+    }
+    if (!ok || s.row0 + local - t + warp * 32 >= P.rows) {
+      if (both) warps_meet(5 + warp, 64);
+      continue;
+    }
     tmem_fence_after();
     const bool whole = s.first == 0 && s.last == s.tiles;
     const Workspace ws = workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows);
     const int64_t part = cta * 2 + (s.first == 0 ? 1 : 0);
     const bool some = live && sum != 0.0f;
     const float inv = some ? 1.0f / sum : 0.0f;
-    uint32_t odd = 0;
-    for (int j = max(s.first, first_masked); j < s.last; ++j)
-      for (int e = 0; e < TILE / 32; ++e) odd |= C.odd[segment % 3][(j - first_masked) * (TILE / 32) + e];
     T* out = static_cast<T*>(P.L.out.data) + s.b * P.L.out.tree_stride + i * P.L.out.node_stride +
              (static_cast<int64_t>(s.head) * P.group + g) * P.L.out.head_stride;
     float4* partial = ws.out + part * (D / 4) * P.ws_rows + local;
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
       __syncwarp();
       tmem_ld32(tm_o + c * 32, o);
-      tmem_wait_ld();
-      if (odd && live) {  // rare: what the zeros in the values' place have left out
-        for (int j = max(s.first, first_masked); j < s.last; ++j) {
-          const int32_t* parent = P.L.nodes.parent + static_cast<int64_t>(s.b) * P.L.nodes.stride;
-          const Seen v = seen_of(P, s, node, j * TILE, [&](int n) { return parent[n] < n ? parent[n] : -1; });
-          for (int e = 0; e < TILE; ++e) {
-            if (!((C.odd[segment % 3][(j - first_masked) * (TILE / 32) + e / 32] >> (e % 32)) & 1)) continue;
-            uint32_t word = v.w[0];
+      if (both) {
+        uint32_t o1[32];
+        tmem_ld32(tm_o + D + c * 32, o1);
+        tmem_wait_ld();
 #pragma unroll
-            for (int k = 1; k < TILE / 32; ++k)
-              if (e / 32 == k) word = v.w[k];
-            if (!((word >> (e % 32)) & 1)) continue;
-            const int64_t off = kv_slot_offset(P.L.kv, s.b, j * TILE + e, P.page_shift);
-            if (off < 0) continue;
-            const T* from = static_cast<const T*>(P.L.kv.v) + P.L.layer * P.L.kv.layer_stride + off +
-                            s.head * P.L.kv.head_stride + c * 32;
-#pragma unroll
-            for (int d = 0; d < 32; ++d) {
-              const float x = static_cast<float>(from[d]);
-              if (!isfinite(x)) o[d] = __float_as_uint(__uint_as_float(o[d]) + x);
-            }
-          }
-        }
+        for (int e = 0; e < 32; ++e)
+          o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
+      } else {
+        tmem_wait_ld();
       }
       if (!whole) {
         if (live) {
@@ -643,54 +766,35 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int64_t 
         }
       }
     }
+    if (s.last > first_masked) {
+      const int from = max(s.first, first_masked);
+      uint32_t odd = 0;
+      for (int x = (from - first_masked) * (TILE / 32); x < (s.last - first_masked) * (TILE / 32); ++x)
+        odd |= C.odd[segment % 3][x];
+      if (odd && live)
+        add_odd<T, D>(P, s, C.odd[segment % 3], from, node, whole ? out : nullptr, reinterpret_cast<float*>(partial));
+    }
     if (!whole && live) ws.sums[part * P.ws_rows + local] = make_float2(ref, sum);
     tmem_fence_before();
+    if (both) warps_meet(5 + warp, 64);
     if (!whole && s.first == 0 && local == 0) {
-      // the CTAs after this one whose ranges begin inside the item
-      const int64_t end = range_start(C.total, cta + 1, ctas) + (s.tiles - s.last);
-      int pieces = 1;
-      while (cta + pieces < ctas && range_start(C.total, cta + pieces, ctas) < end) ++pieces;
+      int pieces = C.pieces;
+      if (pieces == 0) {  // the CTAs after this one whose ranges begin inside the item
+        const int64_t end = C.to + (s.tiles - s.last);
+        for (pieces = 1; cta + pieces < ctas && range_start(C.total, cta + pieces, ctas) < end;) ++pieces;
+      }
       ws.records[cta] = JoinRecord{pieces, s.b, s.row0, s.head};
     }
   }
 }
 
-template <typename T, int D, int NH>
-__global__ void __launch_bounds__(Layout<D, NH>::THREADS, 1)
-    attend_kernel(const __grid_constant__ Plan P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using Y = Layout<D, NH>;
-  extern __shared__ __align__(1024) uint8_t smem[];  // nothing static, so it starts on a swizzle group
-  uint8_t* ring = smem + Y::Q_BYTES;
-  Control& C = *reinterpret_cast<Control*>(ring + Y::STAGES * Y::KV_BYTES);
-  const int warp = __shfl_sync(FULL, threadIdx.x / 32, 0);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < Y::STAGES; ++i) {
-      mbar_init(&C.full[i], 1);
-      mbar_init(&C.empty[i], 1);
-      mbar_init(&C.clean[i], 2);
-    }
-    mbar_init(&C.q_full, 2);
-    mbar_init(&C.q_empty, 1);
-    mbar_init(&C.drain, 1);
-    for (int h = 0; h < NH; ++h) {
-      mbar_init(&C.s_full[h], 1);
-      mbar_init(&C.w_full[h][0], 4);
-      mbar_init(&C.w_full[h][1], 4);
-      mbar_init(&C.o_full[h], 1);
-    }
-    C.abort = 0;
-    fence_mbar_init();
-  }
-  if (warp == NH * 4) tmem_alloc(&C.tmem, Y::COLUMNS);
-  tmem_fence_before();
-  grid_dependency_wait();
-  grid_dependents_launch();
-
-  // where this CTA's range begins: a scan of the trees' tiles
-  const int B = P.L.B, per = (B + Y::THREADS - 1) / Y::THREADS;
+// Where this CTA's range begins: a scan of the trees' tiles over all threads.
+template <int ROWS>
+__device__ __forceinline__ void find_range(const Plan& P, Control& C, int warp, int cta) {
+  const int B = P.L.B, per = (B + THREADS - 1) / THREADS;
   const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += tree_tiles<NH>(P, b);
+  for (int b = b0; b < b1; ++b) mine += tree_tiles<ROWS>(P, b);
   int64_t before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -700,45 +804,132 @@ __global__ void __launch_bounds__(Layout<D, NH>::THREADS, 1)
   if (threadIdx.x % 32 == 31) C.scan[warp] = before;
   __syncthreads();
   int64_t total = 0;
-  for (int w = 0; w < Y::THREADS / 32; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += C.scan[w];
     total += C.scan[w];
   }
   before -= mine;
-  const int ctas = static_cast<int>(min64(gridDim.x, total)), cta = blockIdx.x;
+  const int ctas = static_cast<int>(min64(gridDim.x, total));
   const int64_t from = range_start(total, min(cta, ctas), ctas), to = range_start(total, min(cta + 1, ctas), ctas);
-  if (from < to && before <= from && from < before + mine) {
-    int64_t at = before;
-    for (int b = b0; b < b1; ++b) {
-      const int64_t n = tree_tiles<NH>(P, b);
-      if (from < at + n) {
-        int64_t skip = from - at;
-        int len, cnt;
-        tree_of(P, b, len, cnt);
-        for (int rt = 0;; ++rt) {
-          int end, tiles;
-          item_tiles<NH>(P, len, cnt, rt, end, tiles);
-          const int64_t all = static_cast<int64_t>(tiles) * P.L.kv.n_kv_heads;
-          if (skip < all) {
-            C.b = b;
-            C.rt = rt;
-            C.head = static_cast<int>(skip / tiles);
-            C.at = static_cast<int>(skip % tiles);
-            break;
-          }
-          skip -= all;
-        }
-        break;
-      }
-      at += n;
-    }
-  }
   if (threadIdx.x == 0) {
     C.total = total;
-    workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows).records[cta].pieces = 0;
+    C.from = from;
+    C.to = to;
+    C.pieces = 0;
   }
+  if (from < to && before <= from && from < before + mine) {
+    int64_t skip = from - before;
+    int b = b0;
+    for (int64_t n; skip >= (n = tree_tiles<ROWS>(P, b)); ++b) skip -= n;
+    int len, cnt;
+    tree_of(P, b, len, cnt);
+    for (int rt = 0;; ++rt) {
+      int end, tiles;
+      item_tiles<ROWS>(P, len, cnt, rt, end, tiles);
+      const int64_t all = static_cast<int64_t>(tiles) * P.L.kv.n_kv_heads;
+      if (skip < all) {
+        C.b = b;
+        C.rt = rt;
+        C.head = static_cast<int>(skip / tiles);
+        C.at = static_cast<int>(skip % tiles);
+        break;
+      }
+      skip -= all;
+    }
+  }
+}
+
+// Pieces of an item of `tiles` tiles when a piece is to have about 1 / inv.
+__device__ __forceinline__ int pieces_of(int tiles, float inv) {
+  return max(1, min(tiles, static_cast<int>(ceilf(tiles * inv - 0.001f))));
+}
+
+// For no more items than CTAs: the least length of equal pieces for which
+// there are CTAs enough (one lane tries one of 32 lengths), and this CTA's
+// piece.  False: ranges are better.
+template <int ROWS>
+__device__ __forceinline__ bool find_piece(const Plan& P, Control& C, int warp, int cta) {
+  const int items = P.L.B * P.row_tiles, heads = P.L.kv.n_kv_heads, lane = threadIdx.x % 32;
+  for (int x = threadIdx.x; x < items; x += THREADS) {
+    int len, cnt, end, tiles;
+    tree_of(P, x / P.row_tiles, len, cnt);
+    item_tiles<ROWS>(P, len, cnt, x % P.row_tiles, end, tiles);
+    C.tiles[x] = tiles;
+  }
+  __syncthreads();
+  int sum = 0, most = 1;  // 2^31 slots at most in a tree: 2^24 tiles in each of 2^8 items
+  float total = 0.0f;
+  for (int x = lane; x < items; x += 32) {
+    total += static_cast<float>(C.tiles[x]);
+    most = max(most, C.tiles[x]);
+  }
+  total = warp_sum(total) * heads;
+  most = __reduce_max_sync(FULL, most);
+  const float fair = total / gridDim.x;
+  const int least = max(1, static_cast<int>(fair));
+  const float inv = 1.0f / (least + static_cast<float>(max(0, most - least)) * lane / 31.0f);
+  for (int x = 0; x < items; ++x) sum += pieces_of(C.tiles[x], inv);
+  const uint32_t enough = __ballot_sync(FULL, sum * heads <= static_cast<int>(gridDim.x));
+  // the longest length leaves every item whole, so one is always enough
+  const int best = enough ? __ffs(enough) - 1 : 31;
+  const float chosen = __shfl_sync(FULL, inv, best);
+  if (1.0f / chosen + SEGMENT_COST > fair + 2 * SEGMENT_COST) return false;
+  if (threadIdx.x == 0) {
+    int skip = cta, x = 0, n = 0;
+    for (; x < items; ++x) {
+      n = pieces_of(C.tiles[x], chosen);
+      if (skip < n * heads) break;
+      skip -= n * heads;
+    }
+    C.from = C.to = 0;
+    C.pieces = n;
+    if (x < items) {
+      const int64_t tiles = C.tiles[x], q = skip % n;
+      C.b = x / P.row_tiles;
+      C.rt = x % P.row_tiles;
+      C.head = skip / n;
+      C.at = static_cast<int>(tiles * q / n);
+      C.from = C.at;
+      C.to = tiles * (q + 1) / n;
+    }
+  }
+  return true;
+}
+
+template <typename T, int D, bool PAIR>
+__global__ void __launch_bounds__(THREADS, 1)
+    attend_kernel(const __grid_constant__ Plan P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  using Y = Layout<D, PAIR>;
+  extern __shared__ __align__(1024) uint8_t smem[];  // nothing static, so it starts on a swizzle group
+  uint8_t* ring = smem + Y::Q_BYTES;
+  Control& C = *reinterpret_cast<Control*>(ring + Y::STAGES * Y::KV_BYTES);
+  const int warp = __shfl_sync(FULL, threadIdx.x / 32, 0), cta = blockIdx.x;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Y::STAGES; ++i) {
+      mbar_init(&C.full[i], 1);
+      mbar_init(&C.empty[i], 1);
+    }
+    mbar_init(&C.q_full, 2);
+    mbar_init(&C.q_empty, 1);
+    mbar_init(&C.v_full, 1);
+    mbar_init(&C.v_clean, 2);
+    mbar_init(&C.drain, 1);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&C.s_full[h], 1);
+      mbar_init(&C.w_full[h][0], 4);
+      mbar_init(&C.w_full[h][1], 4);
+      mbar_init(&C.o_full[h], 1);
+    }
+    C.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == HELPERS) tmem_alloc(&C.tmem, COLUMNS);
+  grid_dependency_wait();
+  grid_dependents_launch();
+  if (!P.may_piece || !find_piece<Y::ROWS>(P, C, warp, cta)) find_range<Y::ROWS>(P, C, warp, cta);
+  if (threadIdx.x == 0) workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows).records[cta].pieces = 0;
   if (cta == 0)
-    for (int b = threadIdx.x; b < B; b += Y::THREADS) {
+    for (int b = threadIdx.x; b < P.L.B; b += THREADS) {
       int len, cnt;
       if (const uint32_t bad = tree_of(P, b, len, cnt)) set_status(P.L.status, bad);
     }
@@ -746,32 +937,30 @@ __global__ void __launch_bounds__(Layout<D, NH>::THREADS, 1)
   __syncthreads();
   tmem_fence_after();
 
-  // a softmax thread holds a row of 128 scores in registers: with two halves
-  // (384 threads of 168 registers) the helpers give some of theirs up
-  if (NH > 1) {
-    if (warp < NH * 4)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  }
-  if (warp < NH * 4) {
-    softmax_role<T, D, NH>(P, C, to - from, cta, ctas, warp / 4);
-  } else if (warp == NH * 4) {
-    load_role<D, NH>(P, &mk, &mv, C, smem_u32(ring), to - from);
-  } else if (warp == NH * 4 + 1) {
-    if (!product_role<T, D, NH>(P, C, smem_u32(smem), smem_u32(ring), to - from)) {
-      if (elect()) mma_commit(&C.drain);  // products in flight end before their memory is given back
-      mbar_wait(&C.drain, 0);
-    }
+  // a softmax thread holds a row of 128 scores in registers: of the 168 each
+  // thread starts with, the helpers give some up
+  if (warp < HELPERS) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    softmax_role<T, D, PAIR>(P, C, cta, static_cast<int>(min64(gridDim.x, C.total)), warp / 4);
   } else {
-    side_role<T, D, NH>(P, C, smem_u32(smem), ring, to - from);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == HELPERS) {
+      load_role<D, PAIR>(P, &mk, &mv, C, smem_u32(ring));
+    } else if (warp == HELPERS + 1) {
+      if (!product_role<T, D, PAIR>(P, C, smem_u32(smem), smem_u32(ring))) {
+        if (elect()) mma_commit(&C.drain);  // products in flight end before their memory is given back
+        mbar_wait(&C.drain, 0);
+      }
+    } else {
+      side_role<T, D, PAIR>(P, C, smem_u32(smem), ring);
+    }
   }
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
-  if (warp == NH * 4) {
+  if (warp == HELPERS) {
     tmem_fence_after();
-    tmem_free(C.tmem, Y::COLUMNS);
+    tmem_free(C.tmem, COLUMNS);
   }
 }
 
@@ -788,8 +977,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attend_join_kernel(const __grid_
   const JoinRecord rec = ws.records[cta];
   const int idx = blockIdx.y * JOIN_THREADS + threadIdx.x, r = idx % P.ws_rows, q = idx / P.ws_rows;
   if (rec.pieces == 0 || q >= D / 8 || rec.row0 + r >= P.rows) return;
-  int i, g;
-  Rows(P, rec.row0).get(P, r, i, g);
+  const int i = node_of_row(P, rec.row0 + r), g = rec.row0 + r - i * P.group;
   int len, cnt;
   tree_of(P, rec.b, len, cnt);
   float y[8], sum = 0.0f, top = -INFINITY;
@@ -854,19 +1042,21 @@ bool pool_map(CUtensorMap* map, const spec_tree_kv_t& kv, void* base, int layer,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, int NH>
+template <typename T, int D, bool PAIR>
 cudaError_t attend(Plan& P, cudaStream_t stream) {
-  using Y = Layout<D, NH>;
+  using Y = Layout<D, PAIR>;
   constexpr int SMEM = Y::Q_BYTES + Y::STAGES * Y::KV_BYTES + static_cast<int>(sizeof(Control));
   static_assert(SMEM <= 232448, "shared memory of one CTA");
-  static_assert(NH * (TILE + D) <= Y::COLUMNS, "tensor memory");
-  P.row_tiles = (P.rows + NH * TILE - 1) / (NH * TILE);
+  static_assert(2 * (TILE + D) <= COLUMNS, "tensor memory");
+  P.row_tiles = (P.rows + Y::ROWS - 1) / Y::ROWS;
+  const int64_t items = static_cast<int64_t>(P.L.B) * P.row_tiles;
+  P.may_piece = items * P.L.kv.n_kv_heads <= P.L.num_sms && items <= MAX_PIECE_ITEMS;
   CUtensorMap mk, mv;
   if (!pool_map(&mk, P.L.kv, P.L.kv.k, P.L.layer, P.box) || !pool_map(&mv, P.L.kv, P.L.kv.v, P.L.layer, P.box))
     return cudaErrorInvalidValue;
-  cudaError_t err = cudaFuncSetAttribute(attend_kernel<T, D, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  cudaError_t err = cudaFuncSetAttribute(attend_kernel<T, D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (err != cudaSuccess) return err;
-  err = launch_pdl(attend_kernel<T, D, NH>, dim3(P.L.num_sms), dim3(Y::THREADS), SMEM, stream, P, mk, mv);
+  err = launch_pdl(attend_kernel<T, D, PAIR>, dim3(P.L.num_sms), dim3(THREADS), SMEM, stream, P, mk, mv);
   if (err != cudaSuccess) return err;
   return launch_pdl(attend_join_kernel<T, D>, dim3(P.L.num_sms, (P.ws_rows * (D / 8) + JOIN_THREADS - 1) / JOIN_THREADS),
                     dim3(JOIN_THREADS), 0, stream, P);
@@ -874,7 +1064,7 @@ cudaError_t attend(Plan& P, cudaStream_t stream) {
 
 template <typename T, int D>
 cudaError_t attend_rows(Plan& P, cudaStream_t stream) {
-  return P.rows > TILE ? attend<T, D, 2>(P, stream) : attend<T, D, 1>(P, stream);
+  return P.rows > TILE ? attend<T, D, false>(P, stream) : attend<T, D, true>(P, stream);
 }
 
 int workspace_rows(int64_t rows) { return static_cast<int>(min64(rows, 2 * TILE)); }
@@ -897,7 +1087,7 @@ cudaError_t launch_attend(const AttendLaunch& L, cudaStream_t stream) {
   // a scale of zero would turn -inf into NaN: weights 2^(1e-30 S) are all one as well
   P.scale2 = fminf(fmaxf(fabsf(L.scale) * 1.4426950408889634f, 1e-30f), 3e38f);
   P.negative = L.scale < 0.0f;
-  P.group_inv = P.group == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + P.group - 1) / P.group);
+  P.group_inv = P.group == 1 ? 0 : UINT64_MAX / P.group + 1;
   if (L.kv.dtype == SPEC_TREE_BF16)
     return L.kv.head_dim == 128 ? attend_rows<__nv_bfloat16, 128>(P, stream) : attend_rows<__nv_bfloat16, 64>(P, stream);
   return L.kv.head_dim == 128 ? attend_rows<__half, 128>(P, stream) : attend_rows<__half, 64>(P, stream);

@@ -252,6 +252,25 @@ def test_attention_on_another_stream_and_in_a_graph():
         assert torch.equal(out.cpu(), _run_attend(c2, q)[0])
 
 
+@pytest.mark.parametrize("N,Hq,Hkv,D,begin", [(8, 16, 4, 64, 25), (1, 32, 8, 128, 0), (61, 8, 8, 128, 0), (61, 8, 2, 128, 0)])
+def test_ragged_batch_many_times(N, Hq, Hkv, D, begin):
+    """Warps whose lanes are partly nodes that do not exist, segments of every length: a hundred launches of a
+    ragged batch all end, in time and with the same bits."""
+    rng = np.random.RandomState(1)
+    lens = rng.randint(1, 900, 40).tolist()
+    counts = [begin + int(rng.randint(0, N + 1)) for _ in lens]
+    c = kv_cases.make(47, lens, N, Hkv, D, 32, begin=begin, counts=counts, stale=float("nan"), tree=N > 1)
+    q = _queries(48, c, Hq)
+    cache, qd, ws, status, nodes = _cache(c), q.cuda(), B.AttendWorkspace(40, N, Hq, Hkv, D), _status(), _nodes(c)
+    outs = [torch.zeros_like(qd) for _ in range(4)]
+    for rep in range(25):
+        for out in outs:
+            B.spec_tree_attend(cache, 0, qd, out, ws, status, tree=nodes, node_begin=begin)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and all(torch.equal(outs[0], o) for o in outs)
+    _check_attend(c, q)
+
+
 def test_pages_past_32_bit_offsets():
     """A pool of more than 2^32 elements: the pages used lie at its end."""
     page, Hkv, D = 64, 4, 128
