@@ -22,7 +22,10 @@
 //     below a range's length and two.
 // An item that one CTA has whole is finished there; otherwise each CTA leaves
 // its sums, their reference and its unnormalised output in the workspace, and
-// the parts are put together in order.
+// the parts are put together in the item's order: by attend_join_kernel, or,
+// for calls of up to 16 rows, by whichever CTA is the last to leave its part
+// (a launch less: @@; of many rows the join is long for one warp,
+// and the launch, over all SMs, is faster).
 //
 // Tile.  S = Q K^T in tensor memory (128 lanes: one row per softmax thread);
 // weights w = 2^(scale S - ref), rounded to the cache's type and stored over
@@ -38,6 +41,8 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <algorithm>
+#include <atomic>
 #include <mutex>
 #include <type_traits>
 
@@ -58,7 +63,11 @@ constexpr int THREADS = 3 * TILE;               // two softmax warpgroups and on
 constexpr int HELPERS = 2 * TILE / 32;          // the helpers' first warp
 constexpr int COLUMNS = 512;                    // tensor memory: S of both halves, then O of both
 constexpr int MAX_PIECE_ITEMS = 256;            // (tree, rows) of calls that may be dealt in pieces
-constexpr int SEGMENT_COST = 3;                 // fixed cost of a segment, in tiles
+constexpr int JOIN_INSIDE_ROWS = 16;            // rows of calls that need no join kernel
+// Weights are handed to the product in two parts: the last 32 are made while
+// the product works on the first 96, so it does not wait in between (two parts
+// of 64 left a gap: 2920 against 2500 cycles a tile of 256 rows).
+constexpr int EARLY = 96;
 
 struct Plan {
   AttendLaunch L;
@@ -67,23 +76,27 @@ struct Plan {
   float scale2;        // |scale| log2(e)
   bool may_piece;      // no more items than CTAs
   bool negative;       // scale < 0: the products take -Q
+  bool join_inside;    // no join kernel
+  int q_box;           // nodes of a tiled copy of queries, 0: they are copied row by row
 };
 
-// What a range has left in the workspace for the item it ends in, when others
-// continue it: the join starts from there.
+// Parts of items: slot 0 of a CTA for one that began before it, slot 1 for one
+// that goes on after it.
 struct JoinRecord {
-  int32_t pieces, b, row0, head;
+  int32_t parts, b, row0, head;
 };
 
 struct Workspace {
-  JoinRecord* records;  // [CTA]
-  float2* sums;         // [CTA][2][ws_rows]: (reference, sum)
-  float4* out;          // [CTA][2][D / 4][ws_rows]: neighbouring rows are neighbours in memory
+  uint32_t* arrived;    // [CTA where the item begins]: parts left; zero between calls
+  JoinRecord* records;  // [CTA]: the item that begins there and goes on after it
+  float2* sums;       // [CTA][2][ws_rows]: (reference, sum)
+  float4* out;        // [CTA][2][D / 4][ws_rows]: neighbouring rows are neighbours in memory
 };
 
 __host__ __device__ inline Workspace workspace_of(void* ws, int num_sms, int ws_rows) {
   Workspace w;
-  w.records = static_cast<JoinRecord*>(ws);
+  w.arrived = static_cast<uint32_t*>(ws);
+  w.records = reinterpret_cast<JoinRecord*>(w.arrived + (num_sms + 3) / 4 * 4);
   w.sums = reinterpret_cast<float2*>(w.records + num_sms);
   w.out = reinterpret_cast<float4*>(w.sums + static_cast<size_t>(num_sms) * 2 * ws_rows);
   return w;
@@ -99,13 +112,13 @@ struct Layout {
 };
 
 struct Control {
-  uint64_t full[MAX_STAGES], empty[MAX_STAGES];
-  uint64_t q_full, q_empty, v_full, v_clean, s_full[2], w_full[2][2], o_full[2], drain;
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES], clean[MAX_STAGES];
+  uint64_t q_full, q_empty, s_full[2], w_full[2][2], o_full[2], drain;
   uint32_t tmem;
   int abort;
   int64_t scan[THREADS / 32];
   int64_t total, from, to;  // tiles of the call, and this CTA's range or piece of them
-  int pieces;               // pieces of this CTA's item, 0: ranges
+  int pieces, piece;        // pieces of this CTA's item (0: ranges), and which one this is
   int b, rt, head, at;      // where this CTA begins
   uint32_t odd[3][MASKED_TILES * (TILE / 32)];  // tokens with a value that is not finite, by segment modulo 3
   uint8_t up[2][SPEC_TREE_MAX_NODES];           // node minus parent, by segment modulo 2; 0: none, 255: more
@@ -120,6 +133,7 @@ struct Segment {
   int b, head, row0;     // row0: first row of the item
   int len, cnt;          // committed tokens, nodes that exist
   int first, last, tiles;  // tiles first .. last - 1 of `tiles`
+  int64_t begin;         // where the item begins among all tiles (ranges)
   int end;               // tokens (slots) the item reads
   int clear;             // slots below this one are seen by every row of the item
 };
@@ -150,21 +164,23 @@ __device__ __forceinline__ void item_tiles(const Plan& P, int len, int cnt, int 
   tiles = end > 0 ? (end + TILE - 1) / TILE : 1;
 }
 
+// Tiles of one key head of item group x: tree x / row_tiles, rows x % row_tiles.
 template <int ROWS>
-__device__ __forceinline__ int64_t tree_tiles(const Plan& P, int b) {
-  int len, cnt;
+__device__ __forceinline__ int group_tiles(const Plan& P, int x) {
+  const int b = P.row_tiles == 1 ? x : x / P.row_tiles;
+  int len, cnt, end, tiles;
   tree_of(P, b, len, cnt);
-  int64_t sum = 0;
-#pragma unroll 1
-  for (int rt = 0; rt < P.row_tiles; ++rt) {
-    int end, tiles;
-    item_tiles<ROWS>(P, len, cnt, rt, end, tiles);
-    sum += tiles;
-  }
-  return sum * P.L.kv.n_kv_heads;
+  item_tiles<ROWS>(P, len, cnt, x - b * P.row_tiles, end, tiles);
+  return tiles;
 }
 
 __device__ __forceinline__ int64_t range_start(int64_t total, int c, int ctas) { return total * c / ctas; }
+
+// The CTA whose range holds tile `at`.
+__device__ __forceinline__ int range_of(int64_t total, int64_t at, int ctas) {
+  const int c = static_cast<int>(at * ctas / total);
+  return range_start(total, c + 1, ctas) <= at ? c + 1 : c;
+}
 
 // The segments of a CTA's range, one after the other; every role walks them
 // for itself.
@@ -184,7 +200,7 @@ struct Walk {
     tree_of(P, b, len, cnt);
   }
 
-  __device__ __forceinline__ bool next(const Plan& P, Segment& s) {
+  __device__ __forceinline__ bool next(const Plan& P, const Control& C, Segment& s) {
     if (left <= 0) return false;
     s.b = b;
     s.head = head;
@@ -196,6 +212,7 @@ struct Walk {
     s.first = at;
     const int64_t n = min64(left, s.tiles - at);
     s.last = at + static_cast<int>(n);
+    s.begin = C.to - left - at;
     left -= n;
     at = 0;
     if (s.last == s.tiles && ++head == P.L.kv.n_kv_heads) {
@@ -299,7 +316,7 @@ __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* mk, 
   walk.begin(P, C);
   Segment s;
   uint32_t n = 0;  // loads so far
-  while (walk.next(P, s)) {
+  while (walk.next(P, C, s)) {
     const int32_t* table = P.L.kv.page_table + static_cast<int64_t>(s.b) * P.L.kv.table_stride;
     auto entry = [&](int t) {  // the page of this lane's copy of tile t
       const int slot = t * TILE + lane * P.box;
@@ -356,59 +373,70 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
   Segment s = {};
   uint32_t n = 0, segment = 0;   // loads, segments so far
   uint32_t parity = 0;           // bit h: parity of half h's next weights
-  uint32_t cleaned = 0;          // tiles whose values were cleaned so far
+  uint32_t clean = 0;            // bit i: parity of slot i's next cleaning
 
+  auto issue_scores = [&](uint32_t to, uint32_t a, uint32_t b, uint64_t* bar) {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const int at = (k / 4) * PANEL16 + (k % 4) * 2;
+      mma_ss(to, smem_descriptor(a + at), smem_descriptor(b + at), id_s, k > 0);
+    }
+    mma_commit(bar);
+  };
   auto ready = [&](uint32_t load) { return warp_wait(&C.full[load % Y::STAGES], (load / Y::STAGES) & 1, C, status); };
   // S of half h from the keys of a load
   auto scores = [&](int h, uint32_t load) {
     const uint32_t a = uniform(q_low + (PAIR ? 0 : h * KV16)), b = uniform(k_low + load % Y::STAGES * KV16);
     const uint32_t to = uniform(tmem + h * TILE);
-    if (elect()) {
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const int at = (k / 4) * PANEL16 + (k % 4) * 2;
-        mma_ss(to, smem_descriptor(a + at), smem_descriptor(b + at), id_s, k > 0);
-      }
-      mma_commit(&C.s_full[h]);
-    }
+    if (elect()) issue_scores(to, a, b, &C.s_full[h]);
     __syncwarp();
   };
   auto give_back = [&](uint64_t* bar) {
     if (elect()) mma_commit(bar);
     __syncwarp();
   };
-  // O of half h from the values of a load, as the weights' two parts come
-  auto output = [&](int h, uint32_t load, bool first, bool last) {
-    const uint32_t b = uniform(v_low + load % Y::STAGES * KV16), add = uniform(!first);
-#pragma unroll 1
-    for (int part = 0; part < 2; ++part) {
-      if (!warp_wait(&C.w_full[h][part], (parity >> h) & 1, C, status)) return false;
-      tmem_fence_after();
-      const uint32_t to = uniform(tmem + 2 * TILE + h * D), from = uniform(tmem + h * TILE + part * (TILE / 4));
-      const uint32_t low = uniform(b + part * (64 * 128 / 16));
-      if (elect()) {
+  // O of half h from the values of a load, as the weights' two parts come, and,
+  // unless PAIR, right behind it S of its next tile from the keys of load k
+  // (which are then there; k = 0: none)
+  auto output = [&](int h, uint32_t load, bool first, uint32_t k) {
+    const uint32_t b = uniform(v_low + load % Y::STAGES * KV16), add = uniform(!first), more = uniform(k);
+    const uint32_t to = uniform(tmem + 2 * TILE + h * D), from = uniform(tmem + h * TILE);
+    const uint32_t qa = uniform(q_low + (PAIR ? 0 : h * KV16)), kb = uniform(k_low + k % Y::STAGES * KV16);
+    if (!warp_wait(&C.w_full[h][0], (parity >> h) & 1, C, status)) return false;
+    tmem_fence_after();
+    if (elect()) {
 #pragma unroll
-        for (int k = 0; k < TILE / 32; ++k)
-          mma_ts(to, from + k * 8, smem_descriptor(low + k * (16 * 128 / 16)), ID_O, k > 0 || part || add);
-        if (part == 1 && last) mma_commit(&C.o_full[h]);
-      }
-      __syncwarp();
+      for (int x = 0; x < EARLY / 16; ++x)
+        mma_ts(to, from + x * 8, smem_descriptor(b + x * (16 * 128 / 16)), ID_O, x > 0 || add);
     }
+    __syncwarp();
+    if (!warp_wait(&C.w_full[h][1], (parity >> h) & 1, C, status)) return false;
+    tmem_fence_after();
+    if (elect()) {
+#pragma unroll
+      for (int x = EARLY / 16; x < TILE / 16; ++x)
+        mma_ts(to, from + x * 8, smem_descriptor(b + x * (16 * 128 / 16)), ID_O, true);
+      if (!more)
+        mma_commit(&C.o_full[h]);
+      else if (!PAIR)
+        issue_scores(from, qa, kb, &C.s_full[h]);
+    }
+    __syncwarp();
     parity ^= 1u << h;
     return true;
   };
-  // values of tile t, cleaned where not every row sees it whole: the side
-  // warps are told when they are there, as they do not follow the ring's phases
+  // values of tile t, cleaned where not every row sees it whole
   auto values = [&](int t, uint32_t load) {
+    const uint32_t vs = load % Y::STAGES;
     if (!ready(load)) return false;
     if ((t + 1) * TILE > s.clear) {
-      warp_arrive(&C.v_full);
-      if (!warp_wait(&C.v_clean, cleaned++ & 1, C, status)) return false;
+      if (!warp_wait(&C.clean[vs], (clean >> vs) & 1, C, status)) return false;
+      clean ^= 1u << vs;
     }
     return true;
   };
 
-  while (walk.next(P, s)) {
+  while (walk.next(P, C, s)) {
     const int count = s.last - s.first;
     if (!warp_wait(&C.q_full, segment & 1, C, status) || !ready(n)) return false;
     tmem_fence_after();
@@ -426,7 +454,7 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
       for (int x = 0; x < count; ++x) {
         const uint32_t v = n + 2 * x + 1, k = n + 2 * (x + 2);
         const bool more = x + 2 < count;
-        if (!values(s.first + x, v) || !output(x & 1, v, x < 2, !more)) return false;
+        if (!values(s.first + x, v) || !output(x & 1, v, x < 2, more ? k : 0)) return false;
         give_back(&C.empty[v % Y::STAGES]);
         if (more) {
           if (!ready(k)) return false;
@@ -441,21 +469,13 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
       for (int x = 0; x < count; ++x) {
         const uint32_t v = n + 2 * x + 1, k = v + 1;
         const bool more = x + 1 < count;
-        if (!values(s.first + x, v)) return false;
+        if (!values(s.first + x, v) || (more && !ready(k))) return false;
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          if (!output(h, v, x == 0, !more)) return false;
-          if (more) {
-            if (h == 0 && !ready(k)) return false;
-            tmem_fence_after();
-            scores(h, k);
-          }
-        }
+        for (int h = 0; h < 2; ++h)
+          if (!output(h, v, x == 0, more ? k : 0)) return false;
         give_back(&C.empty[v % Y::STAGES]);
-        if (more) {
-          give_back(&C.empty[k % Y::STAGES]);
-          if (x + 2 == count) give_back(&C.q_empty);
-        }
+        if (more) give_back(&C.empty[k % Y::STAGES]);
+        if (x + 2 == count) give_back(&C.q_empty);
       }
     }
     n += 2 * count;
@@ -464,95 +484,127 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
   return true;
 }
 
+// Whether a 128-byte row holds an infinity or a NaN: those times zero are NaN.
+// Neighbouring threads start at different chunks, as their rows share banks.
+template <typename T>
+__device__ __forceinline__ bool any_odd(const uint4* row, int rotate) {
+  auto acc = Pair<T>::pair(0);
+  const auto zero = acc;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint4 x = row[c ^ rotate];
+    acc = __hfma2(Pair<T>::pair(x.x), zero, acc);
+    acc = __hfma2(Pair<T>::pair(x.y), zero, acc);
+    acc = __hfma2(Pair<T>::pair(x.z), zero, acc);
+    acc = __hfma2(Pair<T>::pair(x.w), zero, acc);
+  }
+  return isnan(__low2float(acc)) || isnan(__high2float(acc));
+}
+
 // Two warps, ahead of the softmax: an item's queries and its nodes' parents
 // into shared memory, and the values of tiles that not every row sees whole:
-// those past the item's end and those that are not finite become zeros.
+// those past the item's end and those that are not finite become zeros.  They
+// pass every slot of the ring, so that their waits keep to its phases.
 template <typename T, int D, bool PAIR>
-__device__ __forceinline__ void side_role(const Plan& P, Control& C, uint32_t q_smem, uint8_t* ring) {
+__device__ __forceinline__ void side_role(const Plan& P, const CUtensorMap* mq, Control& C, uint32_t q_smem, uint8_t* ring) {
   using Y = Layout<D, PAIR>;
   constexpr int CHUNKS = D / 8, SIDE = 64, STEP = SIDE / CHUNKS;
   const int t = threadIdx.x % SIDE;
   uint32_t* status = P.L.status;
-  // what STEP rows on means in nodes and heads
-  const int step_i = node_of_row(P, STEP), step_g = STEP - step_i * P.group;
-  const int64_t step = step_i * P.L.q.node_stride + step_g * P.L.q.head_stride;
-  const int64_t wrap = P.L.q.node_stride - P.group * P.L.q.head_stride;
   Walk<Y::ROWS> walk;
   walk.begin(P, C);
   Segment s;
-  uint32_t segment = 0, tile = 0, cleaned = 0;
-  for (; walk.next(P, s); ++segment, tile += s.last - s.first) {
+  uint32_t segment = 0, n = 0;  // segments, loads so far
+  for (; walk.next(P, C, s); ++segment) {
     if (!warp_wait(&C.q_empty, (segment & 1) ^ 1, C, status)) return;
-    const int n = min(Y::ROWS, P.rows - s.row0), ch = t % CHUNKS;
-    const int row = s.row0 + t / CHUNKS;
-    int i = node_of_row(P, row), g = row - i * P.group;
-    const int nodes = s.cnt - P.L.nodes.begin;  // rows of later nodes are zeros
-    const T* base = static_cast<const T*>(P.L.q.data) + s.b * P.L.q.tree_stride +
-                    static_cast<int64_t>(s.head) * P.group * P.L.q.head_stride + ch * 8;
-    const T* from = base + i * P.L.q.node_stride + g * P.L.q.head_stride;
-    const uint32_t to = q_smem + (ch / 8) * PANEL_BYTES;
+    if (P.q_box) {
+      if (t == 0) {
+        const int node = node_of_row(P, s.row0);
+        mbar_expect_more(&C.q_full, (Y::ROWS / TILE) * Y::PANELS * P.q_box * P.group * 128);
+        for (int h = 0; h < Y::ROWS / TILE; ++h)
+          for (int p = 0; p < Y::PANELS; ++p)
+            tile_g2s(q_smem + h * Y::KV_BYTES + p * PANEL_BYTES, mq, p * PANEL, s.head * P.group, node + h * node_of_row(P, TILE),
+                     s.b, &C.q_full);
+      }
+      __syncwarp();
+    } else {
+      // what STEP rows on means in nodes and heads
+      const int step_i = node_of_row(P, STEP), step_g = STEP - step_i * P.group;
+      const int64_t step = step_i * P.L.q.node_stride + step_g * P.L.q.head_stride;
+      const int64_t wrap = P.L.q.node_stride - P.group * P.L.q.head_stride;
+      const int rows = min(Y::ROWS, P.rows - s.row0), ch = t % CHUNKS, row = s.row0 + t / CHUNKS;
+      int i = node_of_row(P, row), g = row - i * P.group;
+      const int nodes = s.cnt - P.L.nodes.begin;  // rows of later nodes are zeros
+      const T* base = static_cast<const T*>(P.L.q.data) + s.b * P.L.q.tree_stride +
+                      static_cast<int64_t>(s.head) * P.group * P.L.q.head_stride + ch * 8;
+      const T* from = base + i * P.L.q.node_stride + g * P.L.q.head_stride;
+      const uint32_t to = q_smem + (ch / 8) * PANEL_BYTES;
 #pragma unroll 2
-    for (int r = t / CHUNKS; r < n; r += STEP) {
-      const bool live = i < nodes;
-      async_copy16(to + (r / TILE) * Y::KV_BYTES + (r % TILE) * 128 + (((ch % 8) ^ (r % 8)) * 16), live ? from : base, !live);
-      i += step_i;
-      g += step_g;
-      from += step;
-      if (g >= P.group) {
-        g -= P.group;
-        ++i;
-        from += wrap;
+      for (int r = t / CHUNKS; r < rows; r += STEP) {
+        const bool live = i < nodes;
+        async_copy16(to + (r / TILE) * Y::KV_BYTES + (r % TILE) * 128 + (((ch % 8) ^ (r % 8)) * 16), live ? from : base, !live);
+        i += step_i;
+        g += step_g;
+        from += step;
+        if (g >= P.group) {
+          g -= P.group;
+          ++i;
+          from += wrap;
+        }
       }
     }
     if (P.L.nodes.parent) {
       const int32_t* parent = P.L.nodes.parent + static_cast<int64_t>(s.b) * P.L.nodes.stride;
 #pragma unroll 2
-      for (int n = t; n < s.cnt; n += SIDE) {
-        const int up = parent[n];
-        C.up[segment % 2][n] = static_cast<uint8_t>(up < 0 || up >= n ? 0 : min(n - up, 255));
-        if (up >= n) set_status(status, SPEC_TREE_S_NODES);
+      for (int x = t; x < s.cnt; x += SIDE) {
+        const int up = parent[x];
+        C.up[segment % 2][x] = static_cast<uint8_t>(up < 0 || up >= x ? 0 : min(x - up, 255));
+        if (up >= x) set_status(status, SPEC_TREE_S_NODES);
       }
     }
-    async_copies_wait();
-    fence_proxy_async_smem();
+    if (!P.q_box) {
+      async_copies_wait();
+      fence_proxy_async_smem();
+    }
     warp_arrive(&C.q_full);
 
     const int first_masked = s.clear / TILE;
-    for (int j = max(s.first, first_masked); j < s.last; ++j) {
-      const uint32_t v = 2 * (tile + j - s.first) + 1;
-      if (!warp_wait(&C.v_full, cleaned++ & 1, C, status)) return;
-      if (!warp_wait(&C.full[v % Y::STAGES], (v / Y::STAGES) & 1, C, status)) return;
+    for (int j = s.first; j < s.last; ++j) {
 #pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        const int row = part * 64 + t;  // a token
-        uint8_t* at = ring + (v % Y::STAGES) * Y::KV_BYTES + row * 128;
-        const bool past = j * TILE + row >= s.end;
-        bool odd = false;
+      for (int kv = 0; kv < 2; ++kv, ++n) {
+        const int slot = n % Y::STAGES;
+        if (!warp_wait(&C.full[slot], (n / Y::STAGES) & 1, C, status)) return;
+        if (kv == 1 && j >= first_masked) {
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {
+            const int row = part * 64 + t;  // a token
+            uint8_t* at = ring + slot * Y::KV_BYTES + row * 128;
+            bool odd = false;
+            if (j * TILE + row >= s.end) {
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-          uint4* w4 = reinterpret_cast<uint4*>(at + (c / 8) * PANEL_BYTES + (((c % 8) ^ (row % 8)) * 16));
-          if (past) {
-            *w4 = make_uint4(0, 0, 0, 0);
-          } else {
-            const uint4 x = *w4;
-            uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            bool hit = false;
+              for (int c = 0; c < CHUNKS; ++c)
+                *reinterpret_cast<uint4*>(at + (c / 8) * PANEL_BYTES + ((c ^ t) % 8) * 16) = make_uint4(0, 0, 0, 0);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const bool lo = odd16<T>(w[e]), hi = odd16<T>(w[e] >> 16);
-              if (lo) w[e] &= 0xffff0000u;
-              if (hi) w[e] &= 0x0000ffffu;
-              hit |= lo || hi;
+              for (int p = 0; p < Y::PANELS; ++p)
+                odd |= any_odd<T>(reinterpret_cast<const uint4*>(at + p * PANEL_BYTES), t % 8);
             }
-            if (hit) *w4 = make_uint4(w[0], w[1], w[2], w[3]);
-            odd |= hit;
+            const uint32_t word = __ballot_sync(FULL, odd);
+            if (odd) {
+#pragma unroll 1
+              for (int c = 0; c < CHUNKS * 4; ++c) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(at + (c / 32) * PANEL_BYTES) + c % 32;
+                if (odd16<T>(*w)) *w &= 0xffff0000u;
+                if (odd16<T>(*w >> 16)) *w &= 0x0000ffffu;
+              }
+            }
+            if (t % 32 == 0) C.odd[segment % 3][(j - first_masked) * (TILE / 32) + part * 2 + t / 32] = word;
           }
+          fence_proxy_async_smem();
+          warp_arrive(&C.clean[slot]);
         }
-        const uint32_t word = __ballot_sync(FULL, odd);
-        if (t % 32 == 0) C.odd[segment % 3][(j - first_masked) * (TILE / 32) + part * 2 + t / 32] = word;
+        warp_arrive(&C.empty[slot]);
       }
-      fence_proxy_async_smem();
-      warp_arrive(&C.v_clean);
     }
   }
 }
@@ -587,6 +639,68 @@ __device__ __noinline__ void add_odd(const Plan& P, const Segment& s, const uint
   }
 }
 
+// Rows of an item from its parts, which the CTAs from `from` on have left:
+// thread x of `threads` (a power of two) takes 16 bytes at a time of the parts.
+template <typename T, int D>
+__device__ __forceinline__ void join_rows(const Plan& P, const Workspace& ws, const JoinRecord& rec, int cnt, int from,
+                                          int x, int threads) {
+  const int rows = min(P.ws_rows, P.rows - rec.row0);
+  // a thread keeps to one row; neighbours have neighbouring rows
+  int spread = 1;
+  while (spread < rows && spread < threads) spread *= 2;
+  const int local = x % spread, row = rec.row0 + local;
+  if (local >= rows) return;
+  const int i = node_of_row(P, row), g = row - i * P.group;
+  const bool live = P.L.nodes.begin + i < cnt;
+  // part p: slot 1 of the first CTA, slot 0 of the next ones
+  auto slot = [&](int p) { return static_cast<int64_t>(from + p) * 2 + (p == 0 ? 1 : 0); };
+  float top = -INFINITY, sum = 0.0f;
+  if (live) {
+#pragma unroll 4
+    for (int p = 0; p < rec.parts; ++p) top = fmaxf(top, __ldcg(&ws.sums[slot(p) * P.ws_rows + local].x));
+  }
+  const float sub = top == -INFINITY ? 0.0f : top;
+  if (live) {
+#pragma unroll 4
+    for (int p = 0; p < rec.parts; ++p) {
+      const float2 ms = __ldcg(&ws.sums[slot(p) * P.ws_rows + local]);
+      sum += ms.y * ex2(ms.x - sub);
+    }
+  }
+  const bool some = live && sum != 0.0f;
+  const float inv = some ? 1.0f / sum : 0.0f;
+  T* out = static_cast<T*>(P.L.out.data) + rec.b * P.L.out.tree_stride + i * P.L.out.node_stride +
+           (static_cast<int64_t>(rec.head) * P.group + g) * P.L.out.head_stride;
+  constexpr int BATCH = 4;
+  const int step = threads / spread;
+#pragma unroll 1
+  for (int q0 = x / spread; q0 < D / 4; q0 += BATCH * step) {
+    float4 acc[BATCH];
+#pragma unroll
+    for (int e = 0; e < BATCH; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (some) {
+#pragma unroll 4
+      for (int p = 0; p < rec.parts; ++p) {
+        const float f = ex2(__ldcg(&ws.sums[slot(p) * P.ws_rows + local].x) - sub);
+        const float4* part = ws.out + slot(p) * (D / 4) * P.ws_rows + local;
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) {
+          const int q = q0 + e * step;
+          const float4 y = q < D / 4 ? __ldcg(part + q * P.ws_rows) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          acc[e].x += y.x * f, acc[e].y += y.y * f, acc[e].z += y.z * f, acc[e].w += y.w * f;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < BATCH; ++e) {
+      const int q = q0 + e * step;
+      if (q < D / 4)
+        *reinterpret_cast<uint2*>(out + q * 4) = make_uint2(Pair<T>::pack(acc[e].x * inv, acc[e].y * inv),
+                                                            Pair<T>::pack(acc[e].z * inv, acc[e].w * inv));
+    }
+  }
+}
+
 // 128 threads, one row each: weights, the running reference and sum, and the
 // output.
 template <typename T, int D, bool PAIR>
@@ -594,7 +708,7 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
   using Y = Layout<D, PAIR>;
   constexpr int EACH = PAIR ? 2 : 1;  // a half takes every tile, or every other one
   constexpr float SHIFT = std::is_same<T, __half>::value ? 7.0f : 0.0f;
-  const int t = threadIdx.x % TILE, warp = t / 32;
+  const int t = threadIdx.x % TILE, warp = t / 32, lane = t % 32;
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
   const uint32_t tm_s = C.tmem + half * TILE + lanes, tm_o = C.tmem + 2 * TILE + half * D + lanes;
   uint32_t* status = P.L.status;
@@ -603,7 +717,7 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
   Segment s;
   uint32_t tile = 0, segment = 0, ends = 0;  // tiles of this half, segments, segments with a tile of this half so far
   bool ok = true;  // uniform over the warp; a warp that has given up still meets the others at barriers
-  for (; walk.next(P, s); ++segment) {
+  for (; walk.next(P, C, s); ++segment) {
     const int local = (PAIR ? 0 : half * TILE) + t, row = s.row0 + local;
     const int i = node_of_row(P, row), g = row - i * P.group;
     const int node = P.L.nodes.begin + i;
@@ -671,22 +785,26 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
         F2 part[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) part[c] = F2(0.0f, 0.0f);
+        auto weigh = [&](int c) {
+          float a, b;
+          fma2(F2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, shift2).get(a, b);
+          a = ex2(a);
+          b = ex2(b);
+          part[c / 2 % 4] = add2(part[c / 2 % 4], F2(a, b));
+          x[c / 2] = Pair<T>::pack(a, b);
+        };
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {  // the product starts on the first half of the weights
+        for (int c = 0; c < EARLY; c += 2) weigh(c);
+        tmem_st32(tm_s, x);
+        tmem_st16(tm_s + 32, x + 32);
+        tmem_wait_st();
+        tmem_fence_before();
+        warp_arrive(&C.w_full[half][0]);
 #pragma unroll
-          for (int c = p * TILE / 2; c < (p + 1) * TILE / 2; c += 2) {
-            float a, b;
-            fma2(F2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, shift2).get(a, b);
-            a = ex2(a);
-            b = ex2(b);
-            part[c / 2 % 4] = add2(part[c / 2 % 4], F2(a, b));
-            x[c / 2] = Pair<T>::pack(a, b);
-          }
-          tmem_st32(tm_s + p * 32, x + p * 32);
-          tmem_wait_st();
-          tmem_fence_before();
-          if (p == 0) warp_arrive(&C.w_full[half][0]);
-        }
+        for (int c = EARLY; c < TILE; c += 2) weigh(c);
+        tmem_st16(tm_s + EARLY / 2, x + EARLY / 2);
+        tmem_wait_st();
+        tmem_fence_before();
         float a, b;
         add2(add2(part[0], part[1]), add2(part[2], part[3])).get(a, b);
         sum += a + b;
@@ -777,24 +895,42 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
     if (!whole && live) ws.sums[part * P.ws_rows + local] = make_float2(ref, sum);
     tmem_fence_before();
     if (both) warps_meet(5 + warp, 64);
-    if (!whole && s.first == 0 && local == 0) {
-      int pieces = C.pieces;
-      if (pieces == 0) {  // the CTAs after this one whose ranges begin inside the item
-        const int64_t end = C.to + (s.tiles - s.last);
-        for (pieces = 1; cta + pieces < ctas && range_start(C.total, cta + pieces, ctas) < end;) ++pieces;
+    if (!whole && local < 32 && (P.join_inside || s.first == 0)) {  // one warp
+      int from, parts;
+      if (C.pieces) {
+        from = cta - C.piece;
+        parts = C.pieces;
+      } else {
+        from = s.first == 0 ? cta : range_of(C.total, s.begin, ctas);
+        parts = (s.last == s.tiles ? cta : range_of(C.total, s.begin + s.tiles - 1, ctas)) - from + 1;
       }
-      ws.records[cta] = JoinRecord{pieces, s.b, s.row0, s.head};
+      if (P.join_inside) {
+        __threadfence();
+        __syncwarp();
+        uint32_t before = 0;
+        if (lane == 0) before = atomicAdd(&ws.arrived[from], 1);
+        if (__shfl_sync(FULL, before, 0) + 1 == static_cast<uint32_t>(parts)) {
+          if (lane == 0) ws.arrived[from] = 0;
+          __threadfence();
+          join_rows<T, D>(P, ws, JoinRecord{parts, s.b, s.row0, s.head}, s.cnt, from, lane, 32);
+          __syncwarp();
+        }
+      } else if (lane == 0) {
+        ws.records[cta] = JoinRecord{parts, s.b, s.row0, s.head};
+      }
     }
   }
 }
 
-// Where this CTA's range begins: a scan of the trees' tiles over all threads.
+// Where this CTA's range begins: a scan of all items' tiles over all threads.
 template <int ROWS>
 __device__ __forceinline__ void find_range(const Plan& P, Control& C, int warp, int cta) {
-  const int B = P.L.B, per = (B + THREADS - 1) / THREADS;
-  const int b0 = min(B, static_cast<int>(threadIdx.x) * per), b1 = min(B, b0 + per);
+  const int groups = P.L.B * P.row_tiles, per = (groups + THREADS - 1) / THREADS, heads = P.L.kv.n_kv_heads;
+  const int x0 = min(groups, static_cast<int>(threadIdx.x) * per), x1 = min(groups, x0 + per);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += tree_tiles<ROWS>(P, b);
+#pragma unroll 1
+  for (int x = x0; x < x1; ++x) mine += group_tiles<ROWS>(P, x);
+  mine *= heads;
   int64_t before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -804,6 +940,7 @@ __device__ __forceinline__ void find_range(const Plan& P, Control& C, int warp, 
   if (threadIdx.x % 32 == 31) C.scan[warp] = before;
   __syncthreads();
   int64_t total = 0;
+#pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += C.scan[w];
     total += C.scan[w];
@@ -819,43 +956,35 @@ __device__ __forceinline__ void find_range(const Plan& P, Control& C, int warp, 
   }
   if (from < to && before <= from && from < before + mine) {
     int64_t skip = from - before;
-    int b = b0;
-    for (int64_t n; skip >= (n = tree_tiles<ROWS>(P, b)); ++b) skip -= n;
-    int len, cnt;
-    tree_of(P, b, len, cnt);
-    for (int rt = 0;; ++rt) {
-      int end, tiles;
-      item_tiles<ROWS>(P, len, cnt, rt, end, tiles);
-      const int64_t all = static_cast<int64_t>(tiles) * P.L.kv.n_kv_heads;
-      if (skip < all) {
-        C.b = b;
-        C.rt = rt;
-        C.head = static_cast<int>(skip / tiles);
-        C.at = static_cast<int>(skip % tiles);
-        break;
-      }
-      skip -= all;
+    int x = x0, tiles;
+    while (skip >= static_cast<int64_t>(tiles = group_tiles<ROWS>(P, x)) * heads) {
+      skip -= static_cast<int64_t>(tiles) * heads;
+      ++x;
     }
+    C.b = x / P.row_tiles;
+    C.rt = x % P.row_tiles;
+    C.head = static_cast<int>(skip / tiles);
+    C.at = static_cast<int>(skip % tiles);
   }
 }
+
+// In tiles of 128 rows (a tile of 256 counts for two): what leaving and joining
+// parts costs, and the second segment that a range has.
+constexpr float JOIN_COST = 6.0f, ENDS_COST = 4.0f;
 
 // Pieces of an item of `tiles` tiles when a piece is to have about 1 / inv.
 __device__ __forceinline__ int pieces_of(int tiles, float inv) {
   return max(1, min(tiles, static_cast<int>(ceilf(tiles * inv - 0.001f))));
 }
 
-// For no more items than CTAs: the least length of equal pieces for which
-// there are CTAs enough (one lane tries one of 32 lengths), and this CTA's
-// piece.  False: ranges are better.
-template <int ROWS>
+// For no more items than CTAs: the length of equal pieces that costs least, of
+// those for which there are CTAs enough (one lane tries one of 32 lengths), and
+// this CTA's piece.  False: ranges, which always have parts to join and begin
+// and end inside items, cost less.
+template <int ROWS, bool PAIR>
 __device__ __forceinline__ bool find_piece(const Plan& P, Control& C, int warp, int cta) {
   const int items = P.L.B * P.row_tiles, heads = P.L.kv.n_kv_heads, lane = threadIdx.x % 32;
-  for (int x = threadIdx.x; x < items; x += THREADS) {
-    int len, cnt, end, tiles;
-    tree_of(P, x / P.row_tiles, len, cnt);
-    item_tiles<ROWS>(P, len, cnt, x % P.row_tiles, end, tiles);
-    C.tiles[x] = tiles;
-  }
+  for (int x = threadIdx.x; x < items; x += THREADS) C.tiles[x] = group_tiles<ROWS>(P, x);
   __syncthreads();
   int sum = 0, most = 1;  // 2^31 slots at most in a tree: 2^24 tiles in each of 2^8 items
   float total = 0.0f;
@@ -865,15 +994,25 @@ __device__ __forceinline__ bool find_piece(const Plan& P, Control& C, int warp, 
   }
   total = warp_sum(total) * heads;
   most = __reduce_max_sync(FULL, most);
+  constexpr float JOIN = JOIN_COST / (PAIR ? 1.0f : 2.0f), ENDS = ENDS_COST / (PAIR ? 1.0f : 2.0f);
   const float fair = total / gridDim.x;
   const int least = max(1, static_cast<int>(fair));
   const float inv = 1.0f / (least + static_cast<float>(max(0, most - least)) * lane / 31.0f);
-  for (int x = 0; x < items; ++x) sum += pieces_of(C.tiles[x], inv);
-  const uint32_t enough = __ballot_sync(FULL, sum * heads <= static_cast<int>(gridDim.x));
-  // the longest length leaves every item whole, so one is always enough
-  const int best = enough ? __ffs(enough) - 1 : 31;
-  const float chosen = __shfl_sync(FULL, inv, best);
-  if (1.0f / chosen + SEGMENT_COST > fair + 2 * SEGMENT_COST) return false;
+  float longest = 0.0f;
+  bool split = false;
+  for (int x = 0; x < items; ++x) {
+    const int n = pieces_of(C.tiles[x], inv);
+    sum += n;
+    split |= n > 1;
+    longest = fmaxf(longest, static_cast<float>(C.tiles[x]) / n);
+  }
+  // the longest length leaves every item whole, so one is always possible
+  const float cost = sum * heads <= static_cast<int>(gridDim.x) ? longest + (split ? JOIN : 0.0f) : INFINITY;
+  float best = cost;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(FULL, best, o));
+  if (best > fair + JOIN + ENDS) return false;
+  const float chosen = __shfl_sync(FULL, inv, __ffs(__ballot_sync(FULL, cost == best)) - 1);
   if (threadIdx.x == 0) {
     int skip = cta, x = 0, n = 0;
     for (; x < items; ++x) {
@@ -883,6 +1022,7 @@ __device__ __forceinline__ bool find_piece(const Plan& P, Control& C, int warp, 
     }
     C.from = C.to = 0;
     C.pieces = n;
+    C.piece = n ? skip % n : 0;
     if (x < items) {
       const int64_t tiles = C.tiles[x], q = skip % n;
       C.b = x / P.row_tiles;
@@ -898,7 +1038,8 @@ __device__ __forceinline__ bool find_piece(const Plan& P, Control& C, int warp, 
 
 template <typename T, int D, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
-    attend_kernel(const __grid_constant__ Plan P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    attend_kernel(const __grid_constant__ Plan P, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                  const __grid_constant__ CUtensorMap mq) {
   using Y = Layout<D, PAIR>;
   extern __shared__ __align__(1024) uint8_t smem[];  // nothing static, so it starts on a swizzle group
   uint8_t* ring = smem + Y::Q_BYTES;
@@ -907,12 +1048,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < Y::STAGES; ++i) {
       mbar_init(&C.full[i], 1);
-      mbar_init(&C.empty[i], 1);
+      mbar_init(&C.empty[i], 3);  // the products' commit and the side warps
+      mbar_init(&C.clean[i], 2);
     }
     mbar_init(&C.q_full, 2);
     mbar_init(&C.q_empty, 1);
-    mbar_init(&C.v_full, 1);
-    mbar_init(&C.v_clean, 2);
     mbar_init(&C.drain, 1);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&C.s_full[h], 1);
@@ -926,8 +1066,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == HELPERS) tmem_alloc(&C.tmem, COLUMNS);
   grid_dependency_wait();
   grid_dependents_launch();
-  if (!P.may_piece || !find_piece<Y::ROWS>(P, C, warp, cta)) find_range<Y::ROWS>(P, C, warp, cta);
-  if (threadIdx.x == 0) workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows).records[cta].pieces = 0;
+  if (!P.may_piece || !find_piece<Y::ROWS, PAIR>(P, C, warp, cta)) find_range<Y::ROWS>(P, C, warp, cta);
+  if (threadIdx.x == 0 && !P.join_inside) workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows).records[cta].parts = 0;
   if (cta == 0)
     for (int b = threadIdx.x; b < P.L.B; b += THREADS) {
       int len, cnt;
@@ -952,7 +1092,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_wait(&C.drain, 0);
       }
     } else {
-      side_role<T, D, PAIR>(P, C, smem_u32(smem), ring);
+      side_role<T, D, PAIR>(P, &mq, C, smem_u32(smem), ring);
     }
   }
   __syncwarp();
@@ -964,47 +1104,20 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// The rows of items whose tiles lie in several ranges: CTA x of grid.x looks
-// at what range x left, one thread per 8 elements of a row.
-constexpr int JOIN_THREADS = 256;
+// CTA (x, y) of the join: a slice of the rows' elements of the item that begins
+// in range or piece x and goes on after it.
+constexpr int JOIN_THREADS = 256, JOIN_SLICES = 8;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(JOIN_THREADS) attend_join_kernel(const __grid_constant__ Plan P) {
   grid_dependency_wait();
   grid_dependents_launch();
   const Workspace ws = workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows);
-  const int cta = blockIdx.x;
-  const JoinRecord rec = ws.records[cta];
-  const int idx = blockIdx.y * JOIN_THREADS + threadIdx.x, r = idx % P.ws_rows, q = idx / P.ws_rows;
-  if (rec.pieces == 0 || q >= D / 8 || rec.row0 + r >= P.rows) return;
-  const int i = node_of_row(P, rec.row0 + r), g = rec.row0 + r - i * P.group;
+  const JoinRecord rec = ws.records[blockIdx.x];
+  if (rec.parts == 0) return;
   int len, cnt;
   tree_of(P, rec.b, len, cnt);
-  float y[8], sum = 0.0f, top = -INFINITY;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-  if (P.L.nodes.begin + i < cnt) {
-    // part p of the item: the end of range cta, then the starts of the next ones
-    auto part = [&](int p) { return static_cast<int64_t>(cta + p) * 2 + (p == 0 ? 1 : 0); };
-#pragma unroll 4
-    for (int p = 0; p < rec.pieces; ++p) top = fmaxf(top, ws.sums[part(p) * P.ws_rows + r].x);
-    const float sub = top == -INFINITY ? 0.0f : top;
-#pragma unroll 4
-    for (int p = 0; p < rec.pieces; ++p) {
-      const float2 ms = ws.sums[part(p) * P.ws_rows + r];
-      const float4* o = ws.out + (part(p) * (D / 4) + q * 2) * P.ws_rows + r;
-      const float4 a = o[0], b = o[P.ws_rows];
-      const float f = ex2(ms.x - sub);
-      sum += ms.y * f;
-      y[0] += a.x * f, y[1] += a.y * f, y[2] += a.z * f, y[3] += a.w * f;
-      y[4] += b.x * f, y[5] += b.y * f, y[6] += b.z * f, y[7] += b.w * f;
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = sum == 0.0f ? 0.0f : y[e] / sum;
-  T* out = static_cast<T*>(P.L.out.data) + rec.b * P.L.out.tree_stride + i * P.L.out.node_stride +
-           (static_cast<int64_t>(rec.head) * P.group + g) * P.L.out.head_stride + q * 8;
-  *reinterpret_cast<uint4*>(out) = pack8<T>(y);
+  join_rows<T, D>(P, ws, rec, cnt, blockIdx.x, blockIdx.y * JOIN_THREADS + threadIdx.x, JOIN_THREADS * JOIN_SLICES);
 }
 
 // -------------------------------------------------------------------- host ---
@@ -1026,20 +1139,43 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// [page][head][token][element] of one layer: boxes of `box` tokens of 64
-// elements, one head, one page.
-bool pool_map(CUtensorMap* map, const spec_tree_kv_t& kv, void* base, int layer, int box) {
+// Boxes of 64 elements by `box` of a 4-dimensional array of 16-bit elements.
+bool tiled_map(CUtensorMap* map, int dtype, const void* base, const cuuint64_t (&dims)[4], const int64_t (&strides)[3],
+               int box1, int box2) {
   const EncodeTiled fn = encode_tiled();
   if (fn == nullptr) return false;
+  const cuuint64_t bytes[3] = {static_cast<cuuint64_t>(strides[0]) * 2, static_cast<cuuint64_t>(strides[1]) * 2,
+                               static_cast<cuuint64_t>(strides[2]) * 2};
+  const cuuint32_t boxes[4] = {PANEL, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2), 1}, steps[4] = {1, 1, 1, 1};
+  return fn(map, dtype == SPEC_TREE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+            const_cast<void*>(base), dims, bytes, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One layer's keys or values, [page][head][token][element]: `box` tokens of
+// one head and page.
+bool pool_map(CUtensorMap* map, const spec_tree_kv_t& kv, void* base, int layer, int box) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kv.head_dim), static_cast<cuuint64_t>(kv.page_size),
                               static_cast<cuuint64_t>(kv.n_kv_heads), static_cast<cuuint64_t>(kv.n_pages)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(kv.token_stride) * 2, static_cast<cuuint64_t>(kv.head_stride) * 2,
-                                 static_cast<cuuint64_t>(kv.page_stride) * 2};
-  const cuuint32_t boxes[4] = {PANEL, static_cast<cuuint32_t>(box), 1, 1}, steps[4] = {1, 1, 1, 1};
-  return fn(map, kv.dtype == SPEC_TREE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-            static_cast<uint16_t*>(base) + layer * kv.layer_stride, dims, strides, boxes, steps,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const int64_t strides[3] = {kv.token_stride, kv.head_stride, kv.page_stride};
+  return tiled_map(map, kv.dtype, static_cast<uint16_t*>(base) + layer * kv.layer_stride, dims, strides, box, 1);
+}
+
+// Queries, [tree][node][head][element]: one key head's heads of q_box nodes.
+bool query_map(CUtensorMap* map, const Plan& P) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(P.L.kv.head_dim), static_cast<cuuint64_t>(P.L.n_q_heads),
+                              static_cast<cuuint64_t>(P.L.nodes.count), static_cast<cuuint64_t>(P.L.B)};
+  const int64_t strides[3] = {P.L.q.head_stride, P.L.q.node_stride, P.L.q.tree_stride};
+  return tiled_map(map, P.L.kv.dtype, P.L.q.data, dims, strides, P.group, P.q_box);
+}
+
+// Whether queries can be copied by a tensor map: the heads of whole nodes fill
+// a half, and strides are what a map takes.
+bool tiled_queries(const Plan& P) {
+  const int64_t strides[3] = {P.L.q.head_stride, P.L.q.node_stride, P.L.q.tree_stride};
+  for (int64_t x : strides)
+    if (x <= 0 || x >= (1ll << 38)) return false;
+  return TILE % P.group == 0;
 }
 
 template <typename T, int D, bool PAIR>
@@ -1051,15 +1187,24 @@ cudaError_t attend(Plan& P, cudaStream_t stream) {
   P.row_tiles = (P.rows + Y::ROWS - 1) / Y::ROWS;
   const int64_t items = static_cast<int64_t>(P.L.B) * P.row_tiles;
   P.may_piece = items * P.L.kv.n_kv_heads <= P.L.num_sms && items <= MAX_PIECE_ITEMS;
-  CUtensorMap mk, mv;
-  if (!pool_map(&mk, P.L.kv, P.L.kv.k, P.L.layer, P.box) || !pool_map(&mv, P.L.kv, P.L.kv.v, P.L.layer, P.box))
+  P.q_box = tiled_queries(P) ? std::min(TILE / P.group, P.L.nodes.count) : 0;
+  CUtensorMap mk, mv, mq = {};
+  if (!pool_map(&mk, P.L.kv, P.L.kv.k, P.L.layer, P.box) || !pool_map(&mv, P.L.kv, P.L.kv.v, P.L.layer, P.box) ||
+      (P.q_box && !query_map(&mq, P)))
     return cudaErrorInvalidValue;
-  cudaError_t err = cudaFuncSetAttribute(attend_kernel<T, D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  static std::atomic<uint64_t> prepared{0};  // devices that know the kernel's shared memory
+  int device = 0;
+  cudaError_t err = cudaGetDevice(&device);
   if (err != cudaSuccess) return err;
-  err = launch_pdl(attend_kernel<T, D, PAIR>, dim3(P.L.num_sms), dim3(THREADS), SMEM, stream, P, mk, mv);
-  if (err != cudaSuccess) return err;
-  return launch_pdl(attend_join_kernel<T, D>, dim3(P.L.num_sms, (P.ws_rows * (D / 8) + JOIN_THREADS - 1) / JOIN_THREADS),
-                    dim3(JOIN_THREADS), 0, stream, P);
+  const uint64_t bit = device < 64 ? 1ull << device : 0;
+  if (!(prepared.load(std::memory_order_relaxed) & bit)) {
+    err = cudaFuncSetAttribute(attend_kernel<T, D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (err != cudaSuccess) return err;
+    prepared.fetch_or(bit, std::memory_order_relaxed);
+  }
+  err = launch_pdl(attend_kernel<T, D, PAIR>, dim3(P.L.num_sms), dim3(THREADS), SMEM, stream, P, mk, mv, mq);
+  if (err != cudaSuccess || P.join_inside) return err;
+  return launch_pdl(attend_join_kernel<T, D>, dim3(P.L.num_sms, JOIN_SLICES), dim3(JOIN_THREADS), 0, stream, P);
 }
 
 template <typename T, int D>
@@ -1084,6 +1229,7 @@ cudaError_t launch_attend(const AttendLaunch& L, cudaStream_t stream) {
   P.page_shift = log2_of(L.kv.page_size);
   P.box = L.kv.page_size < TILE ? L.kv.page_size : TILE;
   P.ws_rows = workspace_rows(P.rows);
+  P.join_inside = P.rows <= JOIN_INSIDE_ROWS;
   // a scale of zero would turn -inf into NaN: weights 2^(1e-30 S) are all one as well
   P.scale2 = fminf(fmaxf(fabsf(L.scale) * 1.4426950408889634f, 1e-30f), 3e38f);
   P.negative = L.scale < 0.0f;
