@@ -10,6 +10,8 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import struct
+import threading
 from typing import Optional
 
 import torch
@@ -96,13 +98,13 @@ def _load():
     dp = ctypes.POINTER(ctypes.c_double)
     lib.spec_tree_smart_fit.argtypes = [i32, dp, dp, dp, ctypes.c_double, dp, P, dp, dp]
     lib.spec_tree_wait_selftest.argtypes = [ctypes.c_uint32, vp, vp, vp]
-    KV, N, H = ctypes.POINTER(c_kv), ctypes.POINTER(c_nodes), ctypes.POINTER(c_heads)
-    lib.spec_tree_kv_append.argtypes = [i32, KV, i32, N, i32, H, H, H, H, vp, i32, i32, i32, vp, vp, ctypes.c_float,
-                                        vp, vp]
-    lib.spec_tree_attend.argtypes = [i32, KV, i32, N, i32, H, H, ctypes.c_float, vp, ctypes.c_size_t, vp, vp]
+    # structures by address: these calls are made once per layer of a model, and their arguments are packed
+    lib.spec_tree_kv_append.argtypes = [i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp,
+                                        ctypes.c_float, vp, vp]
+    lib.spec_tree_attend.argtypes = [i32, vp, i32, vp, i32, vp, vp, ctypes.c_float, vp, ctypes.c_size_t, vp, vp]
     lib.spec_tree_attend_workspace_bytes.argtypes = [i32] * 5
     lib.spec_tree_attend_workspace_bytes.restype = ctypes.c_size_t
-    lib.spec_tree_kv_commit.argtypes = [i32, KV, vp, vp, i32, vp, vp, vp]
+    lib.spec_tree_kv_commit.argtypes = [i32, vp, vp, vp, i32, vp, vp, vp]
     lib.spec_tree_strerror.argtypes = [i32]
     lib.spec_tree_strerror.restype = ctypes.c_char_p
     for name in EXPORTS:
@@ -156,13 +158,13 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle of the current stream, without the Stream object around it (2.9 us a call)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _check(rc: int):
-    if rc != OK:
+    if rc:
         raise SpecTreeError(f"spec_tree error {rc}: {_lib.spec_tree_strerror(rc).decode()}")
 
 
@@ -396,14 +398,14 @@ class KVCache:
         c = c_kv(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), None, k.stride(0), k.stride(1), k.stride(2),
                  k.stride(3), _HALF[k.dtype], layers, pages, size, heads, dim, page_table.shape[1],
                  max(page_table.stride(0), page_table.shape[1]))
-        self._c = c
+        self._c, self.at = c, ctypes.addressof(c)
+        self.shape = (self.B, heads, dim, k.dtype)
         self.set_lengths(seq_len)
 
     def set_lengths(self, seq_len: torch.Tensor):
         """Committed tokens from now on, e.g. the new_len of spec_tree_kv_commit."""
-        _int_rows("seq_len", seq_len, (self.B,))
+        self._c.seq_len = _int_rows("seq_len", seq_len, (self.B,))
         self.seq_len = seq_len
-        self._c.seq_len = seq_len.data_ptr()
 
     def c(self) -> c_kv:
         return self._c
@@ -418,36 +420,55 @@ class NodeArrays:
     n_nodes: Optional[torch.Tensor] = None
 
 
-def _int_rows(name: str, t: torch.Tensor, shape):
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+def _int_rows(name: str, t: torch.Tensor, shape) -> int:
+    """Address of a contiguous int32 tensor of that shape."""
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise SpecTreeError(f"{name} must be contiguous int32 {list(shape)}")
+    return t.data_ptr()
 
 
-def _nodes(tree, B: int, begin: int, count: int) -> c_nodes:
-    """spec_tree_nodes_t of a TreeBuffers, a NodeArrays or None (a chain of which every node exists)."""
-    if tree is None:
-        return c_nodes(None, None, None, 0, begin, count)
-    parent, depth, n = tree.node_parent, tree.node_depth, tree.n_nodes
-    stride = 0
-    if parent is not None:
-        stride = parent.shape[1] if parent.dim() == 2 else 0
-        _int_rows("node_parent", parent, (B, stride))
-        if depth is not None:
-            _int_rows("node_depth", depth, (B, stride))
-    elif depth is not None:
-        raise SpecTreeError("node_depth without node_parent")
-    if n is not None:
-        _int_rows("n_nodes", n, (B,))
-    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    return c_nodes(at(parent), at(depth), at(n), stride, begin, count)
+class _Packed(threading.local):
+    """One call's spec_tree_nodes_t and up to four spec_tree_heads_t, packed into memory of the thread's own
+    (the entry points read them before they return)."""
+    NODES, HEADS = struct.Struct("@3P3i"), struct.Struct("@P3q")
+
+    def __init__(self):
+        self.buf = ctypes.create_string_buffer(64 + 4 * self.HEADS.size)
+        self.nodes_at = ctypes.addressof(self.buf)
+        self.heads_at = tuple(self.nodes_at + 64 + i * self.HEADS.size for i in range(4))
+
+    def nodes(self, tree, B: int, begin: int, count: int) -> int:
+        """A TreeBuffers, a NodeArrays or None (a chain of which every node exists)."""
+        if tree is None:
+            self.NODES.pack_into(self.buf, 0, 0, 0, 0, 0, begin, count)
+            return self.nodes_at
+        parent, depth, n = tree.node_parent, tree.node_depth, tree.n_nodes
+        at, stride = 0, 0
+        if parent is not None:
+            stride = parent.shape[-1]
+            at = _int_rows("node_parent", parent, (B, stride))
+        elif depth is not None:
+            raise SpecTreeError("node_depth without node_parent")
+        self.NODES.pack_into(self.buf, 0, at, 0 if depth is None else _int_rows("node_depth", depth, (B, stride)),
+                             0 if n is None else _int_rows("n_nodes", n, (B,)), stride, begin, count)
+        return self.nodes_at
+
+    def heads(self, i: int, name: str, x: torch.Tensor, dtype, shape) -> int:
+        """[B][nodes][heads][head_dim] with contiguous head_dim."""
+        s = x.stride()
+        if x.dtype is not dtype or x.shape != shape or s[3] != 1:
+            raise SpecTreeError(f"{name} must be {list(shape)} of {dtype}, head_dim contiguous")
+        self.HEADS.pack_into(self.buf, 64 + i * self.HEADS.size, x.data_ptr(), s[0], s[1], s[2])
+        return self.heads_at[i]
 
 
-def _heads(name: str, x: torch.Tensor, cache: KVCache, count: Optional[int] = None, heads: Optional[int] = None):
-    if x.dim() != 4 or x.dtype != cache.k.dtype or x.stride(3) != 1 or x.shape[0] != cache.B or \
-            x.shape[3] != cache.k.shape[4] or (count is not None and x.shape[1] != count) or \
-            (heads is not None and x.shape[2] != heads):
-        raise SpecTreeError(f"{name} must be [B][nodes][heads][head_dim] of the cache's dtype, head_dim contiguous")
-    return c_heads(x.data_ptr(), x.stride(0), x.stride(1), x.stride(2))
+_packed = _Packed()
+
+
+def _count(q: torch.Tensor):
+    if q.dim() != 4:
+        raise SpecTreeError("q must be [B][nodes][heads][head_dim]")
+    return q.shape[1], q.shape[2]
 
 
 def rope_table(rows: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -466,23 +487,23 @@ def spec_tree_kv_append(cache: KVCache, layer: int, q: torch.Tensor, k: torch.Te
                         stream=None):
     """Nodes node_begin .. node_begin + q.shape[1] - 1 of every tree: head norms (with weights), rotation
     (with a rope table [rows][rot_dim]), keys and values into the cache, queries to q_out."""
-    n, dim = q.shape[1], cache.k.shape[4]
-    cq, ck, cv = _heads("q", q, cache), _heads("k", k, cache, n, cache.k.shape[3]), _heads("v", v, cache, n,
-                                                                                           cache.k.shape[3])
-    co = _heads("q_out", q_out, cache, n, q.shape[2])
-    rows = rot = 0
+    (n, hq), (B, hkv, dim, dtype), pack = _count(q), cache.shape, _packed
+    rows = rot = rope_at = 0
     if rope is not None:
-        if rope.dim() != 2 or rope.dtype != torch.float32 or not rope.is_contiguous():
+        if rope.dim() != 2 or rope.dtype is not torch.float32 or not rope.is_contiguous():
             raise SpecTreeError("rope must be contiguous float32 [rows][rot_dim]")
         rows, rot = rope.shape
+        rope_at = rope.data_ptr()
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and (w.dtype != cache.k.dtype or tuple(w.shape) != (dim,) or not w.is_contiguous()):
+        if w is not None and (w.dtype is not dtype or w.shape != (dim,) or not w.is_contiguous()):
             raise SpecTreeError(f"{name} must be [head_dim] of the cache's dtype")
-    nodes = _nodes(tree, cache.B, node_begin, n)
-    _check(_lib.spec_tree_kv_append(cache.B, ctypes.byref(cache.c()), layer, ctypes.byref(nodes), q.shape[2],
-                                    ctypes.byref(cq), ctypes.byref(ck), ctypes.byref(cv), ctypes.byref(co),
-                                    _ptr(rope), rows, rot, int(interleaved), _ptr(q_weight), _ptr(k_weight), eps,
-                                    _ptr(status), _stream(stream)))
+    qs, ks = (B, n, hq, dim), (B, n, hkv, dim)
+    _check(_lib.spec_tree_kv_append(B, cache.at, layer, pack.nodes(tree, B, node_begin, n), hq,
+                                    pack.heads(0, "q", q, dtype, qs), pack.heads(1, "k", k, dtype, ks),
+                                    pack.heads(2, "v", v, dtype, ks), pack.heads(3, "q_out", q_out, dtype, qs),
+                                    rope_at, rows, rot, interleaved, None if q_weight is None else q_weight.data_ptr(),
+                                    None if k_weight is None else k_weight.data_ptr(), eps, status.data_ptr(),
+                                    _stream(stream)))
 
 
 class AttendWorkspace:
@@ -494,6 +515,7 @@ class AttendWorkspace:
         if n == 0:
             raise SpecTreeError("spec_tree_attend takes no such heads or nodes")
         self.data = torch.zeros(n, dtype=torch.uint8, device=device)
+        self.at, self.bytes = self.data.data_ptr(), n
 
 
 def spec_tree_attend(cache: KVCache, layer: int, q: torch.Tensor, out: torch.Tensor, workspace: AttendWorkspace,
@@ -501,20 +523,22 @@ def spec_tree_attend(cache: KVCache, layer: int, q: torch.Tensor, out: torch.Ten
                      stream=None):
     """Nodes node_begin .. node_begin + q.shape[1] - 1 of every tree attend to the committed tokens, their
     ancestors and themselves; scale defaults to head_dim ** -0.5."""
-    cq, co = _heads("q", q, cache), _heads("out", out, cache, q.shape[1], q.shape[2])
-    nodes = _nodes(tree, cache.B, node_begin, q.shape[1])
-    _check(_lib.spec_tree_attend(cache.B, ctypes.byref(cache.c()), layer, ctypes.byref(nodes), q.shape[2],
-                                 ctypes.byref(cq), ctypes.byref(co),
-                                 cache.k.shape[4] ** -0.5 if scale is None else scale, _ptr(workspace.data),
-                                 workspace.data.numel(), _ptr(status), _stream(stream)))
+    (n, hq), (B, _, dim, dtype), pack = _count(q), cache.shape, _packed
+    qs = (B, n, hq, dim)
+    _check(_lib.spec_tree_attend(B, cache.at, layer, pack.nodes(tree, B, node_begin, n), hq,
+                                 pack.heads(0, "q", q, dtype, qs), pack.heads(1, "out", out, dtype, qs),
+                                 dim ** -0.5 if scale is None else scale, workspace.at, workspace.bytes,
+                                 status.data_ptr(), _stream(stream)))
 
 
 def spec_tree_kv_commit(cache: KVCache, accept_len: torch.Tensor, out_node: torch.Tensor, new_len: torch.Tensor,
                         status: torch.Tensor, stream=None):
     """Move the accepted path (spec_tree_verify's accept_len and out_node) behind the committed tokens in
     every layer; new_len [B] receives the new committed lengths (then cache.set_lengths(new_len))."""
-    _int_rows("accept_len", accept_len, (cache.B,))
-    _int_rows("new_len", new_len, (cache.B,))
-    _int_rows("out_node", out_node, (cache.B, out_node.shape[-1]))
-    _check(_lib.spec_tree_kv_commit(cache.B, ctypes.byref(cache.c()), _ptr(accept_len), _ptr(out_node),
-                                    out_node.shape[1], _ptr(new_len), _ptr(status), _stream(stream)))
+    B = (cache.B,)
+    if out_node.dim() != 2:
+        raise SpecTreeError("out_node must be [B][depth + 1]")
+    stride = out_node.shape[1]
+    _check(_lib.spec_tree_kv_commit(cache.B, cache.at, _int_rows("accept_len", accept_len, B),
+                                    _int_rows("out_node", out_node, (cache.B, stride)), stride,
+                                    _int_rows("new_len", new_len, B), status.data_ptr(), _stream(stream)))

@@ -581,11 +581,11 @@ __device__ __forceinline__ void side_role(const Plan& P, const CUtensorMap* mq, 
             uint8_t* at = ring + slot * Y::KV_BYTES + row * 128;
             bool odd = false;
             if (j * TILE + row >= s.end) {
-#pragma unroll
+#pragma unroll 4
               for (int c = 0; c < CHUNKS; ++c)
                 *reinterpret_cast<uint4*>(at + (c / 8) * PANEL_BYTES + ((c ^ t) % 8) * 16) = make_uint4(0, 0, 0, 0);
-            } else {
-#pragma unroll
+            } else if (j * TILE + row >= s.clear) {  // a token that some rows do not see
+#pragma unroll 1
               for (int p = 0; p < Y::PANELS; ++p)
                 odd |= any_odd<T>(reinterpret_cast<const uint4*>(at + p * PANEL_BYTES), t % 8);
             }

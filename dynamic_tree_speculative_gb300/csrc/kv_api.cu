@@ -94,6 +94,8 @@ int spec_tree_kv_append(int B, const spec_tree_kv_t* kv, int layer, const spec_t
   L.k_weight = k_weight;
   L.eps = eps;
   L.status = status;
+  L.num_sms = st::num_sms_of_current_device();
+  if (L.num_sms <= 0) return SPEC_TREE_E_CUDA;
   return of(st::launch_kv_append(L, as_stream(stream)));
 }
 

@@ -7,114 +7,190 @@
 namespace st {
 namespace {
 
-constexpr int APPEND_THREADS = 256;
+constexpr int APPEND_THREADS = 128, APPEND_BATCH = 4;  // vectors a lane has in flight
+constexpr int APPEND_WARPS = 32;                       // per SM, that a node's heads are spread over warps to reach
 constexpr int COMMIT_THREADS = 128;
 constexpr int COMMIT_BATCH = 8;  // path steps loaded before any is stored
 
-// A head vector belongs to D / 8 neighbouring lanes, 8 elements (16 bytes)
-// each; a CTA takes 256 * 8 / D vectors of one node.  Everything is read and
-// written once: bytes bound it, at few nodes the chain of dependent loads
-// (length, position, rotation row) does.
+// 16 bytes as four pairs of floats.
+template <typename T>
+__device__ __forceinline__ void unpack_pairs(uint4 w, F2 (&x)[4]) {
+  x[0] = F2(Pair<T>::unpack(w.x));
+  x[1] = F2(Pair<T>::unpack(w.y));
+  x[2] = F2(Pair<T>::unpack(w.z));
+  x[3] = F2(Pair<T>::unpack(w.w));
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack_pairs(const F2 (&x)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float lo, hi;
+    x[e].get(lo, hi);
+    w[e] = Pair<T>::pack(lo, hi);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One or more warps per node.  A head vector belongs to D / 8 neighbouring
+// lanes, 8 elements (16 bytes) each, so a warp takes 2 or 4 vectors a step; a
+// lane's place in the vector, and with it its part of the rotation row and of
+// the weights, is the same in every step.
+//
+// With u the vector before the norm, w the weights and r = 1 / rms(u), a turned
+// element is r (u_j (w_j c) + u_p (w_p s)), p its partner, s with the sign of
+// j's place in the pair: the products in brackets are made once per node, and a
+// lane gets its partners' u by shuffling the raw 16 bytes.
+//
+// Everything is read and written once; what bounds it is the issue rate.  At
+// 64 trees of 61 nodes of 48 heads of 128, normalised (95 MB: 14 us at the
+// measured bandwidth): 22.5 us.  One vector per thread, with a node's loads and
+// products made for each, took 37.2 us; three per thread 34.3 (253 instructions
+// a step of a warp, of which this leaves 139).
 template <typename T, int D>
-__global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendLaunch L, int chunks, int page_shift) {
-  constexpr int LANES = D / 8, PER_CTA = APPEND_THREADS / LANES;
-  const int64_t item = blockIdx.x / chunks;
-  const int b = static_cast<int>(item / L.nodes.count), i = static_cast<int>(item % L.nodes.count);
-  const int head = (blockIdx.x % chunks) * PER_CTA + threadIdx.x / LANES;
-  const int lane = threadIdx.x % LANES;
-  const int n_kv = L.kv.n_kv_heads;
-  const bool is_q = head < L.n_q_heads, is_k = !is_q && head < L.n_q_heads + n_kv;
-  const bool any = head < L.n_q_heads + 2 * n_kv;
-  const int h = is_q ? head : (is_k ? head - L.n_q_heads : head - L.n_q_heads - n_kv);
+__global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_constant__ AppendLaunch L, int page_shift,
+                                                                   int nodes, int spread) {
+  constexpr int LANES = D / 8, PER_STEP = 32 / LANES;
+  const int lane = threadIdx.x % LANES, sub = threadIdx.x % 32 / LANES;
+  const int warp = blockIdx.x * (APPEND_THREADS / 32) + threadIdx.x / 32;
+  const int node = warp / spread;
+  if (node >= nodes) return;
+  const int n_q = L.n_q_heads, n_kv = L.kv.n_kv_heads, steps = (n_q + 2 * n_kv + PER_STEP - 1) / PER_STEP;
+  const int b = node / L.nodes.count, i = node - b * L.nodes.count, n = L.nodes.begin + i;
+  // pairs are elements j and j + rot_dim / 2, `half` lanes apart, or neighbours
+  const int half = L.rot_dim / 16;
+  const bool in_rot = lane < 2 * half, first = lane < half;
+  const int partner = !in_rot || L.interleaved ? lane : (first ? lane + half : lane - half);
+  const T* q = static_cast<const T*>(L.q.data) + b * L.q.tree_stride + i * L.q.node_stride + lane * 8;
+  const T* k = static_cast<const T*>(L.k.data) + b * L.k.tree_stride + i * L.k.node_stride + lane * 8;
+  const T* w = static_cast<const T*>(L.v.data) + b * L.v.tree_stride + i * L.v.node_stride + lane * 8;
+  T* q_to = static_cast<T*>(L.q_out.data) + b * L.q_out.tree_stride + i * L.q_out.node_stride + lane * 8;
   grid_dependency_wait();
   grid_dependents_launch();
 
-  const spec_tree_heads_t& in = is_q ? L.q : (is_k ? L.k : L.v);
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (any)
-    raw = *reinterpret_cast<const uint4*>(static_cast<const T*>(in.data) + b * in.tree_stride + i * in.node_stride +
-                                          h * in.head_stride + lane * 8);
-  T* q_to = static_cast<T*>(L.q_out.data) + b * L.q_out.tree_stride + i * L.q_out.node_stride +
-            (is_q ? h : 0) * L.q_out.head_stride + lane * 8;
-  const int n = L.nodes.begin + i;
-  const int len = L.kv.seq_len[b];
-  if (n >= node_count(L.nodes, b) || len < 0) {  // uniform over the CTA
-    if (len < 0 && threadIdx.x == 0) set_status(L.status, SPEC_TREE_S_NODES);
-    if (any && is_q) *reinterpret_cast<uint4*>(q_to) = make_uint4(0, 0, 0, 0);
+  uint4 raw[APPEND_BATCH];
+  auto fetch = [&](int step0) {
+#pragma unroll
+    for (int u = 0; u < APPEND_BATCH; ++u) {
+      const int head = (step0 + u * spread) * PER_STEP + sub;
+      raw[u] = make_uint4(0, 0, 0, 0);
+      if (head < n_q)
+        raw[u] = *reinterpret_cast<const uint4*>(q + head * L.q.head_stride);
+      else if (head < n_q + n_kv)
+        raw[u] = *reinterpret_cast<const uint4*>(k + (head - n_q) * L.k.head_stride);
+      else if (head < n_q + 2 * n_kv)
+        raw[u] = *reinterpret_cast<const uint4*>(w + (head - n_q - n_kv) * L.v.head_stride);
+    }
+  };
+  const int step0 = warp - node * spread;
+  fetch(step0);
+  const int len = L.kv.seq_len[b], cnt = node_count(L.nodes, b);
+  const int depth = L.nodes.depth ? L.nodes.depth[static_cast<int64_t>(b) * L.nodes.stride + n] : n;
+  if (len < 0 && threadIdx.x % 32 == 0) set_status(L.status, SPEC_TREE_S_NODES);
+  if (n >= cnt || len < 0) {
+    for (int step = step0; step * PER_STEP < n_q; step += spread)
+      if (step * PER_STEP + sub < n_q)
+        *reinterpret_cast<uint4*>(q_to + (step * PER_STEP + sub) * L.q_out.head_stride) = make_uint4(0, 0, 0, 0);
     return;
   }
-  const int depth = L.nodes.depth ? L.nodes.depth[static_cast<int64_t>(b) * L.nodes.stride + n] : n;
-  const int64_t pos = static_cast<int64_t>(len) + depth;
   const int64_t off = kv_slot_offset(L.kv, b, static_cast<int64_t>(len) + n, page_shift);
-  const bool has_angle = L.rot_dim > 0 && depth >= 0 && pos < L.rope_rows;
-  if (L.rot_dim > 0 && !has_angle && threadIdx.x == 0) set_status(L.status, SPEC_TREE_S_NODES);
+  if (off < 0 && threadIdx.x % 32 == 0) set_status(L.status, SPEC_TREE_S_PAGES);
 
-  float x[8];
-  unpack8<T>(raw, x);
-  const void* weight = is_q ? L.q_weight : (is_k ? L.k_weight : nullptr);
-  // shuffles are executed by the whole warp, whichever heads its lanes hold
-  float ss = 0.0f;
+  // c and signed s of the lane's elements
+  const int64_t pos = static_cast<int64_t>(len) + depth;
+  const bool turned = L.rot_dim > 0 && depth >= 0 && pos < L.rope_rows;
+  if (L.rot_dim > 0 && !turned && threadIdx.x % 32 == 0) set_status(L.status, SPEC_TREE_S_NODES);
+  F2 c[4], s[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-#pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
-  if (weight) {
-    const float r = rsqrtf(ss * (1.0f / D) + L.eps);
-    float w[8];
-    unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(weight) + lane * 8), w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
-  }
-  if (has_angle) {  // uniform over the CTA
+  for (int e = 0; e < 4; ++e) c[e] = F2(1.0f, 1.0f), s[e] = F2(0.0f, 0.0f);
+  if (turned && in_rot) {
     const float* row = L.rope + pos * L.rot_dim;
-    const bool turns = lane * 8 < L.rot_dim;
     if (L.interleaved) {
-      if (turns && any && (is_q || is_k)) {
-        const float4 c = *reinterpret_cast<const float4*>(row + lane * 4);
-        const float4 s = *reinterpret_cast<const float4*>(row + L.rot_dim / 2 + lane * 4);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss4[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a = x[2 * e], d = x[2 * e + 1];
-          x[2 * e] = a * cc[e] - d * ss4[e];
-          x[2 * e + 1] = a * ss4[e] + d * cc[e];
-        }
-      }
+      const float4 x = *reinterpret_cast<const float4*>(row + lane * 4);
+      const float4 y = *reinterpret_cast<const float4*>(row + L.rot_dim / 2 + lane * 4);
+      c[0] = F2(x.x, x.x), c[1] = F2(x.y, x.y), c[2] = F2(x.z, x.z), c[3] = F2(x.w, x.w);
+      s[0] = F2(-y.x, y.x), s[1] = F2(-y.y, y.y), s[2] = F2(-y.z, y.z), s[3] = F2(-y.w, y.w);
     } else {
-      const int half = L.rot_dim / 16;  // lanes of a half of the pairs
-      const bool first = lane < half;
-      const int partner = turns ? (first ? lane + half : lane - half) : lane;
-      float y[8];
+      const float* at = row + (first ? lane : lane - half) * 8;
+      const float sign = first ? -1.0f : 1.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(FULL, x[e], partner, LANES);
-      if (turns && any && (is_q || is_k)) {
-        const float* cp = row + (first ? lane : lane - half) * 8;
-        const float* sp = cp + L.rot_dim / 2;
-#pragma unroll
-        for (int q4 = 0; q4 < 2; ++q4) {
-          const float4 c = *reinterpret_cast<const float4*>(cp + q4 * 4);
-          const float4 s = *reinterpret_cast<const float4*>(sp + q4 * 4);
-          const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = q4 * 4 + e;
-            x[j] = first ? x[j] * cc[e] - y[j] * sn[e] : y[j] * sn[e] + x[j] * cc[e];
-          }
-        }
+      for (int e = 0; e < 2; ++e) {
+        const float4 x = *reinterpret_cast<const float4*>(at + 4 * e);
+        const float4 y = *reinterpret_cast<const float4*>(at + L.rot_dim / 2 + 4 * e);
+        c[2 * e] = F2(x.x, x.y), c[2 * e + 1] = F2(x.z, x.w);
+        s[2 * e] = F2(sign * y.x, sign * y.y), s[2 * e + 1] = F2(sign * y.z, sign * y.w);
       }
     }
   }
-  if (!any) return;
-  if (is_q) {
-    *reinterpret_cast<uint4*>(q_to) = pack8<T>(x);
-    return;
+  auto swapped = [&](uint4 x) {  // the other element of each neighbouring pair
+    return make_uint4(__byte_perm(x.x, 0, 0x1032), __byte_perm(x.y, 0, 0x1032), __byte_perm(x.z, 0, 0x1032),
+                      __byte_perm(x.w, 0, 0x1032));
+  };
+  F2 cq[4], sq[4], ck[4], sk[4];
+  auto weighted = [&](const void* weight, F2 (&cw)[4], F2 (&sw)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cw[e] = c[e], sw[e] = s[e];
+    if (weight == nullptr) return;
+    F2 x[4], y[4];
+    unpack_pairs<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(weight) + lane * 8), x);
+    const uint4 other = *reinterpret_cast<const uint4*>(static_cast<const T*>(weight) + partner * 8);
+    unpack_pairs<T>(L.interleaved ? swapped(other) : other, y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cw[e] = mul2(c[e], x[e]), sw[e] = mul2(s[e], y[e]);
+  };
+  weighted(L.q_weight, cq, sq);
+  weighted(L.k_weight, ck, sk);
+  const bool norms = L.q_weight || L.k_weight;
+  T* k_to = static_cast<T*>(L.kv.k) + L.layer * L.kv.layer_stride + off + lane * 8;
+  T* v_to = static_cast<T*>(L.kv.v) + L.layer * L.kv.layer_stride + off + lane * 8;
+
+  for (int at = step0; at < steps; at += APPEND_BATCH * spread) {
+    if (at != step0) fetch(at);
+#pragma unroll
+    for (int u = 0; u < APPEND_BATCH; ++u) {
+      // the whole warp takes part in the shuffles, whatever its lanes hold
+      const int head = (at + u * spread) * PER_STEP + sub;
+      const bool is_q = head < n_q, is_k = !is_q && head < n_q + n_kv;
+      uint4 other = raw[u];
+      if (L.interleaved) {
+        other = swapped(other);
+      } else {
+        other.x = __shfl_sync(FULL, other.x, partner, LANES);
+        other.y = __shfl_sync(FULL, other.y, partner, LANES);
+        other.z = __shfl_sync(FULL, other.z, partner, LANES);
+        other.w = __shfl_sync(FULL, other.w, partner, LANES);
+      }
+      F2 x[4], y[4];
+      unpack_pairs<T>(raw[u], x);
+      unpack_pairs<T>(other, y);
+      float r = 1.0f;
+      if (norms) {
+        F2 sum = mul2(x[0], x[0]);
+#pragma unroll
+        for (int e = 1; e < 4; ++e) sum = fma2(x[e], x[e], sum);
+        float lo, hi;
+        sum.get(lo, hi);
+        lo += hi;
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) lo += __shfl_xor_sync(FULL, lo, o);
+        r = rsqrtf(lo * (1.0f / D) + L.eps);
+      }
+      if (is_q) {
+        if (L.q_weight == nullptr) r = 1.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = mul2(fma2(y[e], sq[e], mul2(x[e], cq[e])), F2(r, r));
+        *reinterpret_cast<uint4*>(q_to + head * L.q_out.head_stride) = pack_pairs<T>(x);
+      } else if (is_k) {
+        if (L.k_weight == nullptr) r = 1.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = mul2(fma2(y[e], sk[e], mul2(x[e], ck[e])), F2(r, r));
+        if (off >= 0) *reinterpret_cast<uint4*>(k_to + (head - n_q) * L.kv.head_stride) = pack_pairs<T>(x);
+      } else if (head < n_q + 2 * n_kv && off >= 0) {
+        *reinterpret_cast<uint4*>(v_to + (head - n_q - n_kv) * L.kv.head_stride) = raw[u];
+      }
+    }
   }
-  if (off < 0) {
-    if (lane == 0) set_status(L.status, SPEC_TREE_S_PAGES);
-    return;
-  }
-  T* to = static_cast<T*>(is_k ? L.kv.k : L.kv.v) + L.layer * L.kv.layer_stride + off + h * L.kv.head_stride + lane * 8;
-  *reinterpret_cast<uint4*>(to) = is_k ? pack8<T>(x) : raw;
 }
 
 // One thread per 16 bytes of a slot's entries in one layer of keys or values;
@@ -173,11 +249,13 @@ __global__ void __launch_bounds__(COMMIT_THREADS) kv_commit_kernel(const CommitL
 
 template <typename T, int D>
 cudaError_t append(const AppendLaunch& L, cudaStream_t stream) {
-  constexpr int PER_CTA = APPEND_THREADS / (D / 8);
-  const int chunks = (L.n_q_heads + 2 * L.kv.n_kv_heads + PER_CTA - 1) / PER_CTA;
-  const int64_t ctas = static_cast<int64_t>(L.B) * L.nodes.count * chunks;
+  const int nodes = L.B * L.nodes.count, steps = (L.n_q_heads + 2 * L.kv.n_kv_heads + 256 / D - 1) / (256 / D);
+  int spread = 1;  // warps per node
+  while (spread < steps && static_cast<int64_t>(nodes) * spread < L.num_sms * APPEND_WARPS) spread *= 2;
+  if (spread > steps) spread = steps;
+  const int64_t ctas = (static_cast<int64_t>(nodes) * spread + APPEND_THREADS / 32 - 1) / (APPEND_THREADS / 32);
   return launch_pdl(kv_append_kernel<T, D>, dim3(static_cast<unsigned>(ctas)), dim3(APPEND_THREADS), 0, stream, L,
-                    chunks, log2_of(L.kv.page_size));
+                    log2_of(L.kv.page_size), nodes, spread);
 }
 
 }  // namespace

@@ -79,6 +79,7 @@ struct AppendLaunch {
   const void* k_weight;
   float eps;
   uint32_t* status;
+  int num_sms;
 };
 
 struct AttendLaunch {

@@ -9,6 +9,33 @@
 
 namespace st {
 
+// Pairs of float32 that one instruction works on.
+struct F2 {
+  uint64_t v;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ explicit F2(float2 x) : F2(x.x, x.y) {}
+  __device__ __forceinline__ void get(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+};
+
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 y;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return y;
+}
+
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 y;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y.v) : "l"(a.v), "l"(b.v));
+  return y;
+}
+
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 y;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y.v) : "l"(a.v), "l"(b.v));
+  return y;
+}
+
 // Two 16-bit floats of a 32-bit word, low half first.
 template <typename T>
 struct Pair;

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "st_common.cuh"
+#include "st_kv.cuh"
 
 namespace st {
 
@@ -153,26 +154,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-
-// Pairs of float32 that one instruction works on.
-struct F2 {
-  uint64_t v;
-  __device__ __forceinline__ F2() {}
-  __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
-  __device__ __forceinline__ void get(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-};
-
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 y;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return y;
-}
-
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 y;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y.v) : "l"(a.v), "l"(b.v));
   return y;
 }
 

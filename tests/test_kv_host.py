@@ -1,6 +1,7 @@
 """Key-value cache entry points: refusals before any launch, structures, the oracle (no GPU needed)."""
 import ctypes
 import os
+import struct
 
 import numpy as np
 import pytest
@@ -132,9 +133,10 @@ def test_binding_refuses_tensors_of_another_kind(B):
     with pytest.raises(B.SpecTreeError):
         B.spec_tree_kv_commit(cache, lens.long(), torch.zeros((2, 4), dtype=torch.int32), lens.clone(), status)
     with pytest.raises(B.SpecTreeError):
-        B._nodes(B.NodeArrays(None, torch.zeros((2, 4), dtype=torch.int32), None), 2, 0, 1)
+        B.spec_tree_attend(cache, 0, q, q.clone(), None, status,
+                           tree=B.NodeArrays(None, torch.zeros((2, 4), dtype=torch.int32), None))
     with pytest.raises(B.SpecTreeError):
-        B._nodes(B.NodeArrays(torch.zeros((3, 4), dtype=torch.int32)), 2, 0, 1)
+        B.spec_tree_attend(cache, 0, q, q.clone(), None, status, tree=B.NodeArrays(torch.zeros((3, 4), dtype=torch.int32)))
 
 
 def test_structs_match_the_c_header(B, tmp_path):
@@ -159,6 +161,7 @@ def test_structs_match_the_c_header(B, tmp_path):
         assert int(got[st]) == ctypes.sizeof(cls), st
         for f, _ in cls._fields_:
             assert int(got[f"{st}.{f}"]) == getattr(cls, f).offset, (st, f)
+    assert struct.calcsize("@3P3i") <= ctypes.sizeof(B.c_nodes) and struct.calcsize("@P3q") == ctypes.sizeof(B.c_heads)
     assert (int(got["F16"]), int(got["S_PAGES"]), int(got["S_NODES"])) == (B.F16, B.S_PAGES, B.S_NODES)
 
 
