@@ -304,8 +304,11 @@ __device__ __forceinline__ bool odd16(uint32_t h) {  // infinity or NaN in the l
 // ------------------------------------------------------------------- roles ---
 
 // One warp: tokens' keys and values from their pages into the ring, K and V
-// of a tile one after the other.  Lane i copies the tile's i-th page (or its
-// 128 tokens of a larger one); pages past the item's end are not read.
+// of a tile one after the other.  Lane i looks up the tile's i-th page (or the
+// one that its 128 tokens lie in); pages past the item's end are not read.  The
+// copies are issued by one lane from uniform operands: by each lane for its own
+// page they took 80 cycles each, which at 16 tokens a page is 1300 for 32 KB,
+// no faster than the SM's share of the memory's bandwidth.
 template <int D, bool PAIR>
 __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* mk, const CUtensorMap* mv, Control& C,
                                           uint32_t ring) {
@@ -324,15 +327,13 @@ __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* mk, 
     };
     int next = entry(s.first);
     for (int t = s.first; t < s.last; ++t) {
-      const int slot = t * TILE + lane * P.box;
-      const bool mine = lane < boxes && slot < s.end;
       int page = next;
       next = entry(t + 1);
       if (page < 0 || page >= P.L.kv.n_pages) {
         set_status(P.L.status, SPEC_TREE_S_PAGES);
         page = P.L.kv.n_pages;  // outside the pool: the copy fills zeros
       }
-      const int off = slot & (P.L.kv.page_size - 1);
+      const int off = uniform(P.box == TILE ? (t * TILE) & (P.L.kv.page_size - 1) : 0);
       const int used = s.end > 0 ? min(boxes, (s.end - t * TILE + P.box - 1) / P.box) : 0;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv, ++n) {
@@ -343,13 +344,24 @@ __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* mk, 
             mbar_wait(&C.full[o % Y::STAGES], (o / Y::STAGES) & 1);
           return;
         }
-        if (lane == 0) mbar_expect_tx(&C.full[st], used * P.box * 128 * Y::PANELS);
-        __syncwarp();
-        if (mine) {
+        if (elect()) mbar_expect_tx(&C.full[st], used * P.box * 128 * Y::PANELS);
+        const CUtensorMap* map = kv ? mv : mk;
+        const uint32_t to = uniform(ring + st * Y::KV_BYTES), head = uniform(s.head);
+#pragma unroll 1
+        for (int x0 = 0; x0 < used; x0 += 4) {
+          uint32_t pages[4];
 #pragma unroll
-          for (int p = 0; p < Y::PANELS; ++p)
-            tile_g2s(ring + st * Y::KV_BYTES + p * PANEL_BYTES + lane * P.box * 128, kv ? mv : mk, p * PANEL, off,
-                     s.head, page, &C.full[st]);
+          for (int x = 0; x < 4; ++x) pages[x] = __shfl_sync(FULL, page, x0 + x);
+          if (elect()) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (x0 + x < used) {
+#pragma unroll
+                for (int p = 0; p < Y::PANELS; ++p)
+                  tile_g2s(to + p * PANEL_BYTES + (x0 + x) * P.box * 128, map, p * PANEL, off, head, pages[x], &C.full[st]);
+              }
+          }
+          __syncwarp();
         }
       }
     }
