@@ -1,16 +1,17 @@
 // Attention of a tree's nodes over a paged key-value cache (spec_tree_attend).
 //
 // Rows.  The query heads that share a key head, over all nodes of the call,
-// are the rows of one product: row r is node r / group, head r % group.  128
-// rows fill the lanes of one accumulator ("half"); a CTA has two, so that one
-// half's softmax runs under the other half's products:
-//   - calls of more than 128 rows take 256 rows at a time, 128 in each half,
-//     and load keys and values once for both;
-//   - calls of up to 128 rows (PAIR) give both halves the same rows: one takes
+// are the rows of one product: row r is node r / group, head r % group.  The
+// rows of as many whole nodes as 128 lanes have room for fill one accumulator
+// ("half"); a CTA has two, so that one half's softmax runs under the other
+// half's products:
+//   - calls of more rows than a half's take two halves' at a time and load keys
+//     and values once for both;
+//   - calls of no more (PAIR) give both halves the same rows: one takes
 //     the even tiles of a segment, the other the odd ones, and their sums are
 //     put together at its end.
 //
-// Work.  An item is (tree, rows of 128 or 256, key head); its tokens are cut
+// Work.  An item is (tree, one or two halves' rows, key head); its tokens are cut
 // into tiles of 128.  The tiles are dealt to the CTAs (one per SM) in one of
 // two ways:
 //   - ranges: all items' tiles, one after the other, in equal consecutive
@@ -56,28 +57,27 @@ namespace {
 constexpr int TILE = 128;                       // tokens of a tile, rows of a half
 constexpr int PANEL = 64;                       // elements of a 128-byte row
 constexpr int PANEL_BYTES = TILE * 128;         // 128 rows of 64 elements
+constexpr int MAX_SLOTS = 5;                    // of a ring
 constexpr int MASKED_TILES = SPEC_TREE_MAX_NODES / TILE + 2;
 constexpr float LAZY = 8.0f;                    // log2 of what a weight may exceed its reference by
-constexpr int MAX_STAGES = 10;
 constexpr int THREADS = 3 * TILE;               // two softmax warpgroups and one of helpers
 constexpr int HELPERS = 2 * TILE / 32;          // the helpers' first warp
 constexpr int COLUMNS = 512;                    // tensor memory: S of both halves, then O of both
 constexpr int MAX_PIECE_ITEMS = 256;            // (tree, rows) of calls that may be dealt in pieces
 constexpr int JOIN_INSIDE_ROWS = 16;            // rows of calls that need no join kernel
-// Weights are handed to the product in two parts: the last 32 are made while
-// the product works on the first 96, so it does not wait in between (two parts
-// of 64 left a gap: 2920 against 2500 cycles a tile of 256 rows).
-constexpr int EARLY = 96;
+// Weights are handed to the product in two parts, so that it works on the first
+// while the second is made.
+constexpr int EARLY = 64;
 
 struct Plan {
   AttendLaunch L;
-  int group, rows, row_tiles, page_shift, box, ws_rows;
+  int group, rows, half_rows, row_tiles, page_shift, box, ws_rows;
   uint64_t group_inv;  // floor(2^64 / group) + 1, 0 for a group of one
   float scale2;        // |scale| log2(e)
   bool may_piece;      // no more items than CTAs
   bool negative;       // scale < 0: the products take -Q
   bool join_inside;    // no join kernel
-  int q_box;           // nodes of a tiled copy of queries, 0: they are copied row by row
+  int q_box;           // nodes of a copy of queries
 };
 
 // Parts of items: slot 0 of a CTA for one that began before it, slot 1 for one
@@ -104,38 +104,42 @@ __host__ __device__ inline Workspace workspace_of(void* ws, int num_sms, int ws_
 
 template <int D, bool PAIR>
 struct Layout {
-  static constexpr int ROWS = PAIR ? TILE : 2 * TILE;  // rows of an item
+  static constexpr int HALVES = PAIR ? 1 : 2;  // of an item's rows
   static constexpr int PANELS = D / PANEL;
   static constexpr int KV_BYTES = PANELS * PANEL_BYTES;
-  static constexpr int Q_BYTES = (ROWS / TILE) * KV_BYTES;
-  static constexpr int STAGES = (7 * 32768 - Q_BYTES) / KV_BYTES < MAX_STAGES ? (7 * 32768 - Q_BYTES) / KV_BYTES : MAX_STAGES;
+  static constexpr int Q_BYTES = HALVES * KV_BYTES;
+  // tiles that the rings of keys and of values hold: what 7 * 32 KB leave
+  static constexpr int SLOTS = (7 * 32768 - Q_BYTES) / KV_BYTES;
+  static constexpr int KS = (SLOTS + 1) / 2 < MAX_SLOTS ? (SLOTS + 1) / 2 : MAX_SLOTS;
+  static constexpr int VS = SLOTS / 2 < MAX_SLOTS ? SLOTS / 2 : MAX_SLOTS;
+};
+
+// A consecutive piece of an item's tiles: what one CTA does at a time.
+struct Segment {
+  int b, rt, head, row0;   // row0: first row of the item
+  int len, cnt;            // committed tokens, nodes that exist
+  int first, last, tiles;  // tiles first .. last - 1 of `tiles`
+  int end;                 // tokens (slots) the item reads
+  int clear;               // slots below this one are seen by every row of the item
+  int64_t begin;           // where the item begins among all tiles (ranges)
 };
 
 struct Control {
-  uint64_t full[MAX_STAGES], empty[MAX_STAGES], clean[MAX_STAGES];
+  uint64_t k_full[MAX_SLOTS], k_empty[MAX_SLOTS], v_full[MAX_SLOTS], v_empty[MAX_SLOTS], v_clean[MAX_SLOTS];
   uint64_t q_full, q_empty, s_full[2], w_full[2][2], o_full[2], drain;
   uint32_t tmem;
   int abort;
   int64_t scan[THREADS / 32];
-  int64_t total, from, to;  // tiles of the call, and this CTA's range or piece of them
+  int64_t total;            // tiles of the call (ranges)
+  int64_t count;            // this CTA's tiles
   int pieces, piece;        // pieces of this CTA's item (0: ranges), and which one this is
-  int b, rt, head, at;      // where this CTA begins
+  Segment start;            // where this CTA begins
   uint32_t odd[3][MASKED_TILES * (TILE / 32)];  // tokens with a value that is not finite, by segment modulo 3
   uint8_t up[2][SPEC_TREE_MAX_NODES];           // node minus parent, by segment modulo 2; 0: none, 255: more
   union {
     float2 pair[TILE];         // the odd tiles' (reference, sum)
     int tiles[MAX_PIECE_ITEMS];  // setup: tiles of (tree, rows)
   };
-};
-
-// A consecutive piece of an item's tiles: what one CTA does at a time.
-struct Segment {
-  int b, head, row0;     // row0: first row of the item
-  int len, cnt;          // committed tokens, nodes that exist
-  int first, last, tiles;  // tiles first .. last - 1 of `tiles`
-  int64_t begin;         // where the item begins among all tiles (ranges)
-  int end;               // tokens (slots) the item reads
-  int clear;             // slots below this one are seen by every row of the item
 };
 
 // Committed tokens and nodes of tree b; none of either (and a status bit) for
@@ -155,23 +159,33 @@ __device__ __forceinline__ int node_of_row(const Plan& P, int row) {  // row / g
   return P.group_inv ? static_cast<int>(__umul64hi(row, P.group_inv)) : row;
 }
 
-template <int ROWS>
+template <int HALVES>
 __device__ __forceinline__ void item_tiles(const Plan& P, int len, int cnt, int rt, int& end, int& tiles) {
-  const int last_row = min((rt + 1) * ROWS, P.rows) - 1;
+  const int item_rows = HALVES * P.half_rows;
+  const int last_row = min((rt + 1) * item_rows, P.rows) - 1;
   const int nodes = min(cnt, P.L.nodes.begin + node_of_row(P, last_row) + 1);
-  const int first = P.L.nodes.begin + node_of_row(P, rt * ROWS);
+  const int first = P.L.nodes.begin + node_of_row(P, rt * item_rows);
   end = first < cnt ? len + nodes : 0;  // rows of nodes that do not exist read nothing
   tiles = end > 0 ? (end + TILE - 1) / TILE : 1;
 }
 
 // Tiles of one key head of item group x: tree x / row_tiles, rows x % row_tiles.
-template <int ROWS>
+template <int HALVES>
 __device__ __forceinline__ int group_tiles(const Plan& P, int x) {
   const int b = P.row_tiles == 1 ? x : x / P.row_tiles;
   int len, cnt, end, tiles;
   tree_of(P, b, len, cnt);
-  item_tiles<ROWS>(P, len, cnt, x - b * P.row_tiles, end, tiles);
+  item_tiles<HALVES>(P, len, cnt, x - b * P.row_tiles, end, tiles);
   return tiles;
+}
+
+// The item (tree s.b, rows s.rt); its lengths are there already if `known`.
+template <int HALVES>
+__device__ __forceinline__ void set_item(const Plan& P, Segment& s, bool known) {
+  if (!known) tree_of(P, s.b, s.len, s.cnt);
+  s.row0 = s.rt * HALVES * P.half_rows;
+  item_tiles<HALVES>(P, s.len, s.cnt, s.rt, s.end, s.tiles);
+  s.clear = P.L.nodes.parent ? s.len : s.len + min(s.cnt, P.L.nodes.begin + node_of_row(P, s.row0) + 1);
 }
 
 __device__ __forceinline__ int64_t range_start(int64_t total, int c, int ctas) { return total * c / ctas; }
@@ -182,46 +196,31 @@ __device__ __forceinline__ int range_of(int64_t total, int64_t at, int ctas) {
   return range_start(total, c + 1, ctas) <= at ? c + 1 : c;
 }
 
-// The segments of a CTA's range, one after the other; every role walks them
-// for itself.
-template <int ROWS>
+// The segments of a CTA, one after the other; every role walks them for itself.
+template <int HALVES>
 struct Walk {
-  int b, rt, head, at;
+  Segment s;
   int64_t left;
-  int len, cnt;
+  bool fresh = true;
 
-  __device__ __forceinline__ void begin(const Plan& P, const Control& C) {
-    left = C.to - C.from;
-    if (left <= 0) return;
-    b = C.b;
-    rt = C.rt;
-    head = C.head;
-    at = C.at;
-    tree_of(P, b, len, cnt);
-  }
+  __device__ __forceinline__ explicit Walk(const Control& C) : s(C.start), left(C.count) {}
 
-  __device__ __forceinline__ bool next(const Plan& P, const Control& C, Segment& s) {
+  __device__ __forceinline__ bool next(const Plan& P) {
     if (left <= 0) return false;
-    s.b = b;
-    s.head = head;
-    s.row0 = rt * ROWS;
-    s.len = len;
-    s.cnt = cnt;
-    item_tiles<ROWS>(P, len, cnt, rt, s.end, s.tiles);
-    s.clear = P.L.nodes.parent ? len : len + min(cnt, P.L.nodes.begin + node_of_row(P, s.row0) + 1);
-    s.first = at;
-    const int64_t n = min64(left, s.tiles - at);
-    s.last = at + static_cast<int>(n);
-    s.begin = C.to - left - at;
-    left -= n;
-    at = 0;
-    if (s.last == s.tiles && ++head == P.L.kv.n_kv_heads) {
-      head = 0;
-      if (++rt == P.row_tiles) {
-        rt = 0;
-        if (left > 0) tree_of(P, ++b, len, cnt);
+    if (!fresh) {
+      s.first = 0;
+      s.begin += s.tiles;
+      if (++s.head == P.L.kv.n_kv_heads) {
+        s.head = 0;
+        const bool same = ++s.rt < P.row_tiles;
+        if (!same) s.rt = 0, ++s.b;
+        set_item<HALVES>(P, s, same);
       }
     }
+    fresh = false;
+    const int n = static_cast<int>(min64(left, s.tiles - s.first));
+    s.last = s.first + n;
+    left -= n;
     return true;
   }
 };
@@ -303,30 +302,31 @@ __device__ __forceinline__ bool odd16(uint32_t h) {  // infinity or NaN in the l
 
 // ------------------------------------------------------------------- roles ---
 
-// One warp: tokens' keys and values from their pages into the ring, K and V
-// of a tile one after the other.  Lane i looks up the tile's i-th page (or the
-// one that its 128 tokens lie in); pages past the item's end are not read.  The
-// copies are issued by one lane from uniform operands: by each lane for its own
-// page they took 80 cycles each, which at 16 tokens a page is 1300 for 32 KB,
-// no faster than the SM's share of the memory's bandwidth.
-template <int D, bool PAIR>
-__device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* mk, const CUtensorMap* mv, Control& C,
-                                          uint32_t ring) {
+// Two warps, one for keys and one for values: tokens from their pages into the
+// ring.  Lane i looks up the tile's i-th page (or the one that its 128 tokens
+// lie in); pages past the item's end are not read.  A copy takes 70 to 80
+// cycles to issue, whoever issues it, and at 16 tokens a page a tile has 32:
+// by one warp for both, 1300 cycles for 32 KB were no faster than the SM's
+// share of the memory's bandwidth.
+template <int D, bool PAIR, bool KEYS>
+__device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* map, Control& C, uint32_t ring) {
   using Y = Layout<D, PAIR>;
+  constexpr int SLOTS = KEYS ? Y::KS : Y::VS;
+  uint64_t* full = KEYS ? C.k_full : C.v_full;
+  uint64_t* empty = KEYS ? C.k_empty : C.v_empty;
   const int lane = threadIdx.x % 32;
   const int boxes = TILE / P.box;
-  Walk<Y::ROWS> walk;
-  walk.begin(P, C);
-  Segment s;
+  Walk<Y::HALVES> walk(C);
+  const Segment& s = walk.s;
   uint32_t n = 0;  // loads so far
-  while (walk.next(P, C, s)) {
+  while (walk.next(P)) {
     const int32_t* table = P.L.kv.page_table + static_cast<int64_t>(s.b) * P.L.kv.table_stride;
     auto entry = [&](int t) {  // the page of this lane's copy of tile t
       const int slot = t * TILE + lane * P.box;
       return t < s.last && lane < boxes && slot < s.end ? table[slot >> P.page_shift] : 0;
     };
     int next = entry(s.first);
-    for (int t = s.first; t < s.last; ++t) {
+    for (int t = s.first; t < s.last; ++t, ++n) {
       int page = next;
       next = entry(t + 1);
       if (page < 0 || page >= P.L.kv.n_pages) {
@@ -335,34 +335,29 @@ __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* mk, 
       }
       const int off = uniform(P.box == TILE ? (t * TILE) & (P.L.kv.page_size - 1) : 0);
       const int used = s.end > 0 ? min(boxes, (s.end - t * TILE + P.box - 1) / P.box) : 0;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv, ++n) {
-        const int st = n % Y::STAGES;
-        if (!warp_wait(&C.empty[st], ((n / Y::STAGES) & 1) ^ 1, C, P.L.status)) {
-          // copies in flight land before the CTA ends
-          for (uint32_t o = n > Y::STAGES ? n - Y::STAGES : 0; o < n; ++o)
-            mbar_wait(&C.full[o % Y::STAGES], (o / Y::STAGES) & 1);
-          return;
-        }
-        if (elect()) mbar_expect_tx(&C.full[st], used * P.box * 128 * Y::PANELS);
-        const CUtensorMap* map = kv ? mv : mk;
-        const uint32_t to = uniform(ring + st * Y::KV_BYTES), head = uniform(s.head);
+      const int slot = n % SLOTS;
+      if (!warp_wait(&empty[slot], ((n / SLOTS) & 1) ^ 1, C, P.L.status)) {
+        // copies in flight land before the CTA ends
+        for (uint32_t o = n > SLOTS ? n - SLOTS : 0; o < n; ++o) mbar_wait(&full[o % SLOTS], (o / SLOTS) & 1);
+        return;
+      }
+      if (elect()) mbar_expect_tx(&full[slot], used * P.box * 128 * Y::PANELS);
+      const uint32_t to = uniform(ring + slot * Y::KV_BYTES), head = uniform(s.head);
 #pragma unroll 1
-        for (int x0 = 0; x0 < used; x0 += 4) {
-          uint32_t pages[4];
+      for (int x0 = 0; x0 < used; x0 += 4) {
+        uint32_t pages[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) pages[x] = __shfl_sync(FULL, page, x0 + x);
-          if (elect()) {
+        for (int x = 0; x < 4; ++x) pages[x] = __shfl_sync(FULL, page, x0 + x);
+        if (elect()) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (x0 + x < used) {
+          for (int x = 0; x < 4; ++x)
+            if (x0 + x < used) {
 #pragma unroll
-                for (int p = 0; p < Y::PANELS; ++p)
-                  tile_g2s(to + p * PANEL_BYTES + (x0 + x) * P.box * 128, map, p * PANEL, off, head, pages[x], &C.full[st]);
-              }
-          }
-          __syncwarp();
+              for (int p = 0; p < Y::PANELS; ++p)
+                tile_g2s(to + p * PANEL_BYTES + (x0 + x) * P.box * 128, map, p * PANEL, off, head, pages[x], &full[slot]);
+            }
         }
+        __syncwarp();
       }
     }
   }
@@ -371,19 +366,18 @@ __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* mk, 
 // One warp: the products.  The halves take turns, so that while one half's
 // weights are made the other half's products run.  False: a wait gave up.
 template <typename T, int D, bool PAIR>
-__device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t q_smem, uint32_t ring) {
+__device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem) {
   using Y = Layout<D, PAIR>;
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t ID_S = mma_descriptor(BF, TILE, false), ID_O = mma_descriptor(BF, D, true);
   constexpr int KV16 = Y::KV_BYTES / 16, PANEL16 = PANEL_BYTES / 16;  // descriptors count 16 bytes
   const uint32_t tmem = uniform(C.tmem), q_low = uniform(smem_descriptor_low(q_smem, 0));
-  const uint32_t k_low = smem_descriptor_low(ring, 0), v_low = smem_descriptor_low(ring, PANEL_BYTES);
+  const uint32_t k_low = smem_descriptor_low(k_smem, 0), v_low = smem_descriptor_low(v_smem, PANEL_BYTES);
   const uint32_t id_s = uniform(P.negative ? ID_S | MMA_NEGATE_A : ID_S);
   uint32_t* status = P.L.status;
-  Walk<Y::ROWS> walk;
-  walk.begin(P, C);
-  Segment s = {};
-  uint32_t n = 0, segment = 0;   // loads, segments so far
+  Walk<Y::HALVES> walk(C);
+  const Segment& s = walk.s;
+  uint32_t n = 0, segment = 0;   // tiles, segments so far
   uint32_t parity = 0;           // bit h: parity of half h's next weights
   uint32_t clean = 0;            // bit i: parity of slot i's next cleaning
 
@@ -395,10 +389,10 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
     }
     mma_commit(bar);
   };
-  auto ready = [&](uint32_t load) { return warp_wait(&C.full[load % Y::STAGES], (load / Y::STAGES) & 1, C, status); };
-  // S of half h from the keys of a load
-  auto scores = [&](int h, uint32_t load) {
-    const uint32_t a = uniform(q_low + (PAIR ? 0 : h * KV16)), b = uniform(k_low + load % Y::STAGES * KV16);
+  auto keys = [&](uint32_t tile) { return warp_wait(&C.k_full[tile % Y::KS], (tile / Y::KS) & 1, C, status); };
+  // S of half h from a tile's keys
+  auto scores = [&](int h, uint32_t tile) {
+    const uint32_t a = uniform(q_low + (PAIR ? 0 : h * KV16)), b = uniform(k_low + tile % Y::KS * KV16);
     const uint32_t to = uniform(tmem + h * TILE);
     if (elect()) issue_scores(to, a, b, &C.s_full[h]);
     __syncwarp();
@@ -407,13 +401,13 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
     if (elect()) mma_commit(bar);
     __syncwarp();
   };
-  // O of half h from the values of a load, as the weights' two parts come, and,
-  // unless PAIR, right behind it S of its next tile from the keys of load k
-  // (which are then there; k = 0: none)
-  auto output = [&](int h, uint32_t load, bool first, uint32_t k) {
-    const uint32_t b = uniform(v_low + load % Y::STAGES * KV16), add = uniform(!first), more = uniform(k);
+  // O of half h from a tile's values, as the weights' two parts come, and,
+  // unless PAIR, right behind it S from the next tile's keys (which are then
+  // there) if there is one; the values are given back in between
+  auto output = [&](int h, uint32_t tile, bool first, bool last) {
+    const uint32_t b = uniform(v_low + tile % Y::VS * KV16), add = uniform(!first), more = uniform(!last);
     const uint32_t to = uniform(tmem + 2 * TILE + h * D), from = uniform(tmem + h * TILE);
-    const uint32_t qa = uniform(q_low + (PAIR ? 0 : h * KV16)), kb = uniform(k_low + k % Y::STAGES * KV16);
+    const uint32_t qa = uniform(q_low + (PAIR ? 0 : h * KV16)), kb = uniform(k_low + (tile + 1) % Y::KS * KV16);
     if (!warp_wait(&C.w_full[h][0], (parity >> h) & 1, C, status)) return false;
     tmem_fence_after();
     if (elect()) {
@@ -428,6 +422,7 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
 #pragma unroll
       for (int x = EARLY / 16; x < TILE / 16; ++x)
         mma_ts(to, from + x * 8, smem_descriptor(b + x * (16 * 128 / 16)), ID_O, true);
+      if (PAIR || h == 1) mma_commit(&C.v_empty[tile % Y::VS]);
       if (!more)
         mma_commit(&C.o_full[h]);
       else if (!PAIR)
@@ -437,60 +432,56 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
     parity ^= 1u << h;
     return true;
   };
-  // values of tile t, cleaned where not every row sees it whole
-  auto values = [&](int t, uint32_t load) {
-    const uint32_t vs = load % Y::STAGES;
-    if (!ready(load)) return false;
+  // a tile's values (token tile t), cleaned where not every row sees it whole
+  auto values = [&](int t, uint32_t tile) {
+    const uint32_t vs = tile % Y::VS;
+    if (!warp_wait(&C.v_full[vs], (tile / Y::VS) & 1, C, status)) return false;
     if ((t + 1) * TILE > s.clear) {
-      if (!warp_wait(&C.clean[vs], (clean >> vs) & 1, C, status)) return false;
+      if (!warp_wait(&C.v_clean[vs], (clean >> vs) & 1, C, status)) return false;
       clean ^= 1u << vs;
     }
     return true;
   };
 
-  while (walk.next(P, C, s)) {
+  while (walk.next(P)) {
     const int count = s.last - s.first;
-    if (!warp_wait(&C.q_full, segment & 1, C, status) || !ready(n)) return false;
+    if (!warp_wait(&C.q_full, segment & 1, C, status) || !keys(n)) return false;
     tmem_fence_after();
 #pragma unroll 1
     for (int h = 0; h < 2 && (!PAIR || h < count); ++h) {
-      if (PAIR && h == 1 && !ready(n + 2)) return false;
-      scores(h, PAIR ? n + 2 * h : n);
-      if (PAIR) give_back(&C.empty[(n + 2 * h) % Y::STAGES]);
+      if (PAIR && h == 1 && !keys(n + 1)) return false;
+      scores(h, PAIR ? n + h : n);
+      if (PAIR) give_back(&C.k_empty[(n + h) % Y::KS]);
     }
-    if (!PAIR) give_back(&C.empty[n % Y::STAGES]);
+    if (!PAIR) give_back(&C.k_empty[n % Y::KS]);
     if (count <= (PAIR ? 2 : 1)) give_back(&C.q_empty);
     if (PAIR) {
       // tile x by half x % 2; its successor there is tile x + 2
 #pragma unroll 1
       for (int x = 0; x < count; ++x) {
-        const uint32_t v = n + 2 * x + 1, k = n + 2 * (x + 2);
         const bool more = x + 2 < count;
-        if (!values(s.first + x, v) || !output(x & 1, v, x < 2, more ? k : 0)) return false;
-        give_back(&C.empty[v % Y::STAGES]);
+        if (!values(s.first + x, n + x) || !output(x & 1, n + x, x < 2, !more)) return false;
         if (more) {
-          if (!ready(k)) return false;
+          if (!keys(n + x + 2)) return false;
           tmem_fence_after();
-          scores(x & 1, k);
-          give_back(&C.empty[k % Y::STAGES]);
+          scores(x & 1, n + x + 2);
+          give_back(&C.k_empty[(n + x + 2) % Y::KS]);
           if (x + 3 == count) give_back(&C.q_empty);
         }
       }
     } else {
 #pragma unroll 1
       for (int x = 0; x < count; ++x) {
-        const uint32_t v = n + 2 * x + 1, k = v + 1;
         const bool more = x + 1 < count;
-        if (!values(s.first + x, v) || (more && !ready(k))) return false;
+        if (!values(s.first + x, n + x) || (more && !keys(n + x + 1))) return false;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h)
-          if (!output(h, v, x == 0, more ? k : 0)) return false;
-        give_back(&C.empty[v % Y::STAGES]);
-        if (more) give_back(&C.empty[k % Y::STAGES]);
+          if (!output(h, n + x, x == 0, !more)) return false;
+        if (more) give_back(&C.k_empty[(n + x + 1) % Y::KS]);
         if (x + 2 == count) give_back(&C.q_empty);
       }
     }
-    n += 2 * count;
+    n += count;
     ++segment;
   }
   return true;
@@ -513,110 +504,77 @@ __device__ __forceinline__ bool any_odd(const uint4* row, int rotate) {
   return isnan(__low2float(acc)) || isnan(__high2float(acc));
 }
 
-// Two warps, ahead of the softmax: an item's queries and its nodes' parents
-// into shared memory, and the values of tiles that not every row sees whole:
-// those past the item's end and those that are not finite become zeros.  They
-// pass every slot of the ring, so that their waits keep to its phases.
+// One warp, ahead of the softmax: an item's queries and its nodes' parents into
+// shared memory, and the values of tiles that not every row sees whole: those
+// past the item's end and those that are not finite become zeros.  It passes
+// every slot of the values' ring, so that its waits keep to the ring's phases.
 template <typename T, int D, bool PAIR>
-__device__ __forceinline__ void side_role(const Plan& P, const CUtensorMap* mq, Control& C, uint32_t q_smem, uint8_t* ring) {
+__device__ __forceinline__ void side_role(const Plan& P, const CUtensorMap* mq, Control& C, uint32_t q_smem, uint8_t* v_ring) {
   using Y = Layout<D, PAIR>;
-  constexpr int CHUNKS = D / 8, SIDE = 64, STEP = SIDE / CHUNKS;
-  const int t = threadIdx.x % SIDE;
+  constexpr int CHUNKS = D / 8;
+  const int lane = threadIdx.x % 32;
   uint32_t* status = P.L.status;
-  Walk<Y::ROWS> walk;
-  walk.begin(P, C);
-  Segment s;
-  uint32_t segment = 0, n = 0;  // segments, loads so far
-  for (; walk.next(P, C, s); ++segment) {
+  Walk<Y::HALVES> walk(C);
+  const Segment& s = walk.s;
+  uint32_t segment = 0, n = 0;  // segments, tiles so far
+  for (; walk.next(P); ++segment) {
     if (!warp_wait(&C.q_empty, (segment & 1) ^ 1, C, status)) return;
-    if (P.q_box) {
-      if (t == 0) {
-        const int node = node_of_row(P, s.row0);
-        mbar_expect_more(&C.q_full, (Y::ROWS / TILE) * Y::PANELS * P.q_box * P.group * 128);
-        for (int h = 0; h < Y::ROWS / TILE; ++h)
-          for (int p = 0; p < Y::PANELS; ++p)
-            tile_g2s(q_smem + h * Y::KV_BYTES + p * PANEL_BYTES, mq, p * PANEL, s.head * P.group, node + h * node_of_row(P, TILE),
-                     s.b, &C.q_full);
-      }
-      __syncwarp();
-    } else {
-      // what STEP rows on means in nodes and heads
-      const int step_i = node_of_row(P, STEP), step_g = STEP - step_i * P.group;
-      const int64_t step = step_i * P.L.q.node_stride + step_g * P.L.q.head_stride;
-      const int64_t wrap = P.L.q.node_stride - P.group * P.L.q.head_stride;
-      const int rows = min(Y::ROWS, P.rows - s.row0), ch = t % CHUNKS, row = s.row0 + t / CHUNKS;
-      int i = node_of_row(P, row), g = row - i * P.group;
-      const int nodes = s.cnt - P.L.nodes.begin;  // rows of later nodes are zeros
-      const T* base = static_cast<const T*>(P.L.q.data) + s.b * P.L.q.tree_stride +
-                      static_cast<int64_t>(s.head) * P.group * P.L.q.head_stride + ch * 8;
-      const T* from = base + i * P.L.q.node_stride + g * P.L.q.head_stride;
-      const uint32_t to = q_smem + (ch / 8) * PANEL_BYTES;
-#pragma unroll 2
-      for (int r = t / CHUNKS; r < rows; r += STEP) {
-        const bool live = i < nodes;
-        async_copy16(to + (r / TILE) * Y::KV_BYTES + (r % TILE) * 128 + (((ch % 8) ^ (r % 8)) * 16), live ? from : base, !live);
-        i += step_i;
-        g += step_g;
-        from += step;
-        if (g >= P.group) {
-          g -= P.group;
-          ++i;
-          from += wrap;
-        }
-      }
+    const int node = node_of_row(P, s.row0);
+    if (elect()) {
+      mbar_expect_more(&C.q_full, Y::HALVES * Y::PANELS * P.q_box * P.group * 128);
+#pragma unroll
+      for (int h = 0; h < Y::HALVES; ++h)
+#pragma unroll
+        for (int p = 0; p < Y::PANELS; ++p)
+          tile_g2s(q_smem + h * Y::KV_BYTES + p * PANEL_BYTES, mq, p * PANEL, s.head * P.group, node + h * P.q_box, s.b,
+                   &C.q_full);
     }
+    __syncwarp();
     if (P.L.nodes.parent) {
       const int32_t* parent = P.L.nodes.parent + static_cast<int64_t>(s.b) * P.L.nodes.stride;
 #pragma unroll 2
-      for (int x = t; x < s.cnt; x += SIDE) {
+      for (int x = lane; x < s.cnt; x += 32) {
         const int up = parent[x];
         C.up[segment % 2][x] = static_cast<uint8_t>(up < 0 || up >= x ? 0 : min(x - up, 255));
         if (up >= x) set_status(status, SPEC_TREE_S_NODES);
       }
     }
-    if (!P.q_box) {
-      async_copies_wait();
-      fence_proxy_async_smem();
-    }
     warp_arrive(&C.q_full);
 
     const int first_masked = s.clear / TILE;
-    for (int j = s.first; j < s.last; ++j) {
+    for (int j = s.first; j < s.last; ++j, ++n) {
+      const int slot = n % Y::VS;
+      if (!warp_wait(&C.v_full[slot], (n / Y::VS) & 1, C, status)) return;
+      if (j >= first_masked) {
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv, ++n) {
-        const int slot = n % Y::STAGES;
-        if (!warp_wait(&C.full[slot], (n / Y::STAGES) & 1, C, status)) return;
-        if (kv == 1 && j >= first_masked) {
-#pragma unroll 1
-          for (int part = 0; part < 2; ++part) {
-            const int row = part * 64 + t;  // a token
-            uint8_t* at = ring + slot * Y::KV_BYTES + row * 128;
-            bool odd = false;
-            if (j * TILE + row >= s.end) {
+        for (int part = 0; part < TILE / 32; ++part) {
+          const int row = part * 32 + lane;  // a token
+          uint8_t* at = v_ring + slot * Y::KV_BYTES + row * 128;
+          bool odd = false;
+          if (j * TILE + row >= s.end) {
 #pragma unroll 4
-              for (int c = 0; c < CHUNKS; ++c)
-                *reinterpret_cast<uint4*>(at + (c / 8) * PANEL_BYTES + ((c ^ t) % 8) * 16) = make_uint4(0, 0, 0, 0);
-            } else if (j * TILE + row >= s.clear) {  // a token that some rows do not see
+            for (int c = 0; c < CHUNKS; ++c)
+              *reinterpret_cast<uint4*>(at + (c / 8) * PANEL_BYTES + ((c ^ lane) % 8) * 16) = make_uint4(0, 0, 0, 0);
+          } else if (j * TILE + row >= s.clear) {  // a token that some rows do not see
 #pragma unroll 1
-              for (int p = 0; p < Y::PANELS; ++p)
-                odd |= any_odd<T>(reinterpret_cast<const uint4*>(at + p * PANEL_BYTES), t % 8);
-            }
-            const uint32_t word = __ballot_sync(FULL, odd);
-            if (odd) {
-#pragma unroll 1
-              for (int c = 0; c < CHUNKS * 4; ++c) {
-                uint32_t* w = reinterpret_cast<uint32_t*>(at + (c / 32) * PANEL_BYTES) + c % 32;
-                if (odd16<T>(*w)) *w &= 0xffff0000u;
-                if (odd16<T>(*w >> 16)) *w &= 0x0000ffffu;
-              }
-            }
-            if (t % 32 == 0) C.odd[segment % 3][(j - first_masked) * (TILE / 32) + part * 2 + t / 32] = word;
+            for (int p = 0; p < Y::PANELS; ++p)
+              odd |= any_odd<T>(reinterpret_cast<const uint4*>(at + p * PANEL_BYTES), lane % 8);
           }
-          fence_proxy_async_smem();
-          warp_arrive(&C.clean[slot]);
+          const uint32_t word = __ballot_sync(FULL, odd);
+          if (odd) {
+#pragma unroll 1
+            for (int c = 0; c < CHUNKS * 4; ++c) {
+              uint32_t* w = reinterpret_cast<uint32_t*>(at + (c / 32) * PANEL_BYTES) + c % 32;
+              if (odd16<T>(*w)) *w &= 0xffff0000u;
+              if (odd16<T>(*w >> 16)) *w &= 0x0000ffffu;
+            }
+          }
+          if (lane == 0) C.odd[segment % 3][(j - first_masked) * (TILE / 32) + part] = word;
         }
-        warp_arrive(&C.empty[slot]);
+        fence_proxy_async_smem();
+        warp_arrive(&C.v_clean[slot]);
       }
+      warp_arrive(&C.v_empty[slot]);
     }
   }
 }
@@ -656,7 +614,7 @@ __device__ __noinline__ void add_odd(const Plan& P, const Segment& s, const uint
 template <typename T, int D>
 __device__ __forceinline__ void join_rows(const Plan& P, const Workspace& ws, const JoinRecord& rec, int cnt, int from,
                                           int x, int threads) {
-  const int rows = min(P.ws_rows, P.rows - rec.row0);
+  const int rows = min(P.ws_rows, P.rows - rec.row0);  // ws_rows: of a whole item
   // a thread keeps to one row; neighbours have neighbouring rows
   int spread = 1;
   while (spread < rows && spread < threads) spread *= 2;
@@ -724,16 +682,16 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
   const uint32_t tm_s = C.tmem + half * TILE + lanes, tm_o = C.tmem + 2 * TILE + half * D + lanes;
   uint32_t* status = P.L.status;
-  Walk<Y::ROWS> walk;
-  walk.begin(P, C);
-  Segment s;
+  Walk<Y::HALVES> walk(C);
+  const Segment& s = walk.s;
   uint32_t tile = 0, segment = 0, ends = 0;  // tiles of this half, segments, segments with a tile of this half so far
   bool ok = true;  // uniform over the warp; a warp that has given up still meets the others at barriers
-  for (; walk.next(P, C, s); ++segment) {
-    const int local = (PAIR ? 0 : half * TILE) + t, row = s.row0 + local;
+  for (; walk.next(P); ++segment) {
+    const int local = (PAIR ? 0 : half * P.half_rows) + t, row = s.row0 + local;
+    const bool in_call = t < P.half_rows && row < P.rows;
     const int i = node_of_row(P, row), g = row - i * P.group;
     const int node = P.L.nodes.begin + i;
-    const bool live = row < P.rows && node < s.cnt;
+    const bool live = in_call && node < s.cnt;
     const bool warp_live = __any_sync(FULL, live);
     const int first_masked = s.clear / TILE;  // tiles from here on are not seen whole by every row
     float ref = -INFINITY, sum = 0.0f;
@@ -808,13 +766,12 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
 #pragma unroll
         for (int c = 0; c < EARLY; c += 2) weigh(c);
         tmem_st32(tm_s, x);
-        tmem_st16(tm_s + 32, x + 32);
         tmem_wait_st();
         tmem_fence_before();
         warp_arrive(&C.w_full[half][0]);
 #pragma unroll
         for (int c = EARLY; c < TILE; c += 2) weigh(c);
-        tmem_st16(tm_s + EARLY / 2, x + EARLY / 2);
+        tmem_st32(tm_s + EARLY / 2, x + EARLY / 2);
         tmem_wait_st();
         tmem_fence_before();
         float a, b;
@@ -851,7 +808,7 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
     } else if (PAIR && half == 1) {
       continue;
     }
-    if (!ok || s.row0 + local - t + warp * 32 >= P.rows) {
+    if (!ok || !__any_sync(FULL, in_call)) {
       if (both) warps_meet(5 + warp, 64);
       continue;
     }
@@ -886,7 +843,7 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
             partial[(c * 8 + q) * P.ws_rows] = make_float4(__uint_as_float(o[q * 4]), __uint_as_float(o[q * 4 + 1]),
                                                            __uint_as_float(o[q * 4 + 2]), __uint_as_float(o[q * 4 + 3]));
         }
-      } else if (row < P.rows) {
+      } else if (in_call) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float y[8];
@@ -901,13 +858,14 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
       uint32_t odd = 0;
       for (int x = (from - first_masked) * (TILE / 32); x < (s.last - first_masked) * (TILE / 32); ++x)
         odd |= C.odd[segment % 3][x];
+      const Segment copy = s;  // the callee takes its address, and s is to stay in registers
       if (odd && live)
-        add_odd<T, D>(P, s, C.odd[segment % 3], from, node, whole ? out : nullptr, reinterpret_cast<float*>(partial));
+        add_odd<T, D>(P, copy, C.odd[segment % 3], from, node, whole ? out : nullptr, reinterpret_cast<float*>(partial));
     }
     if (!whole && live) ws.sums[part * P.ws_rows + local] = make_float2(ref, sum);
     tmem_fence_before();
     if (both) warps_meet(5 + warp, 64);
-    if (!whole && local < 32 && (P.join_inside || s.first == 0)) {  // one warp
+    if (!whole && local - lane == 0 && (P.join_inside || s.first == 0)) {  // one warp
       int from, parts;
       if (C.pieces) {
         from = cta - C.piece;
@@ -935,13 +893,13 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
 }
 
 // Where this CTA's range begins: a scan of all items' tiles over all threads.
-template <int ROWS>
+template <int HALVES>
 __device__ __forceinline__ void find_range(const Plan& P, Control& C, int warp, int cta) {
   const int groups = P.L.B * P.row_tiles, per = (groups + THREADS - 1) / THREADS, heads = P.L.kv.n_kv_heads;
   const int x0 = min(groups, static_cast<int>(threadIdx.x) * per), x1 = min(groups, x0 + per);
   int64_t mine = 0;
 #pragma unroll 1
-  for (int x = x0; x < x1; ++x) mine += group_tiles<ROWS>(P, x);
+  for (int x = x0; x < x1; ++x) mine += group_tiles<HALVES>(P, x);
   mine *= heads;
   int64_t before = mine;
 #pragma unroll
@@ -962,21 +920,23 @@ __device__ __forceinline__ void find_range(const Plan& P, Control& C, int warp, 
   const int64_t from = range_start(total, min(cta, ctas), ctas), to = range_start(total, min(cta + 1, ctas), ctas);
   if (threadIdx.x == 0) {
     C.total = total;
-    C.from = from;
-    C.to = to;
+    C.count = to - from;
     C.pieces = 0;
   }
   if (from < to && before <= from && from < before + mine) {
     int64_t skip = from - before;
     int x = x0, tiles;
-    while (skip >= static_cast<int64_t>(tiles = group_tiles<ROWS>(P, x)) * heads) {
+    while (skip >= static_cast<int64_t>(tiles = group_tiles<HALVES>(P, x)) * heads) {
       skip -= static_cast<int64_t>(tiles) * heads;
       ++x;
     }
-    C.b = x / P.row_tiles;
-    C.rt = x % P.row_tiles;
-    C.head = static_cast<int>(skip / tiles);
-    C.at = static_cast<int>(skip % tiles);
+    Segment& s = C.start;
+    s.b = x / P.row_tiles;
+    s.rt = x - s.b * P.row_tiles;
+    s.head = static_cast<int>(skip / tiles);
+    s.first = static_cast<int>(skip - static_cast<int64_t>(s.head) * tiles);
+    s.begin = from - s.first;
+    set_item<HALVES>(P, s, false);
   }
 }
 
@@ -993,10 +953,10 @@ __device__ __forceinline__ int pieces_of(int tiles, float inv) {
 // those for which there are CTAs enough (one lane tries one of 32 lengths), and
 // this CTA's piece.  False: ranges, which always have parts to join and begin
 // and end inside items, cost less.
-template <int ROWS, bool PAIR>
+template <int HALVES>
 __device__ __forceinline__ bool find_piece(const Plan& P, Control& C, int warp, int cta) {
   const int items = P.L.B * P.row_tiles, heads = P.L.kv.n_kv_heads, lane = threadIdx.x % 32;
-  for (int x = threadIdx.x; x < items; x += THREADS) C.tiles[x] = group_tiles<ROWS>(P, x);
+  for (int x = threadIdx.x; x < items; x += THREADS) C.tiles[x] = group_tiles<HALVES>(P, x);
   __syncthreads();
   int sum = 0, most = 1;  // 2^31 slots at most in a tree: 2^24 tiles in each of 2^8 items
   float total = 0.0f;
@@ -1006,17 +966,18 @@ __device__ __forceinline__ bool find_piece(const Plan& P, Control& C, int warp, 
   }
   total = warp_sum(total) * heads;
   most = __reduce_max_sync(FULL, most);
-  constexpr float JOIN = JOIN_COST / (PAIR ? 1.0f : 2.0f), ENDS = ENDS_COST / (PAIR ? 1.0f : 2.0f);
-  const float fair = total / gridDim.x;
+  constexpr float JOIN = JOIN_COST / HALVES, ENDS = ENDS_COST / HALVES;
+  const float fair = __fdividef(total, static_cast<float>(gridDim.x));
   const int least = max(1, static_cast<int>(fair));
-  const float inv = 1.0f / (least + static_cast<float>(max(0, most - least)) * lane / 31.0f);
+  const float inv = __fdividef(1.0f, least + static_cast<float>(max(0, most - least)) * lane * (1.0f / 31.0f));
   float longest = 0.0f;
   bool split = false;
+#pragma unroll 4
   for (int x = 0; x < items; ++x) {
     const int n = pieces_of(C.tiles[x], inv);
     sum += n;
     split |= n > 1;
-    longest = fmaxf(longest, static_cast<float>(C.tiles[x]) / n);
+    longest = fmaxf(longest, __fdividef(static_cast<float>(C.tiles[x]), static_cast<float>(n)));
   }
   // the longest length leaves every item whole, so one is always possible
   const float cost = sum * heads <= static_cast<int>(gridDim.x) ? longest + (split ? JOIN : 0.0f) : INFINITY;
@@ -1032,17 +993,20 @@ __device__ __forceinline__ bool find_piece(const Plan& P, Control& C, int warp, 
       if (skip < n * heads) break;
       skip -= n * heads;
     }
-    C.from = C.to = 0;
+    C.count = 0;
     C.pieces = n;
-    C.piece = n ? skip % n : 0;
     if (x < items) {
-      const int64_t tiles = C.tiles[x], q = skip % n;
-      C.b = x / P.row_tiles;
-      C.rt = x % P.row_tiles;
-      C.head = skip / n;
-      C.at = static_cast<int>(tiles * q / n);
-      C.from = C.at;
-      C.to = tiles * (q + 1) / n;
+      // fewer than 2^8 pieces of at most 2^24 tiles
+      const uint32_t tiles = C.tiles[x], head = static_cast<uint32_t>(skip) / n, q = skip - head * n;
+      Segment& s = C.start;
+      C.piece = q;
+      s.b = P.row_tiles == 1 ? x : x / P.row_tiles;
+      s.rt = x - s.b * P.row_tiles;
+      s.head = head;
+      s.first = tiles * q / n;
+      s.begin = 0;
+      C.count = tiles * (q + 1) / n - s.first;
+      set_item<HALVES>(P, s, false);
     }
   }
   return true;
@@ -1054,16 +1018,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                   const __grid_constant__ CUtensorMap mq) {
   using Y = Layout<D, PAIR>;
   extern __shared__ __align__(1024) uint8_t smem[];  // nothing static, so it starts on a swizzle group
-  uint8_t* ring = smem + Y::Q_BYTES;
-  Control& C = *reinterpret_cast<Control*>(ring + Y::STAGES * Y::KV_BYTES);
+  uint8_t* k_ring = smem + Y::Q_BYTES;
+  uint8_t* v_ring = k_ring + Y::KS * Y::KV_BYTES;
+  Control& C = *reinterpret_cast<Control*>(v_ring + Y::VS * Y::KV_BYTES);
   const int warp = __shfl_sync(FULL, threadIdx.x / 32, 0), cta = blockIdx.x;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Y::STAGES; ++i) {
-      mbar_init(&C.full[i], 1);
-      mbar_init(&C.empty[i], 3);  // the products' commit and the side warps
-      mbar_init(&C.clean[i], 2);
+    for (int i = 0; i < MAX_SLOTS; ++i) {
+      mbar_init(&C.k_full[i], 1);
+      mbar_init(&C.k_empty[i], 1);
+      mbar_init(&C.v_full[i], 1);
+      mbar_init(&C.v_empty[i], 2);  // the products' commit and the side warp
+      mbar_init(&C.v_clean[i], 1);
     }
-    mbar_init(&C.q_full, 2);
+    mbar_init(&C.q_full, 1);
     mbar_init(&C.q_empty, 1);
     mbar_init(&C.drain, 1);
     for (int h = 0; h < 2; ++h) {
@@ -1076,9 +1043,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_mbar_init();
   }
   if (warp == HELPERS) tmem_alloc(&C.tmem, COLUMNS);
+  if (threadIdx.x == THREADS - 1) {
+    prefetch_map(&mk);
+    prefetch_map(&mv);
+    prefetch_map(&mq);
+  }
   grid_dependency_wait();
   grid_dependents_launch();
-  if (!P.may_piece || !find_piece<Y::ROWS, PAIR>(P, C, warp, cta)) find_range<Y::ROWS>(P, C, warp, cta);
+  if (!P.may_piece || !find_piece<Y::HALVES>(P, C, warp, cta)) find_range<Y::HALVES>(P, C, warp, cta);
   if (threadIdx.x == 0 && !P.join_inside) workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows).records[cta].parts = 0;
   if (cta == 0)
     for (int b = threadIdx.x; b < P.L.B; b += THREADS) {
@@ -1097,14 +1069,16 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == HELPERS) {
-      load_role<D, PAIR>(P, &mk, &mv, C, smem_u32(ring));
+      load_role<D, PAIR, true>(P, &mk, C, smem_u32(k_ring));
     } else if (warp == HELPERS + 1) {
-      if (!product_role<T, D, PAIR>(P, C, smem_u32(smem), smem_u32(ring))) {
+      load_role<D, PAIR, false>(P, &mv, C, smem_u32(v_ring));
+    } else if (warp == HELPERS + 2) {
+      if (!product_role<T, D, PAIR>(P, C, smem_u32(smem), smem_u32(k_ring), smem_u32(v_ring))) {
         if (elect()) mma_commit(&C.drain);  // products in flight end before their memory is given back
         mbar_wait(&C.drain, 0);
       }
     } else {
-      side_role<T, D, PAIR>(P, &mq, C, smem_u32(smem), ring);
+      side_role<T, D, PAIR>(P, &mq, C, smem_u32(smem), v_ring);
     }
   }
   __syncwarp();
@@ -1156,8 +1130,9 @@ bool tiled_map(CUtensorMap* map, int dtype, const void* base, const cuuint64_t (
                int box1, int box2) {
   const EncodeTiled fn = encode_tiled();
   if (fn == nullptr) return false;
-  const cuuint64_t bytes[3] = {static_cast<cuuint64_t>(strides[0]) * 2, static_cast<cuuint64_t>(strides[1]) * 2,
-                               static_cast<cuuint64_t>(strides[2]) * 2};
+  cuuint64_t bytes[3];
+  for (int i = 0; i < 3; ++i)  // the stride of a single entry means nothing
+    bytes[i] = dims[i + 1] == 1 ? 16 : static_cast<cuuint64_t>(strides[i]) * 2;
   const cuuint32_t boxes[4] = {PANEL, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2), 1}, steps[4] = {1, 1, 1, 1};
   return fn(map, dtype == SPEC_TREE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
             const_cast<void*>(base), dims, bytes, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1181,28 +1156,20 @@ bool query_map(CUtensorMap* map, const Plan& P) {
   return tiled_map(map, P.L.kv.dtype, P.L.q.data, dims, strides, P.group, P.q_box);
 }
 
-// Whether queries can be copied by a tensor map: the heads of whole nodes fill
-// a half, and strides are what a map takes.
-bool tiled_queries(const Plan& P) {
-  const int64_t strides[3] = {P.L.q.head_stride, P.L.q.node_stride, P.L.q.tree_stride};
-  for (int64_t x : strides)
-    if (x <= 0 || x >= (1ll << 38)) return false;
-  return TILE % P.group == 0;
-}
-
 template <typename T, int D, bool PAIR>
 cudaError_t attend(Plan& P, cudaStream_t stream) {
   using Y = Layout<D, PAIR>;
-  constexpr int SMEM = Y::Q_BYTES + Y::STAGES * Y::KV_BYTES + static_cast<int>(sizeof(Control));
+  constexpr int SMEM = Y::Q_BYTES + (Y::KS + Y::VS) * Y::KV_BYTES + static_cast<int>(sizeof(Control));
   static_assert(SMEM <= 232448, "shared memory of one CTA");
   static_assert(2 * (TILE + D) <= COLUMNS, "tensor memory");
-  P.row_tiles = (P.rows + Y::ROWS - 1) / Y::ROWS;
+  const int item_rows = Y::HALVES * P.half_rows;
+  P.row_tiles = (P.rows + item_rows - 1) / item_rows;
+  P.ws_rows = std::min(P.rows, item_rows);
   const int64_t items = static_cast<int64_t>(P.L.B) * P.row_tiles;
   P.may_piece = items * P.L.kv.n_kv_heads <= P.L.num_sms && items <= MAX_PIECE_ITEMS;
-  P.q_box = tiled_queries(P) ? std::min(TILE / P.group, P.L.nodes.count) : 0;
-  CUtensorMap mk, mv, mq = {};
+  CUtensorMap mk, mv, mq;
   if (!pool_map(&mk, P.L.kv, P.L.kv.k, P.L.layer, P.box) || !pool_map(&mv, P.L.kv, P.L.kv.v, P.L.layer, P.box) ||
-      (P.q_box && !query_map(&mq, P)))
+      !query_map(&mq, P))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> prepared{0};  // devices that know the kernel's shared memory
   int device = 0;
@@ -1221,7 +1188,7 @@ cudaError_t attend(Plan& P, cudaStream_t stream) {
 
 template <typename T, int D>
 cudaError_t attend_rows(Plan& P, cudaStream_t stream) {
-  return P.rows > TILE ? attend<T, D, false>(P, stream) : attend<T, D, true>(P, stream);
+  return P.rows > P.half_rows ? attend<T, D, false>(P, stream) : attend<T, D, true>(P, stream);
 }
 
 int workspace_rows(int64_t rows) { return static_cast<int>(min64(rows, 2 * TILE)); }
@@ -1238,9 +1205,10 @@ cudaError_t launch_attend(const AttendLaunch& L, cudaStream_t stream) {
   P.L = L;
   P.group = L.n_q_heads / L.kv.n_kv_heads;
   P.rows = L.nodes.count * P.group;
+  P.half_rows = TILE / P.group * P.group;
+  P.q_box = std::min(TILE / P.group, L.nodes.count);
   P.page_shift = log2_of(L.kv.page_size);
   P.box = L.kv.page_size < TILE ? L.kv.page_size : TILE;
-  P.ws_rows = workspace_rows(P.rows);
   P.join_inside = P.rows <= JOIN_INSIDE_ROWS;
   // a scale of zero would turn -inf into NaN: weights 2^(1e-30 S) are all one as well
   P.scale2 = fminf(fmaxf(fabsf(L.scale) * 1.4426950408889634f, 1e-30f), 3e38f);

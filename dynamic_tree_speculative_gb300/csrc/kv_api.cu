@@ -12,6 +12,8 @@ namespace {
 constexpr int MAX_CHAIN = 1 << 20;
 constexpr int MAX_HEADS = 1 << 14;
 constexpr int MAX_TREES = 65535;
+constexpr int MAX_GROUP = 128;            // query heads of a key head
+constexpr int64_t MAX_STRIDE = 1ll << 38;  // elements
 
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
@@ -30,7 +32,7 @@ int check_kv(int B, const spec_tree_kv_t* kv, int layer) {
   if (!aligned16(kv->k) || !aligned16(kv->v)) return SPEC_TREE_E_LAYOUT;
   const int64_t st[4] = {kv->layer_stride, kv->page_stride, kv->token_stride, kv->head_stride};
   for (int64_t x : st)
-    if (x < 0 || x % 8 != 0 || x >= (1ll << 38)) return SPEC_TREE_E_LAYOUT;
+    if (x < 0 || x % 8 != 0 || x >= MAX_STRIDE) return SPEC_TREE_E_LAYOUT;
   return SPEC_TREE_OK;
 }
 
@@ -44,8 +46,10 @@ int check_nodes(const spec_tree_nodes_t* n, bool need_depth) {
 
 int check_heads(const spec_tree_heads_t* h) {
   if (h == nullptr || h->data == nullptr) return SPEC_TREE_E_PARAM;
-  if (!aligned16(h->data) || h->tree_stride % 8 != 0 || h->node_stride % 8 != 0 || h->head_stride % 8 != 0)
-    return SPEC_TREE_E_LAYOUT;
+  if (!aligned16(h->data)) return SPEC_TREE_E_LAYOUT;
+  const int64_t st[3] = {h->tree_stride, h->node_stride, h->head_stride};
+  for (int64_t x : st)
+    if (x < 0 || x % 8 != 0 || x >= MAX_STRIDE) return SPEC_TREE_E_LAYOUT;
   return SPEC_TREE_OK;
 }
 
@@ -101,7 +105,7 @@ int spec_tree_kv_append(int B, const spec_tree_kv_t* kv, int layer, const spec_t
 
 size_t spec_tree_attend_workspace_bytes(int B, int count, int n_q_heads, int n_kv_heads, int head_dim) {
   if (B < 1 || count < 1 || count > MAX_CHAIN || n_kv_heads < 1 || n_q_heads < n_kv_heads || n_q_heads > MAX_HEADS ||
-      n_q_heads % n_kv_heads != 0 || (head_dim != 64 && head_dim != 128))
+      n_q_heads % n_kv_heads != 0 || n_q_heads / n_kv_heads > MAX_GROUP || (head_dim != 64 && head_dim != 128))
     return 0;
   const int sms = st::num_sms_of_current_device();
   return sms <= 0 ? 0 : st::attend_workspace_bytes(sms, static_cast<int64_t>(count) * (n_q_heads / n_kv_heads), head_dim);
@@ -114,7 +118,7 @@ int spec_tree_attend(int B, const spec_tree_kv_t* kv, int layer, const spec_tree
   if (rc) return rc;
   if ((rc = check_nodes(nodes, false))) return rc;
   if (n_q_heads < kv->n_kv_heads || n_q_heads > MAX_HEADS || n_q_heads % kv->n_kv_heads != 0 ||
-      static_cast<int64_t>(B) * nodes->count * n_q_heads > (1 << 30))
+      n_q_heads / kv->n_kv_heads > MAX_GROUP || static_cast<int64_t>(B) * nodes->count * n_q_heads > (1 << 30))
     return SPEC_TREE_E_PARAM;
   if ((rc = check_heads(q)) || (rc = check_heads(out))) return rc;
   if (!isfinite(scale) || workspace == nullptr || q->data == out->data) return SPEC_TREE_E_PARAM;

@@ -53,14 +53,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
 // ---------------------------------------------------------------- products ---
 
 // Instruction descriptor of a 16-bit product with float32 sums: M = 128, N
@@ -135,12 +127,9 @@ __device__ __forceinline__ void tile_g2s(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// 16 bytes global -> shared, or zeros; complete after async_copies_wait().
-__device__ __forceinline__ void async_copy16(uint32_t dst, const void* src, bool zeros) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(zeros ? 0 : 16) : "memory");
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
-
-__device__ __forceinline__ void async_copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Bytes that the current phase of `bar` is to wait for, without an arrival.
 __device__ __forceinline__ void mbar_expect_more(uint64_t* bar, uint32_t bytes) {

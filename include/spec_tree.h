@@ -476,7 +476,7 @@ typedef struct spec_tree_kv_t {
 
 /* Vectors of head_dim elements per (tree, node of the call, head): element d
  * at data[b * tree_stride + i * node_stride + h * head_stride + d].  16-byte
- * aligned, strides multiples of 8 elements. */
+ * aligned, strides >= 0 and multiples of 8 elements. */
 typedef struct spec_tree_heads_t {
   void* data;
   int64_t tree_stride, node_stride, head_stride;
@@ -537,7 +537,7 @@ int spec_tree_kv_append(int B, const spec_tree_kv_t* kv, int layer, const spec_t
  * included).  A node that does not exist, or that sees no score above -inf,
  * gets zeros.
  *   q, out: n_q_heads vectors per node of kv->dtype, n_q_heads a multiple of
- *           n_kv_heads; out must not overlap q.
+ *           n_kv_heads, 1 to 128 times it; out must not overlap q.
  *   scale:  finite, usually head_dim^-0.5.
  *   workspace: device, spec_tree_attend_workspace_bytes() bytes, 16-byte
  *           aligned, zero before the first call that uses it; every call
