@@ -188,11 +188,16 @@ __device__ __forceinline__ void set_item(const Plan& P, Segment& s, bool known) 
   s.clear = P.L.nodes.parent ? s.len : s.len + min(s.cnt, P.L.nodes.begin + node_of_row(P, s.row0) + 1);
 }
 
-__device__ __forceinline__ int64_t range_start(int64_t total, int c, int ctas) { return total * c / ctas; }
+// Where range c of `ctas` (at most 2^8) begins, and the range that holds tile
+// `at`.  64-bit divisions are long: there are seldom tiles enough for them.
+__device__ __forceinline__ int64_t range_start(int64_t total, int c, int ctas) {
+  if (total < 1 << 24) return static_cast<uint32_t>(total) * c / ctas;
+  return total * c / ctas;
+}
 
-// The CTA whose range holds tile `at`.
 __device__ __forceinline__ int range_of(int64_t total, int64_t at, int ctas) {
-  const int c = static_cast<int>(at * ctas / total);
+  const int c = total < 1 << 24 ? static_cast<uint32_t>(at) * ctas / static_cast<uint32_t>(total)
+                                : static_cast<int>(at * ctas / total);
   return range_start(total, c + 1, ctas) <= at ? c + 1 : c;
 }
 
@@ -622,45 +627,52 @@ __device__ __forceinline__ void join_rows(const Plan& P, const Workspace& ws, co
   if (local >= rows) return;
   const int i = node_of_row(P, row), g = row - i * P.group;
   const bool live = P.L.nodes.begin + i < cnt;
-  // part p: slot 1 of the first CTA, slot 0 of the next ones
-  auto slot = [&](int p) { return static_cast<int64_t>(from + p) * 2 + (p == 0 ? 1 : 0); };
-  float top = -INFINITY, sum = 0.0f;
-  if (live) {
-#pragma unroll 4
-    for (int p = 0; p < rec.parts; ++p) top = fmaxf(top, __ldcg(&ws.sums[slot(p) * P.ws_rows + local].x));
-  }
-  const float sub = top == -INFINITY ? 0.0f : top;
-  if (live) {
-#pragma unroll 4
-    for (int p = 0; p < rec.parts; ++p) {
-      const float2 ms = __ldcg(&ws.sums[slot(p) * P.ws_rows + local]);
-      sum += ms.y * ex2(ms.x - sub);
-    }
-  }
-  const bool some = live && sum != 0.0f;
-  const float inv = some ? 1.0f / sum : 0.0f;
   T* out = static_cast<T*>(P.L.out.data) + rec.b * P.L.out.tree_stride + i * P.L.out.node_stride +
            (static_cast<int64_t>(rec.head) * P.group + g) * P.L.out.head_stride;
-  constexpr int BATCH = 4;
+  // BATCH quads of PARTS parts at a time: their loads are in flight together
+  constexpr int BATCH = 4, PARTS = 4;
   const int step = threads / spread;
 #pragma unroll 1
   for (int q0 = x / spread; q0 < D / 4; q0 += BATCH * step) {
     float4 acc[BATCH];
+    float top = -INFINITY, sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < BATCH; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (some) {
-#pragma unroll 4
-      for (int p = 0; p < rec.parts; ++p) {
-        const float f = ex2(__ldcg(&ws.sums[slot(p) * P.ws_rows + local].x) - sub);
-        const float4* part = ws.out + slot(p) * (D / 4) * P.ws_rows + local;
+#pragma unroll 1
+    for (int p0 = 0; live && p0 < rec.parts; p0 += PARTS) {
+      float2 ms[PARTS];
+      float4 y[PARTS][BATCH];
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        // part p: slot 1 of the first CTA, slot 0 of the next ones
+        const int64_t slot = static_cast<int64_t>(from + p0 + p) * 2 + (p0 + p == 0 ? 1 : 0);
+        const float4* part = ws.out + slot * (D / 4) * P.ws_rows + local;
+        const bool there = p0 + p < rec.parts;
+        ms[p] = there ? __ldcg(&ws.sums[slot * P.ws_rows + local]) : make_float2(-INFINITY, 0.0f);
 #pragma unroll
         for (int e = 0; e < BATCH; ++e) {
           const int q = q0 + e * step;
-          const float4 y = q < D / 4 ? __ldcg(part + q * P.ws_rows) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          acc[e].x += y.x * f, acc[e].y += y.y * f, acc[e].z += y.z * f, acc[e].w += y.w * f;
+          y[p][e] = there && q < D / 4 ? __ldcg(part + q * P.ws_rows) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
       }
+      float next = top;
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) next = fmaxf(next, ms[p].x);
+      const float sub = next == -INFINITY ? 0.0f : next, keep = ex2(top - sub);
+      top = next;
+      sum *= keep;
+#pragma unroll
+      for (int e = 0; e < BATCH; ++e) acc[e].x *= keep, acc[e].y *= keep, acc[e].z *= keep, acc[e].w *= keep;
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        const float f = ex2(ms[p].x - sub);
+        sum += ms[p].y * f;
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e)
+          acc[e].x += y[p][e].x * f, acc[e].y += y[p][e].y * f, acc[e].z += y[p][e].z * f, acc[e].w += y[p][e].w * f;
+      }
     }
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;  // no sum: zeros, as acc is
 #pragma unroll
     for (int e = 0; e < BATCH; ++e) {
       const int q = q0 + e * step;
@@ -699,22 +711,27 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
     for (int j = s.first + (PAIR ? half : 0); j < s.last; j += EACH, ++tile) {
       const int base = j * TILE;
       const bool masked = base + TILE > s.clear;
+      Seen v;
+      // while the scores are made; a segment's first ones say that its parents are there
+      if (masked && j < s.first + EACH) ok = ok && warp_wait(&C.s_full[half], tile & 1, C, status);
+      if (masked && live) {
+        const int32_t* parent = P.L.nodes.parent + static_cast<int64_t>(s.b) * P.L.nodes.stride;
+        v = seen_of(P, s, node, base, [&](int n) {
+          const int up = C.up[segment % 2][n];
+          return up == 0 ? -1 : (up == 255 ? parent[n] : n - up);
+        });
+      }
       ok = ok && warp_wait(&C.s_full[half], tile & 1, C, status);
       if (warp_live && ok) {
         tmem_fence_after();
         uint32_t x[TILE];
         if (masked) {
-          const int32_t* parent = P.L.nodes.parent + static_cast<int64_t>(s.b) * P.L.nodes.stride;
-          const Seen v = seen_of(P, s, live ? node : -1, base, [&](int n) {
-            const int up = C.up[segment % 2][n];
-            return up == 0 ? -1 : (up == 255 ? parent[n] : n - up);
-          });
 #pragma unroll 1
           for (int c = 0; c < TILE / 32; ++c) {
-            __syncwarp();
+            const uint32_t word = live ? v.get(c) : 0xffffffffu;
+            if (__all_sync(FULL, word == 0xffffffffu)) continue;
             tmem_ld32(tm_s + c * 32, x);
             tmem_wait_ld();
-            const uint32_t word = v.get(c);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!((word >> e) & 1)) x[e] = 0xff800000u;
