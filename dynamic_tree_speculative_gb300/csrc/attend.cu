@@ -23,10 +23,12 @@
 //     below a range's length and two.
 // An item that one CTA has whole is finished there; otherwise each CTA leaves
 // its sums, their reference and its unnormalised output in the workspace, and
-// the parts are put together in the item's order: by attend_join_kernel, or,
-// for calls of up to 16 rows, by whichever CTA is the last to leave its part
-// (a launch less: @@; of many rows the join is long for one warp,
-// and the launch, over all SMs, is faster).
+// the parts are put together in the item's order:
+//   - calls of up to 16 rows: by whichever CTA is the last to leave its part
+//     (which saves a launch; of many rows the join is long for one CTA);
+//   - ranges: by the item's first CTA as it comes to its own part, if the
+//     others have left theirs, as they nearly always have;
+//   - else by attend_join_kernel, over all SMs.
 //
 // Tile.  S = Q K^T in tensor memory (128 lanes: one row per softmax thread);
 // weights w = 2^(scale S - ref), rounded to the cache's type and stored over
@@ -64,6 +66,7 @@ constexpr int THREADS = 3 * TILE;               // two softmax warpgroups and on
 constexpr int HELPERS = 2 * TILE / 32;          // the helpers' first warp
 constexpr int COLUMNS = 512;                    // tensor memory: S of both halves, then O of both
 constexpr int MAX_PIECE_ITEMS = 256;            // (tree, rows) of calls that may be dealt in pieces
+constexpr int JOIN_PARTS = 4;                   // parts of an item joined at a time
 constexpr int JOIN_INSIDE_ROWS = 16;            // rows of calls that need no join kernel
 // Weights are handed to the product in two parts, so that it works on the first
 // while the second is made.
@@ -87,8 +90,9 @@ struct JoinRecord {
 };
 
 struct Workspace {
-  uint32_t* arrived;    // [CTA where the item begins]: parts left; zero between calls
-  JoinRecord* records;  // [CTA]: the item that begins there and goes on after it
+  uint32_t* arrived;    // [CTA where the item begins][softmax warp]: parts left; zero between calls
+  uint32_t* pending;    // [CTA]: bit w: rows of softmax warp w that the join kernel is to put together
+  JoinRecord* records;  // [CTA]: the item that they are of
   float2* sums;       // [CTA][2][ws_rows]: (reference, sum)
   float4* out;        // [CTA][2][D / 4][ws_rows]: neighbouring rows are neighbours in memory
 };
@@ -96,7 +100,8 @@ struct Workspace {
 __host__ __device__ inline Workspace workspace_of(void* ws, int num_sms, int ws_rows) {
   Workspace w;
   w.arrived = static_cast<uint32_t*>(ws);
-  w.records = reinterpret_cast<JoinRecord*>(w.arrived + (num_sms + 3) / 4 * 4);
+  w.pending = w.arrived + num_sms * 8;
+  w.records = reinterpret_cast<JoinRecord*>(w.pending + (num_sms + 3) / 4 * 4);
   w.sums = reinterpret_cast<float2*>(w.records + num_sms);
   w.out = reinterpret_cast<float4*>(w.sums + static_cast<size_t>(num_sms) * 2 * ws_rows);
   return w;
@@ -260,6 +265,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Contro
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if (threadIdx.x % 32 == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
 }
 
 // A barrier of some of the CTA's warps (converged: .aligned instructions of a
@@ -616,21 +627,23 @@ __device__ __noinline__ void add_odd(const Plan& P, const Segment& s, const uint
 
 // Rows of an item from its parts, which the CTAs from `from` on have left:
 // thread x of `threads` (a power of two) takes 16 bytes at a time of the parts.
+// Only rows of the softmax warps in `warps`.
 template <typename T, int D>
 __device__ __forceinline__ void join_rows(const Plan& P, const Workspace& ws, const JoinRecord& rec, int cnt, int from,
-                                          int x, int threads) {
+                                          int x, int threads, uint32_t warps = 0xffffffffu) {
   const int rows = min(P.ws_rows, P.rows - rec.row0);  // ws_rows: of a whole item
   // a thread keeps to one row; neighbours have neighbouring rows
   int spread = 1;
   while (spread < rows && spread < threads) spread *= 2;
   const int local = x % spread, row = rec.row0 + local;
-  if (local >= rows) return;
+  const int half = local >= P.half_rows;  // which softmax warp had the row
+  if (local >= rows || !((warps >> (half * 4 + (local - half * P.half_rows) / 32)) & 1)) return;
   const int i = node_of_row(P, row), g = row - i * P.group;
   const bool live = P.L.nodes.begin + i < cnt;
   T* out = static_cast<T*>(P.L.out.data) + rec.b * P.L.out.tree_stride + i * P.L.out.node_stride +
            (static_cast<int64_t>(rec.head) * P.group + g) * P.L.out.head_stride;
-  // BATCH quads of PARTS parts at a time: their loads are in flight together
-  constexpr int BATCH = 4, PARTS = 4;
+  // BATCH quads of JOIN_PARTS parts at a time: their loads are in flight together
+  constexpr int BATCH = 4;
   const int step = threads / spread;
 #pragma unroll 1
   for (int q0 = x / spread; q0 < D / 4; q0 += BATCH * step) {
@@ -639,11 +652,11 @@ __device__ __forceinline__ void join_rows(const Plan& P, const Workspace& ws, co
 #pragma unroll
     for (int e = 0; e < BATCH; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-    for (int p0 = 0; live && p0 < rec.parts; p0 += PARTS) {
-      float2 ms[PARTS];
-      float4 y[PARTS][BATCH];
+    for (int p0 = 0; live && p0 < rec.parts; p0 += JOIN_PARTS) {
+      float2 ms[JOIN_PARTS];
+      float4 y[JOIN_PARTS][BATCH];
 #pragma unroll
-      for (int p = 0; p < PARTS; ++p) {
+      for (int p = 0; p < JOIN_PARTS; ++p) {
         // part p: slot 1 of the first CTA, slot 0 of the next ones
         const int64_t slot = static_cast<int64_t>(from + p0 + p) * 2 + (p0 + p == 0 ? 1 : 0);
         const float4* part = ws.out + slot * (D / 4) * P.ws_rows + local;
@@ -657,19 +670,20 @@ __device__ __forceinline__ void join_rows(const Plan& P, const Workspace& ws, co
       }
       float next = top;
 #pragma unroll
-      for (int p = 0; p < PARTS; ++p) next = fmaxf(next, ms[p].x);
+      for (int p = 0; p < JOIN_PARTS; ++p) next = fmaxf(next, ms[p].x);
       const float sub = next == -INFINITY ? 0.0f : next, keep = ex2(top - sub);
       top = next;
       sum *= keep;
 #pragma unroll
       for (int e = 0; e < BATCH; ++e) acc[e].x *= keep, acc[e].y *= keep, acc[e].z *= keep, acc[e].w *= keep;
 #pragma unroll
-      for (int p = 0; p < PARTS; ++p) {
+      for (int p = 0; p < JOIN_PARTS; ++p) {
         const float f = ex2(ms[p].x - sub);
-        sum += ms[p].y * f;
+        sum = fmaf(ms[p].y, f, sum);
 #pragma unroll
         for (int e = 0; e < BATCH; ++e)
-          acc[e].x += y[p][e].x * f, acc[e].y += y[p][e].y * f, acc[e].z += y[p][e].z * f, acc[e].w += y[p][e].w * f;
+          acc[e].x = fmaf(y[p][e].x, f, acc[e].x), acc[e].y = fmaf(y[p][e].y, f, acc[e].y),
+          acc[e].z = fmaf(y[p][e].z, f, acc[e].z), acc[e].w = fmaf(y[p][e].w, f, acc[e].w);
       }
     }
     const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;  // no sum: zeros, as acc is
@@ -833,8 +847,44 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
     const bool whole = s.first == 0 && s.last == s.tiles;
     const Workspace ws = workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows);
     const int64_t part = cta * 2 + (s.first == 0 ? 1 : 0);
-    const bool some = live && sum != 0.0f;
-    const float inv = some ? 1.0f / sum : 0.0f;
+    int from = cta, parts = 1;  // of the item: its first CTA, and how many have a part of it
+    if (C.pieces) {
+      from = cta - C.piece;
+      parts = C.pieces;
+    } else if (!whole) {
+      if (s.first > 0) from = range_of(C.total, s.begin, ctas);
+      parts = (s.last == s.tiles ? cta : range_of(C.total, s.begin + s.tiles - 1, ctas)) - from + 1;
+    }
+    // Ranges: an item is what its first CTA does last and the next ones do
+    // first, so their parts have long been left when the first CTA comes to its
+    // own; it then puts them together itself, with join_rows' operations in
+    // their order, so that the bits do not depend on who does it.
+    uint32_t* arrived = ws.arrived + from * 8 + half * 4 + warp;
+    bool rest_there = false;
+    float top = ref, total = sum;
+    if (!whole && !C.pieces && !P.join_inside && s.first == 0 && parts <= JOIN_PARTS) {
+      uint32_t n = 0;
+      if (lane == 0) n = load_acquire(arrived);
+      rest_there = __shfl_sync(FULL, n, 0) + 1 == static_cast<uint32_t>(parts);
+      if (rest_there) {
+        if (lane == 0) *arrived = 0;
+        float2 ms[JOIN_PARTS - 1];
+#pragma unroll
+        for (int p = 1; p < JOIN_PARTS; ++p)
+          ms[p - 1] = live && p < parts ? __ldcg(&ws.sums[static_cast<int64_t>(from + p) * 2 * P.ws_rows + local])
+                                        : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int p = 1; p < JOIN_PARTS; ++p) top = fmaxf(top, ms[p - 1].x);
+        const float sub = top == -INFINITY ? 0.0f : top;
+        total = sum * ex2(ref - sub);
+#pragma unroll
+        for (int p = 1; p < JOIN_PARTS; ++p) total = fmaf(ms[p - 1].y, ex2(ms[p - 1].x - sub), total);
+      }
+    }
+    const bool finish = whole || rest_there;
+    const float top0 = top == -INFINITY ? 0.0f : top, own = rest_there ? ex2(ref - top0) : 1.0f;
+    const bool some = live && total != 0.0f;
+    const float inv = some ? 1.0f / total : 0.0f;
     T* out = static_cast<T*>(P.L.out.data) + s.b * P.L.out.tree_stride + i * P.L.out.node_stride +
              (static_cast<int64_t>(s.head) * P.group + g) * P.L.out.head_stride;
     float4* partial = ws.out + part * (D / 4) * P.ws_rows + local;
@@ -853,7 +903,27 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
       } else {
         tmem_wait_ld();
       }
-      if (!whole) {
+      if (rest_there && live) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * own);
+#pragma unroll 1
+        for (int p = 1; p < parts; ++p) {
+          const int64_t at = static_cast<int64_t>(from + p) * 2;
+          const float4* theirs = ws.out + (at * (D / 4) + c * 8) * P.ws_rows + local;
+          const float f = ex2(__ldcg(&ws.sums[at * P.ws_rows + local].x) - top0);
+          float4 y[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) y[q] = __ldcg(theirs + q * P.ws_rows);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            o[q * 4] = __float_as_uint(fmaf(y[q].x, f, __uint_as_float(o[q * 4])));
+            o[q * 4 + 1] = __float_as_uint(fmaf(y[q].y, f, __uint_as_float(o[q * 4 + 1])));
+            o[q * 4 + 2] = __float_as_uint(fmaf(y[q].z, f, __uint_as_float(o[q * 4 + 2])));
+            o[q * 4 + 3] = __float_as_uint(fmaf(y[q].w, f, __uint_as_float(o[q * 4 + 3])));
+          }
+        }
+      }
+      if (!finish) {
         if (live) {
 #pragma unroll
           for (int q = 0; q < 8; ++q)
@@ -871,40 +941,33 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
       }
     }
     if (s.last > first_masked) {
-      const int from = max(s.first, first_masked);
+      const int masked0 = max(s.first, first_masked);
       uint32_t odd = 0;
-      for (int x = (from - first_masked) * (TILE / 32); x < (s.last - first_masked) * (TILE / 32); ++x)
+      for (int x = (masked0 - first_masked) * (TILE / 32); x < (s.last - first_masked) * (TILE / 32); ++x)
         odd |= C.odd[segment % 3][x];
       const Segment copy = s;  // the callee takes its address, and s is to stay in registers
       if (odd && live)
-        add_odd<T, D>(P, copy, C.odd[segment % 3], from, node, whole ? out : nullptr, reinterpret_cast<float*>(partial));
+        add_odd<T, D>(P, copy, C.odd[segment % 3], masked0, node, finish ? out : nullptr, reinterpret_cast<float*>(partial));
     }
-    if (!whole && live) ws.sums[part * P.ws_rows + local] = make_float2(ref, sum);
+    if (!finish && live) ws.sums[part * P.ws_rows + local] = make_float2(ref, sum);
     tmem_fence_before();
     if (both) warps_meet(5 + warp, 64);
-    if (!whole && local - lane == 0 && (P.join_inside || s.first == 0)) {  // one warp
-      int from, parts;
-      if (C.pieces) {
-        from = cta - C.piece;
-        parts = C.pieces;
-      } else {
-        from = s.first == 0 ? cta : range_of(C.total, s.begin, ctas);
-        parts = (s.last == s.tiles ? cta : range_of(C.total, s.begin + s.tiles - 1, ctas)) - from + 1;
-      }
-      if (P.join_inside) {
+    if (finish) continue;
+    if (P.join_inside || (!C.pieces && s.first > 0)) {
+      // say that this part is there; the last to do so joins a call of few rows
+      __threadfence();
+      __syncwarp();
+      uint32_t before = 0;
+      if (lane == 0) before = atomicAdd(arrived, 1);
+      if (P.join_inside && __shfl_sync(FULL, before, 0) + 1 == static_cast<uint32_t>(parts)) {
+        if (lane == 0) *arrived = 0;
         __threadfence();
-        __syncwarp();
-        uint32_t before = 0;
-        if (lane == 0) before = atomicAdd(&ws.arrived[from], 1);
-        if (__shfl_sync(FULL, before, 0) + 1 == static_cast<uint32_t>(parts)) {
-          if (lane == 0) ws.arrived[from] = 0;
-          __threadfence();
-          join_rows<T, D>(P, ws, JoinRecord{parts, s.b, s.row0, s.head}, s.cnt, from, lane, 32);
-          __syncwarp();
-        }
-      } else if (lane == 0) {
-        ws.records[cta] = JoinRecord{parts, s.b, s.row0, s.head};
+        join_rows<T, D>(P, ws, JoinRecord{parts, s.b, s.row0, s.head}, s.cnt, from, lane, 32);
       }
+      __syncwarp();
+    } else if (s.first == 0 && lane == 0) {
+      ws.records[cta] = JoinRecord{parts, s.b, s.row0, s.head};
+      atomicOr(&ws.pending[cta], 1u << (half * 4 + warp));
     }
   }
 }
@@ -1068,7 +1131,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   grid_dependency_wait();
   grid_dependents_launch();
   if (!P.may_piece || !find_piece<Y::HALVES>(P, C, warp, cta)) find_range<Y::HALVES>(P, C, warp, cta);
-  if (threadIdx.x == 0 && !P.join_inside) workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows).records[cta].parts = 0;
+  if (threadIdx.x == 0 && !P.join_inside) workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows).pending[cta] = 0;
   if (cta == 0)
     for (int b = threadIdx.x; b < P.L.B; b += THREADS) {
       int len, cnt;
@@ -1108,7 +1171,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // CTA (x, y) of the join: a slice of the rows' elements of the item that begins
-// in range or piece x and goes on after it.
+// in range or piece x and goes on after it, where that CTA has not put them
+// together itself.
 constexpr int JOIN_THREADS = 256, JOIN_SLICES = 8;
 
 template <typename T, int D>
@@ -1116,11 +1180,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) attend_join_kernel(const __grid_
   grid_dependency_wait();
   grid_dependents_launch();
   const Workspace ws = workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows);
+  const uint32_t pending = ws.pending[blockIdx.x];
+  if (pending == 0) return;
   const JoinRecord rec = ws.records[blockIdx.x];
-  if (rec.parts == 0) return;
+  if (blockIdx.y == 0 && threadIdx.x < 8 && ((pending >> threadIdx.x) & 1)) ws.arrived[blockIdx.x * 8 + threadIdx.x] = 0;
   int len, cnt;
   tree_of(P, rec.b, len, cnt);
-  join_rows<T, D>(P, ws, rec, cnt, blockIdx.x, blockIdx.y * JOIN_THREADS + threadIdx.x, JOIN_THREADS * JOIN_SLICES);
+  join_rows<T, D>(P, ws, rec, cnt, blockIdx.x, blockIdx.y * JOIN_THREADS + threadIdx.x, JOIN_THREADS * JOIN_SLICES, pending);
 }
 
 // -------------------------------------------------------------------- host ---
