@@ -1022,7 +1022,7 @@ __device__ __forceinline__ void find_range(const Plan& P, Control& C, int warp, 
 
 // In tiles of 128 rows (a tile of 256 counts for two): what leaving and joining
 // parts costs, and the second segment that a range has.
-constexpr float JOIN_COST = 6.0f, ENDS_COST = 4.0f;
+constexpr float JOIN_COST = 6.0f, ENDS_COST = 10.0f;
 
 // Pieces of an item of `tiles` tiles when a piece is to have about 1 / inv.
 __device__ __forceinline__ int pieces_of(int tiles, float inv) {

@@ -460,3 +460,87 @@ def test_commit_leaves_bad_paths_alone():
     torch.cuda.synchronize()
     assert int(status.item()) == B.S_NODES and new.tolist() == [20, 23, 20, -1, 20]
     assert torch.equal(cache.k.cpu(), c.k)
+
+
+# ------------------------------------------------------------- all together ---
+
+def test_committed_cache_equals_a_plain_pass_over_the_tokens():
+    """Rounds of drafting, verification and commit leave the keys and values that a plain pass over the same
+    tokens makes: up to the roundings of two bf16 layers (four of half a step, 2^-8, each)."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import tree_decode
+    target, tokens, accepted = tree_decode.decode(B=3, rounds=8)
+    assert max(map(max, accepted)) > 0
+    lengths = target.cache.seq_len.tolist()
+    assert lengths == [len(t) - 1 for t in tokens]
+    status = _status()
+    for b, row in enumerate(tokens):
+        plain = tree_decode.Model(0, 3, target.rope.shape[0], 4096, 2, max_nodes=256)
+        plain.step(torch.tensor([row[:-1]] * 3, device="cuda"), status)
+        for mine, theirs in ((target.cache.k, plain.cache.k), (target.cache.v, plain.cache.v)):
+            size = mine.shape[2]
+            slots = torch.arange(lengths[b], device="cuda")
+            a = mine[:, target.cache.page_table[b].long()[slots // size], slots % size].double()
+            c = theirs[:, plain.cache.page_table[b].long()[slots // size], slots % size].double()
+            off = (a - c).norm(dim=-1) / c.norm(dim=-1)
+            assert float(off[0].max()) <= 2 * 2.0 ** -8 and float(off.max()) <= 4 * 2.0 ** -8 * 2, off.amax((1, 2))
+    assert int(status.item()) == 0
+
+
+# --------------------------------------------------------- more shapes of heads ---
+
+@pytest.mark.parametrize("Hq,Hkv,N", [(3, 1, 50), (128, 1, 3), (64, 1, 9), (48, 16, 7), (100, 1, 4), (6, 6, 150)])
+def test_group_sizes(Hq, Hkv, N):
+    c = kv_cases.make(49, [60, 140], N, Hkv, 64, 16, counts=[N, max(1, N - 2)], stale=float("nan"))
+    _check_attend(c, _queries(51, c, Hq))
+
+
+def test_chunk_of_a_group_that_does_not_divide_128():
+    c = kv_cases.make(52, [75, 300], 90, 1, 128, 32, tree=False, stale=float("nan"))
+    _check_attend(c, _queries(53, c, 7))
+
+
+@pytest.mark.parametrize("dim", [0, 1, 2])
+def test_broadcast_queries(dim):
+    """Queries shared by all trees, nodes or heads (stride 0)."""
+    c = kv_cases.make(54, [66, 20], 12, 2, 128, 16)
+    q = _queries(55, c, 4)
+    q = q.narrow(dim, 0, 1).expand(q.shape)
+    ref, _ = _run_attend(c, q.contiguous())
+    cache, status = _cache(c), _status()
+    out = torch.zeros(q.shape, dtype=c.dtype, device="cuda")
+    B.spec_tree_attend(cache, 0, q.narrow(dim, 0, 1).cuda().expand(q.shape), out, B.AttendWorkspace(2, 12, 4, 2, 128), status,
+                       tree=_nodes(c))
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), ref) and int(status.item()) == 0
+
+
+def test_one_long_tree_in_many_parts():
+    """A tree over one long sequence: an item in more parts than are joined at a time."""
+    c = kv_cases.make(56, [9000], 40, 1, 64, 64)
+    _check_attend(c, _queries(57, c, 4))
+
+
+def test_items_split_between_ranges():
+    """More items than CTAs, of unequal lengths: ranges begin and end inside items; many launches, the same bits."""
+    rng = np.random.RandomState(3)
+    lens = rng.randint(100, 1500, 60).tolist()
+    c = kv_cases.make(58, lens, 33, 4, 64, 64)
+    q = _queries(59, c, 8)
+    cache, qd, nodes, status, ws = _cache(c), q.cuda(), _nodes(c), _status(), B.AttendWorkspace(60, 33, 8, 4, 64)
+    outs = [torch.zeros_like(qd) for _ in range(3)]
+    for _ in range(20):
+        for out in outs:
+            B.spec_tree_attend(cache, 0, qd, out, ws, status, tree=nodes)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and all(torch.equal(outs[0], o) for o in outs)
+    sub = [0, 17, 59]  # the oracle is slow: three of the trees
+    c3 = kv_cases.dataclasses.replace(c, table=c.table[sub], seq_len=c.seq_len[sub], parent=c.parent[sub], depth=c.depth[sub],
+                                      counts=[c.counts[i] for i in sub])
+    k, v = c.pools(0)
+    want, mean_abs, score_abs, sum_abs = O.attend(q[sub].double().numpy(), k, v, c3.table.numpy(), c3.seq_len.numpy(),
+                                                  c3.parent.numpy(), c3.counts, 0, 64 ** -0.5)
+    bound = kv_cases.attend_bound(c.dtype, want, mean_abs, score_abs, sum_abs, 64, 1533)
+    assert (np.abs(outs[0].cpu()[sub].double().numpy() - want) <= bound).all()

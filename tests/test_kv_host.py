@@ -84,6 +84,8 @@ def test_bad_calls(B):
         assert call(B, kv, trees=0, nodes=N(256, 256, None, 512, 0, 512)) == B.OK
         assert call(B, kv, trees=0, q=B.c_heads(264, 512, 512, 128)) == B.E_LAYOUT
         assert call(B, kv, trees=0, q=B.c_heads(256, 512, 516, 128)) == B.E_LAYOUT
+        assert call(B, kv, trees=0, q=B.c_heads(256, 512, 512, -128)) == B.E_LAYOUT
+        assert call(B, kv, trees=0, q=B.c_heads(256, 1 << 38, 512, 128)) == B.E_LAYOUT
         assert call(B, kv, trees=0, q=B.c_heads(None, 512, 512, 128)) == B.E_PARAM
         assert call(B, kv, trees=0, hq=0) == B.E_PARAM
     assert _append(B, kv, trees=0, nodes=N(256, None, None, 10, 0, 1)) == B.E_PARAM        # parents without depths
@@ -97,6 +99,10 @@ def test_bad_calls(B):
         assert _append(B, kv, trees=0, eps=eps) == B.E_PARAM
     assert _attend(B, _kv(B, n_kv_heads=3), trees=0) == B.E_PARAM                          # 4 query heads over 3
     assert _attend(B, _kv(B, n_kv_heads=8), trees=0) == B.E_PARAM
+    assert _attend(B, kv, trees=0, hq=128) == B.OK and _attend(B, kv, trees=0, hq=129) == B.E_PARAM  # heads of a key head
+    assert B._lib.spec_tree_attend_workspace_bytes(1, 1, 129, 1, 64) == 0
+    assert B._lib.spec_tree_attend_workspace_bytes(1, 1, 8, 3, 64) == 0
+    assert B._lib.spec_tree_attend_workspace_bytes(1, 1, 8, 1, 96) == 0
     assert _attend(B, kv, trees=0, out=B.c_heads(256, 512, 512, 128)) == B.E_PARAM         # out over q
     assert _attend(B, kv, trees=0, scale=float("nan")) == B.E_PARAM
     assert _attend(B, kv, trees=0, ws=None) == B.E_PARAM and _attend(B, kv, trees=0, ws=264) == B.E_LAYOUT
