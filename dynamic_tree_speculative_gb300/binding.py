@@ -159,7 +159,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:  # the handle of the current stream, without the Stream object around it (2.9 us a call)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -430,12 +430,12 @@ def _int_rows(name: str, t: torch.Tensor, shape) -> int:
 class _Packed(threading.local):
     """One call's spec_tree_nodes_t and up to four spec_tree_heads_t, packed into memory of the thread's own
     (the entry points read them before they return)."""
-    NODES, HEADS = struct.Struct("@3P3i"), struct.Struct("@P3q")
+    NODES, HEADS2, HEADS4 = struct.Struct("@3P3i"), struct.Struct("@P3qP3q"), struct.Struct("@P3qP3qP3qP3q")
 
     def __init__(self):
-        self.buf = ctypes.create_string_buffer(64 + 4 * self.HEADS.size)
+        self.buf = ctypes.create_string_buffer(64 + self.HEADS4.size)
         self.nodes_at = ctypes.addressof(self.buf)
-        self.heads_at = tuple(self.nodes_at + 64 + i * self.HEADS.size for i in range(4))
+        self.heads_at = tuple(self.nodes_at + 64 + i * (self.HEADS4.size // 4) for i in range(4))
 
     def nodes(self, tree, B: int, begin: int, count: int) -> int:
         """A TreeBuffers, a NodeArrays or None (a chain of which every node exists)."""
@@ -453,13 +453,23 @@ class _Packed(threading.local):
                              0 if n is None else _int_rows("n_nodes", n, (B,)), stride, begin, count)
         return self.nodes_at
 
-    def heads(self, i: int, name: str, x: torch.Tensor, dtype, shape) -> int:
-        """[B][nodes][heads][head_dim] with contiguous head_dim."""
-        s = x.stride()
-        if x.dtype is not dtype or x.shape != shape or s[3] != 1:
-            raise SpecTreeError(f"{name} must be {list(shape)} of {dtype}, head_dim contiguous")
-        self.HEADS.pack_into(self.buf, 64 + i * self.HEADS.size, x.data_ptr(), s[0], s[1], s[2])
-        return self.heads_at[i]
+    def heads2(self, a: torch.Tensor, b: torch.Tensor):
+        """Two tensors of vectors; their addresses in the buffer."""
+        (a0, a1, a2, _), (b0, b1, b2, _) = a.stride(), b.stride()
+        self.HEADS2.pack_into(self.buf, 64, a.data_ptr(), a0, a1, a2, b.data_ptr(), b0, b1, b2)
+        return self.heads_at
+
+    def heads4(self, a: torch.Tensor, b: torch.Tensor, c: torch.Tensor, d: torch.Tensor):
+        (a0, a1, a2, _), (b0, b1, b2, _), (c0, c1, c2, _), (d0, d1, d2, _) = a.stride(), b.stride(), c.stride(), d.stride()
+        self.HEADS4.pack_into(self.buf, 64, a.data_ptr(), a0, a1, a2, b.data_ptr(), b0, b1, b2, c.data_ptr(), c0, c1, c2,
+                              d.data_ptr(), d0, d1, d2)
+        return self.heads_at
+
+
+def _vectors(name: str, x: torch.Tensor, dtype, shape):
+    """Refuse what is not [B][nodes][heads][head_dim] of that shape and dtype with contiguous head_dim."""
+    if x.dtype is not dtype or x.shape != shape or x.stride(3) != 1:
+        raise SpecTreeError(f"{name} must be {list(shape)} of {dtype}, head_dim contiguous")
 
 
 _packed = _Packed()
@@ -498,9 +508,12 @@ def spec_tree_kv_append(cache: KVCache, layer: int, q: torch.Tensor, k: torch.Te
         if w is not None and (w.dtype is not dtype or w.shape != (dim,) or not w.is_contiguous()):
             raise SpecTreeError(f"{name} must be [head_dim] of the cache's dtype")
     qs, ks = (B, n, hq, dim), (B, n, hkv, dim)
-    _check(_lib.spec_tree_kv_append(B, cache.at, layer, pack.nodes(tree, B, node_begin, n), hq,
-                                    pack.heads(0, "q", q, dtype, qs), pack.heads(1, "k", k, dtype, ks),
-                                    pack.heads(2, "v", v, dtype, ks), pack.heads(3, "q_out", q_out, dtype, qs),
+    _vectors("q", q, dtype, qs)
+    _vectors("k", k, dtype, ks)
+    _vectors("v", v, dtype, ks)
+    _vectors("q_out", q_out, dtype, qs)
+    q_at, k_at, v_at, out_at = pack.heads4(q, k, v, q_out)
+    _check(_lib.spec_tree_kv_append(B, cache.at, layer, pack.nodes(tree, B, node_begin, n), hq, q_at, k_at, v_at, out_at,
                                     rope_at, rows, rot, interleaved, None if q_weight is None else q_weight.data_ptr(),
                                     None if k_weight is None else k_weight.data_ptr(), eps, status.data_ptr(),
                                     _stream(stream)))
@@ -525,8 +538,10 @@ def spec_tree_attend(cache: KVCache, layer: int, q: torch.Tensor, out: torch.Ten
     ancestors and themselves; scale defaults to head_dim ** -0.5."""
     (n, hq), (B, _, dim, dtype), pack = _count(q), cache.shape, _packed
     qs = (B, n, hq, dim)
-    _check(_lib.spec_tree_attend(B, cache.at, layer, pack.nodes(tree, B, node_begin, n), hq,
-                                 pack.heads(0, "q", q, dtype, qs), pack.heads(1, "out", out, dtype, qs),
+    _vectors("q", q, dtype, qs)
+    _vectors("out", out, dtype, qs)
+    q_at, out_at, _, _ = pack.heads2(q, out)
+    _check(_lib.spec_tree_attend(B, cache.at, layer, pack.nodes(tree, B, node_begin, n), hq, q_at, out_at,
                                  dim ** -0.5 if scale is None else scale, workspace.at, workspace.bytes,
                                  status.data_ptr(), _stream(stream)))
 

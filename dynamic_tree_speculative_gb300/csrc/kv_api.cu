@@ -12,6 +12,7 @@ namespace {
 constexpr int MAX_CHAIN = 1 << 20;
 constexpr int MAX_HEADS = 1 << 14;
 constexpr int MAX_TREES = 65535;
+constexpr int64_t MAX_SLOTS = 1ll << 30;  // of a sequence
 constexpr int MAX_GROUP = 128;            // query heads of a key head
 constexpr int64_t MAX_STRIDE = 1ll << 38;  // elements
 
@@ -28,7 +29,7 @@ int check_kv(int B, const spec_tree_kv_t* kv, int layer) {
   if (kv->head_dim != 64 && kv->head_dim != 128) return SPEC_TREE_E_PARAM;
   if (kv->page_size < 8 || kv->page_size > 65536 || (kv->page_size & (kv->page_size - 1)) != 0)
     return SPEC_TREE_E_PARAM;
-  if (static_cast<int64_t>(kv->max_pages) * kv->page_size > INT32_MAX) return SPEC_TREE_E_PARAM;
+  if (static_cast<int64_t>(kv->max_pages) * kv->page_size > MAX_SLOTS) return SPEC_TREE_E_PARAM;
   if (!aligned16(kv->k) || !aligned16(kv->v)) return SPEC_TREE_E_LAYOUT;
   const int64_t st[4] = {kv->layer_stride, kv->page_stride, kv->token_stride, kv->head_stride};
   for (int64_t x : st)

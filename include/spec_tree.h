@@ -460,7 +460,7 @@ int spec_tree_wait_selftest(uint32_t polls, uint32_t* status, uint32_t* result, 
  *   page_size   a power of two, 8 to 65536;
  *   page_table  device [B][table_stride] int32, max_pages <= table_stride
  *               entries used, each 0 .. n_pages - 1 where the sequence has
- *               tokens (others are not read);
+ *               tokens (others are not read); max_pages * page_size <= 2^30;
  *   seq_len     device [B] int32 >= 0: committed tokens.
  * k and v are 16-byte aligned and strides multiples of 8 elements, else
  * SPEC_TREE_E_LAYOUT.
@@ -541,8 +541,9 @@ int spec_tree_kv_append(int B, const spec_tree_kv_t* kv, int layer, const spec_t
  *   scale:  finite, usually head_dim^-0.5.
  *   workspace: device, spec_tree_attend_workspace_bytes() bytes, 16-byte
  *           aligned, zero before the first call that uses it; every call
- *           leaves what the next one needs.  Calls that overlap on the GPU
- *           must not share one.
+ *           leaves what the next one needs, except one that reported
+ *           SPEC_TREE_S_TIMEOUT, after which it is to be zeroed again.  Calls
+ *           that overlap on the GPU must not share one.
  * A slot whose page is not in the pool sets SPEC_TREE_S_PAGES and reads as
  * zeros; a tree with slots past the page table sets it too, one of negative
  * length sets SPEC_TREE_S_NODES, and both get zeros; a parent that does not

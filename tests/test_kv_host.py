@@ -1,7 +1,6 @@
 """Key-value cache entry points: refusals before any launch, structures, the oracle (no GPU needed)."""
 import ctypes
 import os
-import struct
 
 import numpy as np
 import pytest
@@ -167,7 +166,7 @@ def test_structs_match_the_c_header(B, tmp_path):
         assert int(got[st]) == ctypes.sizeof(cls), st
         for f, _ in cls._fields_:
             assert int(got[f"{st}.{f}"]) == getattr(cls, f).offset, (st, f)
-    assert struct.calcsize("@3P3i") <= ctypes.sizeof(B.c_nodes) and struct.calcsize("@P3q") == ctypes.sizeof(B.c_heads)
+    assert B._Packed.NODES.size <= ctypes.sizeof(B.c_nodes) and B._Packed.HEADS4.size == 4 * ctypes.sizeof(B.c_heads)
     assert (int(got["F16"]), int(got["S_PAGES"]), int(got["S_NODES"])) == (B.F16, B.S_PAGES, B.S_NODES)
 
 
