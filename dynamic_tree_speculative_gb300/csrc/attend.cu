@@ -24,11 +24,13 @@
 // An item that one CTA has whole is finished there; otherwise each CTA leaves
 // its sums, their reference and its unnormalised output in the workspace, and
 // the parts are put together in the item's order:
-//   - calls of up to 16 rows: by whichever CTA is the last to leave its part
-//     (which saves a launch; of many rows the join is long for one CTA);
-//   - ranges: by the item's first CTA as it comes to its own part, if the
-//     others have left theirs, as they nearly always have;
-//   - else by attend_join_kernel, over all SMs.
+//   - ranges: an item is what its first CTA does last and the next ones do
+//     first, so the others have nearly always left their parts when the first
+//     comes to its own, and it puts them together without leaving its own.  If
+//     not, and for calls of up to 16 rows, whoever is the last to leave a part
+//     does it;
+//   - pieces, of more rows: they end together, and one CTA would be long about
+//     it: attend_join_kernel, over all SMs.
 //
 // Tile.  S = Q K^T in tensor memory (128 lanes: one row per softmax thread);
 // weights w = 2^(scale S - ref), rounded to the cache's type and stored over
@@ -86,22 +88,20 @@ struct Plan {
 // Parts of items: slot 0 of a CTA for one that began before it, slot 1 for one
 // that goes on after it.
 struct JoinRecord {
-  int32_t parts, b, row0, head;
+  int32_t parts, b, row0, head;  // parts = 0: nothing to join
 };
 
 struct Workspace {
   uint32_t* arrived;    // [CTA where the item begins][softmax warp]: parts left; zero between calls
-  uint32_t* pending;    // [CTA]: bit w: rows of softmax warp w that the join kernel is to put together
-  JoinRecord* records;  // [CTA]: the item that they are of
-  float2* sums;       // [CTA][2][ws_rows]: (reference, sum)
-  float4* out;        // [CTA][2][D / 4][ws_rows]: neighbouring rows are neighbours in memory
+  JoinRecord* records;  // [CTA]: the item of which it has the first piece, for the join kernel
+  float2* sums;         // [CTA][2][ws_rows]: (reference, sum)
+  float4* out;          // [CTA][2][D / 4][ws_rows]: neighbouring rows are neighbours in memory
 };
 
 __host__ __device__ inline Workspace workspace_of(void* ws, int num_sms, int ws_rows) {
   Workspace w;
   w.arrived = static_cast<uint32_t*>(ws);
-  w.pending = w.arrived + num_sms * 8;
-  w.records = reinterpret_cast<JoinRecord*>(w.pending + (num_sms + 3) / 4 * 4);
+  w.records = reinterpret_cast<JoinRecord*>(w.arrived + num_sms * 8);
   w.sums = reinterpret_cast<float2*>(w.records + num_sms);
   w.out = reinterpret_cast<float4*>(w.sums + static_cast<size_t>(num_sms) * 2 * ws_rows);
   return w;
@@ -625,19 +625,18 @@ __device__ __noinline__ void add_odd(const Plan& P, const Segment& s, const uint
   }
 }
 
-// Rows of an item from its parts, which the CTAs from `from` on have left:
-// thread x of `threads` (a power of two) takes 16 bytes at a time of the parts.
-// Only rows of the softmax warps in `warps`.
+// Rows local0 .. local0 + rows - 1 of an item from its parts, which the CTAs
+// from `from` on have left: thread x of `threads` (a power of two) takes 16
+// bytes at a time of the parts.
 template <typename T, int D>
 __device__ __forceinline__ void join_rows(const Plan& P, const Workspace& ws, const JoinRecord& rec, int cnt, int from,
-                                          int x, int threads, uint32_t warps = 0xffffffffu) {
-  const int rows = min(P.ws_rows, P.rows - rec.row0);  // ws_rows: of a whole item
+                                          int local0, int rows, int x, int threads) {
+  rows = min(rows, P.rows - rec.row0 - local0);
   // a thread keeps to one row; neighbours have neighbouring rows
   int spread = 1;
   while (spread < rows && spread < threads) spread *= 2;
-  const int local = x % spread, row = rec.row0 + local;
-  const int half = local >= P.half_rows;  // which softmax warp had the row
-  if (local >= rows || !((warps >> (half * 4 + (local - half * P.half_rows) / 32)) & 1)) return;
+  if (x % spread >= rows) return;
+  const int local = local0 + x % spread, row = rec.row0 + local;
   const int i = node_of_row(P, row), g = row - i * P.group;
   const bool live = P.L.nodes.begin + i < cnt;
   T* out = static_cast<T*>(P.L.out.data) + rec.b * P.L.out.tree_stride + i * P.L.out.node_stride +
@@ -855,10 +854,9 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
       if (s.first > 0) from = range_of(C.total, s.begin, ctas);
       parts = (s.last == s.tiles ? cta : range_of(C.total, s.begin + s.tiles - 1, ctas)) - from + 1;
     }
-    // Ranges: an item is what its first CTA does last and the next ones do
-    // first, so their parts have long been left when the first CTA comes to its
-    // own; it then puts them together itself, with join_rows' operations in
-    // their order, so that the bits do not depend on who does it.
+    // Ranges: the first CTA puts the parts together if the others are there,
+    // with join_rows' operations in their order: the bits do not depend on who
+    // does it.
     uint32_t* arrived = ws.arrived + from * 8 + half * 4 + warp;
     bool rest_there = false;
     float top = ref, total = sum;
@@ -953,21 +951,21 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
     tmem_fence_before();
     if (both) warps_meet(5 + warp, 64);
     if (finish) continue;
-    if (P.join_inside || (!C.pieces && s.first > 0)) {
-      // say that this part is there; the last to do so joins a call of few rows
+    if (P.join_inside || !C.pieces) {
+      // this part is there; the last to say so for its rows puts them together
       __threadfence();
       __syncwarp();
       uint32_t before = 0;
       if (lane == 0) before = atomicAdd(arrived, 1);
-      if (P.join_inside && __shfl_sync(FULL, before, 0) + 1 == static_cast<uint32_t>(parts)) {
+      if (__shfl_sync(FULL, before, 0) + 1 == static_cast<uint32_t>(parts)) {
         if (lane == 0) *arrived = 0;
         __threadfence();
-        join_rows<T, D>(P, ws, JoinRecord{parts, s.b, s.row0, s.head}, s.cnt, from, lane, 32);
+        join_rows<T, D>(P, ws, JoinRecord{parts, s.b, s.row0, s.head}, s.cnt, from, local - lane,
+                        min(32, P.half_rows - warp * 32), lane, 32);
       }
       __syncwarp();
-    } else if (s.first == 0 && lane == 0) {
+    } else if (s.first == 0 && local == 0) {
       ws.records[cta] = JoinRecord{parts, s.b, s.row0, s.head};
-      atomicOr(&ws.pending[cta], 1u << (half * 4 + warp));
     }
   }
 }
@@ -1131,7 +1129,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   grid_dependency_wait();
   grid_dependents_launch();
   if (!P.may_piece || !find_piece<Y::HALVES>(P, C, warp, cta)) find_range<Y::HALVES>(P, C, warp, cta);
-  if (threadIdx.x == 0 && !P.join_inside) workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows).pending[cta] = 0;
+  if (threadIdx.x == 0 && P.may_piece) workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows).records[cta].parts = 0;
   if (cta == 0)
     for (int b = threadIdx.x; b < P.L.B; b += THREADS) {
       int len, cnt;
@@ -1170,23 +1168,20 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// CTA (x, y) of the join: a slice of the rows' elements of the item that begins
-// in range or piece x and goes on after it, where that CTA has not put them
-// together itself.
-constexpr int JOIN_THREADS = 256, JOIN_SLICES = 8;
+// CTA (x, y) of the join: a slice of the elements of the item whose first piece
+// was CTA x's.
+constexpr int JOIN_THREADS = 256, JOIN_SLICES = 4;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(JOIN_THREADS) attend_join_kernel(const __grid_constant__ Plan P) {
   grid_dependency_wait();
   grid_dependents_launch();
   const Workspace ws = workspace_of(P.L.workspace, P.L.num_sms, P.ws_rows);
-  const uint32_t pending = ws.pending[blockIdx.x];
-  if (pending == 0) return;
   const JoinRecord rec = ws.records[blockIdx.x];
-  if (blockIdx.y == 0 && threadIdx.x < 8 && ((pending >> threadIdx.x) & 1)) ws.arrived[blockIdx.x * 8 + threadIdx.x] = 0;
+  if (rec.parts == 0) return;
   int len, cnt;
   tree_of(P, rec.b, len, cnt);
-  join_rows<T, D>(P, ws, rec, cnt, blockIdx.x, blockIdx.y * JOIN_THREADS + threadIdx.x, JOIN_THREADS * JOIN_SLICES, pending);
+  join_rows<T, D>(P, ws, rec, cnt, blockIdx.x, 0, P.ws_rows, blockIdx.y * JOIN_THREADS + threadIdx.x, JOIN_THREADS * JOIN_SLICES);
 }
 
 // -------------------------------------------------------------------- host ---
@@ -1265,7 +1260,7 @@ cudaError_t attend(Plan& P, cudaStream_t stream) {
     prepared.fetch_or(bit, std::memory_order_relaxed);
   }
   err = launch_pdl(attend_kernel<T, D, PAIR>, dim3(P.L.num_sms), dim3(THREADS), SMEM, stream, P, mk, mv, mq);
-  if (err != cudaSuccess || P.join_inside) return err;
+  if (err != cudaSuccess || P.join_inside || !P.may_piece) return err;
   return launch_pdl(attend_join_kernel<T, D>, dim3(P.L.num_sms, JOIN_SLICES), dim3(JOIN_THREADS), 0, stream, P);
 }
 
