@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
   F2 c[4], s[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) c[e] = F2(1.0f, 1.0f), s[e] = F2(0.0f, 0.0f);
-  if (turned && in_rot) {
+  const bool turns = turned && in_rot;
+  if (turns) {
     const float* row = L.rope + pos * L.rot_dim;
     if (L.interleaved) {
       const float4 x = *reinterpret_cast<const float4*>(row + lane * 4);
@@ -141,6 +142,8 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
   };
   weighted(L.q_weight, cq, sq);
   weighted(L.k_weight, ck, sk);
+  // where nothing turns, an infinity times the zero of s would be a NaN
+  auto part = [&](F2 y, F2 s, F2 x) { return turns ? fma2(y, s, x) : x; };
   const bool norms = L.q_weight || L.k_weight;
   T* k_to = static_cast<T*>(L.kv.k) + L.layer * L.kv.layer_stride + off + lane * 8;
   T* v_to = static_cast<T*>(L.kv.v) + L.layer * L.kv.layer_stride + off + lane * 8;
@@ -179,12 +182,12 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
       if (is_q) {
         if (L.q_weight == nullptr) r = 1.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = mul2(fma2(y[e], sq[e], mul2(x[e], cq[e])), F2(r, r));
+        for (int e = 0; e < 4; ++e) x[e] = mul2(part(y[e], sq[e], mul2(x[e], cq[e])), F2(r, r));
         *reinterpret_cast<uint4*>(q_to + head * L.q_out.head_stride) = pack_pairs<T>(x);
       } else if (is_k) {
         if (L.k_weight == nullptr) r = 1.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = mul2(fma2(y[e], sk[e], mul2(x[e], ck[e])), F2(r, r));
+        for (int e = 0; e < 4; ++e) x[e] = mul2(part(y[e], sk[e], mul2(x[e], ck[e])), F2(r, r));
         if (off >= 0) *reinterpret_cast<uint4*>(k_to + (head - n_q) * L.kv.head_stride) = pack_pairs<T>(x);
       } else if (head < n_q + 2 * n_kv && off >= 0) {
         *reinterpret_cast<uint4*>(v_to + (head - n_q - n_kv) * L.kv.head_stride) = raw[u];

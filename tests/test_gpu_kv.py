@@ -392,6 +392,24 @@ def test_append_far_positions():
         assert (np.abs(got.double().cpu().numpy() - want) <= bound).all()
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot,rows", [(0, 0), (32, 8), (64, 4)])
+def test_append_keeps_infinities_where_nothing_turns(rot, rows, interleaved):
+    """Without norms the part past rot_dim, and a node outside the table (rows), is a copy: infinities stay, no NaN."""
+    c = kv_cases.make(54, [3], 3, 1, 64, 16, tree=False)
+    x = torch.randn((1, 3, 1, 64), generator=torch.Generator().manual_seed(1)).to(c.dtype)
+    x[0, 1:, 0, 40], x[0, 1:, 0, 51] = float("inf"), float("-inf")
+    cache, status, out = _cache(c), _status(), torch.zeros_like(x, device="cuda")
+    B.spec_tree_kv_append(cache, 0, x.cuda(), x.cuda(), x.cuda(), out, B.rope_table(rows, rot) if rot else None, status,
+                          tree=_nodes(c), interleaved=interleaved)
+    torch.cuda.synchronize()
+    assert int(status.item()) == (B.S_NODES if rot == 64 else 0)
+    slots = c.table[0, 0].item(), slice(3, 6)
+    start = rot if rot < 64 else 0       # nodes 1 and 2 lie at positions 4 and 5, past a table of 4 rows
+    for got in (out.cpu()[0, 1:], cache.k.cpu()[0][slots][1:]):
+        assert torch.equal(got[..., start:], x[0, 1:, :, start:]) and not got.isnan().any()
+
+
 def test_append_reports_what_it_cannot_place():
     c = kv_cases.make(53, [30], 4, 1, 64, 16, tree=False)
     x = torch.randn((1, 4, 1, 64)).to(c.dtype).cuda()
