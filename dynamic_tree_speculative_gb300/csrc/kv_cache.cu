@@ -45,7 +45,8 @@ __device__ __forceinline__ uint4 pack_pairs(const F2 (&x)[4]) {
 //
 // Everything is read and written once; what bounds it is the issue rate.  At
 // 64 trees of 61 nodes of 48 heads of 128, normalised (95 MB: 14 us at the
-// measured bandwidth): 22.5 us.  One vector per thread, with a node's loads and
+// measured bandwidth): 21.2 us (22.9 with queries' and keys' products held side
+// by side and chosen per vector).  One vector per thread, with a node's loads and
 // products made for each, took 37.2 us; three per thread 34.3 (253 instructions
 // a step of a warp, of which this leaves 139).
 template <typename T, int D>
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
   const int warp = blockIdx.x * (APPEND_THREADS / 32) + threadIdx.x / 32;
   const int node = warp / spread;
   if (node >= nodes) return;
-  const int n_q = L.n_q_heads, n_kv = L.kv.n_kv_heads, steps = (n_q + 2 * n_kv + PER_STEP - 1) / PER_STEP;
+  const int n_q = L.n_q_heads, n_kv = L.kv.n_kv_heads;
   const int b = node / L.nodes.count, i = node - b * L.nodes.count, n = L.nodes.begin + i;
   // pairs are elements j and j + rot_dim / 2, `half` lanes apart, or neighbours
   const int half = L.rot_dim / 16;
@@ -69,22 +70,27 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
   grid_dependency_wait();
   grid_dependents_launch();
 
+  // a node's steps, dealt to its warps: the query heads first, then the key and
+  // value heads (as one row); no step holds both, so one set of weighted
+  // products lives at a time
+  const int step0 = warp - node * spread, q_steps = (n_q + PER_STEP - 1) / PER_STEP;
+  const int kv_step0 = (step0 < q_steps ? (q_steps - step0 + spread - 1) / spread * spread : 0) + step0 - q_steps;
   uint4 raw[APPEND_BATCH];
-  auto fetch = [&](int step0) {
+  auto fetch = [&](bool queries, int step) {
 #pragma unroll
     for (int u = 0; u < APPEND_BATCH; ++u) {
-      const int head = (step0 + u * spread) * PER_STEP + sub;
+      const int head = (step + u * spread) * PER_STEP + sub;
       raw[u] = make_uint4(0, 0, 0, 0);
-      if (head < n_q)
-        raw[u] = *reinterpret_cast<const uint4*>(q + head * L.q.head_stride);
-      else if (head < n_q + n_kv)
-        raw[u] = *reinterpret_cast<const uint4*>(k + (head - n_q) * L.k.head_stride);
-      else if (head < n_q + 2 * n_kv)
-        raw[u] = *reinterpret_cast<const uint4*>(w + (head - n_q - n_kv) * L.v.head_stride);
+      if (queries) {
+        if (head < n_q) raw[u] = *reinterpret_cast<const uint4*>(q + head * L.q.head_stride);
+      } else if (head < n_kv) {
+        raw[u] = *reinterpret_cast<const uint4*>(k + head * L.k.head_stride);
+      } else if (head < 2 * n_kv) {
+        raw[u] = *reinterpret_cast<const uint4*>(w + (head - n_kv) * L.v.head_stride);
+      }
     }
   };
-  const int step0 = warp - node * spread;
-  fetch(step0);
+  fetch(true, step0);
   const int len = L.kv.seq_len[b], cnt = node_count(L.nodes, b);
   const int depth = L.nodes.depth ? L.nodes.depth[static_cast<int64_t>(b) * L.nodes.stride + n] : n;
   if (len < 0 && threadIdx.x % 32 == 0) set_status(L.status, SPEC_TREE_S_NODES);
@@ -128,8 +134,8 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
     return make_uint4(__byte_perm(x.x, 0, 0x1032), __byte_perm(x.y, 0, 0x1032), __byte_perm(x.z, 0, 0x1032),
                       __byte_perm(x.w, 0, 0x1032));
   };
-  F2 cq[4], sq[4], ck[4], sk[4];
-  auto weighted = [&](const void* weight, F2 (&cw)[4], F2 (&sw)[4]) {
+  F2 cw[4], sw[4];  // with the weights of the heads in hand
+  auto weighted = [&](const void* weight) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) cw[e] = c[e], sw[e] = s[e];
     if (weight == nullptr) return;
@@ -140,57 +146,68 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
 #pragma unroll
     for (int e = 0; e < 4; ++e) cw[e] = mul2(c[e], x[e]), sw[e] = mul2(s[e], y[e]);
   };
-  weighted(L.q_weight, cq, sq);
-  weighted(L.k_weight, ck, sk);
-  // where nothing turns, an infinity times the zero of s would be a NaN
-  auto part = [&](F2 y, F2 s, F2 x) { return turns ? fma2(y, s, x) : x; };
-  const bool norms = L.q_weight || L.k_weight;
-  T* k_to = static_cast<T*>(L.kv.k) + L.layer * L.kv.layer_stride + off + lane * 8;
-  T* v_to = static_cast<T*>(L.kv.v) + L.layer * L.kv.layer_stride + off + lane * 8;
+  // the vector normalised (if there are weights) and turned; the whole warp
+  // takes part in the shuffles, whatever its lanes hold
+  auto turn = [&](uint4 u, bool norm) {
+    uint4 other = u;
+    if (L.interleaved) {
+      other = swapped(other);
+    } else {
+      other.x = __shfl_sync(FULL, other.x, partner, LANES);
+      other.y = __shfl_sync(FULL, other.y, partner, LANES);
+      other.z = __shfl_sync(FULL, other.z, partner, LANES);
+      other.w = __shfl_sync(FULL, other.w, partner, LANES);
+    }
+    F2 x[4], y[4];
+    unpack_pairs<T>(u, x);
+    unpack_pairs<T>(other, y);
+    F2 r(1.0f, 1.0f);
+    if (norm) {
+      F2 sum = mul2(x[0], x[0]);
+#pragma unroll
+      for (int e = 1; e < 4; ++e) sum = fma2(x[e], x[e], sum);
+      float lo, hi;
+      sum.get(lo, hi);
+      lo += hi;
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) lo += __shfl_xor_sync(FULL, lo, o);
+      lo = rsqrtf(lo * (1.0f / D) + L.eps);
+      r = F2(lo, lo);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = mul2(x[e], cw[e]);
+      if (turns) x[e] = fma2(y[e], sw[e], x[e]);  // elsewhere an infinity times the zero of s would be a NaN
+      x[e] = mul2(x[e], r);
+    }
+    return pack_pairs<T>(x);
+  };
 
-  for (int at = step0; at < steps; at += APPEND_BATCH * spread) {
-    if (at != step0) fetch(at);
+  weighted(L.q_weight);
+  for (int at = step0; at < q_steps; at += APPEND_BATCH * spread) {
+    if (at != step0) fetch(true, at);
 #pragma unroll
     for (int u = 0; u < APPEND_BATCH; ++u) {
-      // the whole warp takes part in the shuffles, whatever its lanes hold
       const int head = (at + u * spread) * PER_STEP + sub;
-      const bool is_q = head < n_q, is_k = !is_q && head < n_q + n_kv;
-      uint4 other = raw[u];
-      if (L.interleaved) {
-        other = swapped(other);
-      } else {
-        other.x = __shfl_sync(FULL, other.x, partner, LANES);
-        other.y = __shfl_sync(FULL, other.y, partner, LANES);
-        other.z = __shfl_sync(FULL, other.z, partner, LANES);
-        other.w = __shfl_sync(FULL, other.w, partner, LANES);
-      }
-      F2 x[4], y[4];
-      unpack_pairs<T>(raw[u], x);
-      unpack_pairs<T>(other, y);
-      float r = 1.0f;
-      if (norms) {
-        F2 sum = mul2(x[0], x[0]);
+      const uint4 y = turn(raw[u], L.q_weight != nullptr);
+      if (head < n_q) *reinterpret_cast<uint4*>(q_to + head * L.q_out.head_stride) = y;
+    }
+  }
+  weighted(L.k_weight);
+  T* k_to = static_cast<T*>(L.kv.k) + L.layer * L.kv.layer_stride + off + lane * 8;
+  T* v_to = static_cast<T*>(L.kv.v) + L.layer * L.kv.layer_stride + off + lane * 8;
+  for (int at = kv_step0; at * PER_STEP < 2 * n_kv; at += APPEND_BATCH * spread) {
+    fetch(false, at);
 #pragma unroll
-        for (int e = 1; e < 4; ++e) sum = fma2(x[e], x[e], sum);
-        float lo, hi;
-        sum.get(lo, hi);
-        lo += hi;
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) lo += __shfl_xor_sync(FULL, lo, o);
-        r = rsqrtf(lo * (1.0f / D) + L.eps);
-      }
-      if (is_q) {
-        if (L.q_weight == nullptr) r = 1.0f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = mul2(part(y[e], sq[e], mul2(x[e], cq[e])), F2(r, r));
-        *reinterpret_cast<uint4*>(q_to + head * L.q_out.head_stride) = pack_pairs<T>(x);
-      } else if (is_k) {
-        if (L.k_weight == nullptr) r = 1.0f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = mul2(part(y[e], sk[e], mul2(x[e], ck[e])), F2(r, r));
-        if (off >= 0) *reinterpret_cast<uint4*>(k_to + (head - n_q) * L.kv.head_stride) = pack_pairs<T>(x);
-      } else if (head < n_q + 2 * n_kv && off >= 0) {
-        *reinterpret_cast<uint4*>(v_to + (head - n_q - n_kv) * L.kv.head_stride) = raw[u];
+    for (int u = 0; u < APPEND_BATCH; ++u) {
+      const int head = (at + u * spread) * PER_STEP + sub;
+      uint4 y = raw[u];
+      if ((at + u * spread) * PER_STEP < n_kv) y = turn(raw[u], L.k_weight != nullptr);  // uniform over the warp
+      if (off >= 0) {
+        if (head < n_kv)
+          *reinterpret_cast<uint4*>(k_to + head * L.kv.head_stride) = y;
+        else if (head < 2 * n_kv)
+          *reinterpret_cast<uint4*>(v_to + (head - n_kv) * L.kv.head_stride) = raw[u];
       }
     }
   }
@@ -252,7 +269,9 @@ __global__ void __launch_bounds__(COMMIT_THREADS) kv_commit_kernel(const CommitL
 
 template <typename T, int D>
 cudaError_t append(const AppendLaunch& L, cudaStream_t stream) {
-  const int nodes = L.B * L.nodes.count, steps = (L.n_q_heads + 2 * L.kv.n_kv_heads + 256 / D - 1) / (256 / D);
+  constexpr int PER_STEP = 256 / D;
+  const int nodes = L.B * L.nodes.count;
+  const int steps = (L.n_q_heads + PER_STEP - 1) / PER_STEP + (2 * L.kv.n_kv_heads + PER_STEP - 1) / PER_STEP;
   int spread = 1;  // warps per node
   while (spread < steps && static_cast<int64_t>(nodes) * spread < L.num_sms * APPEND_WARPS) spread *= 2;
   if (spread > steps) spread = steps;
