@@ -7,8 +7,12 @@
 namespace st {
 namespace {
 
-constexpr int APPEND_THREADS = 128, APPEND_BATCH = 4;  // vectors a lane has in flight
-constexpr int APPEND_WARPS = 32;                       // per SM, that a node's heads are spread over warps to reach
+constexpr int APPEND_THREADS = 64, APPEND_BATCH = 4;  // heads whose loads a lane has in flight
+// A node's heads are spread over warps until an SM has this many; a warp pays a
+// node's lookups and rotation row once, so few with more heads each are faster:
+// 8, 16 and 32 take 6.2, 9.2 and 10.0 us for 8 trees of 61 nodes (inputs past
+// the L2), 11.3, 13.2 and 18.3 for 32, 19.7, 19.7 and 22.1 for 64.
+constexpr int APPEND_WARPS = 8;
 constexpr int COMMIT_THREADS = 128;
 constexpr int COMMIT_BATCH = 8;  // path steps loaded before any is stored
 
@@ -33,40 +37,41 @@ __device__ __forceinline__ uint4 pack_pairs(const F2 (&x)[4]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One or more warps per node.  A head vector belongs to D / 8 neighbouring
-// lanes, 8 elements (16 bytes) each, so a warp takes 2 or 4 vectors a step; a
-// lane's place in the vector, and with it its part of the rotation row and of
-// the weights, is the same in every step.
+// One or more warps per node.  A head vector belongs to D / 16 neighbouring
+// lanes, two chunks of 8 elements (16 bytes) each: the two that turn with each
+// other (elements j and j + rot_dim / 2), or two neighbours where pairs are
+// neighbours or nothing turns.  So a warp takes 4 or 8 vectors a step, pairs
+// meet in their lane, and a lane's place in the vector, with it its part of the
+// rotation row and of the weights, is the same in every step.
 //
 // With u the vector before the norm, w the weights and r = 1 / rms(u), a turned
 // element is r (u_j (w_j c) + u_p (w_p s)), p its partner, s with the sign of
-// j's place in the pair: the products in brackets are made once per node, and a
-// lane gets its partners' u by shuffling the raw 16 bytes.
+// j's place in the pair: the products in brackets are made once per node.
 //
-// Everything is read and written once; what bounds it is the issue rate.  At
-// 64 trees of 61 nodes of 48 heads of 128, normalised (95 MB: 14 us at the
-// measured bandwidth): 21.2 us (22.9 with queries' and keys' products held side
-// by side and chosen per vector).  One vector per thread, with a node's loads and
-// products made for each, took 37.2 us; three per thread 34.3 (253 instructions
-// a step of a warp, of which this leaves 139).
-template <typename T, int D>
+// Everything is read and written once; what bounds it is the issue rate and the
+// loads in flight.  At 64 trees of 61 nodes of 48 heads of 128, normalised (95 MB:
+// 14 us at the measured bandwidth): 19.6 us with inputs past the L2, 16 with them
+// in it.  One chunk per lane, the partner's got by shuffles, took 24.5 (21.2 in
+// the L2), with a warp per 32nd of an SM at most; one vector per thread, with a
+// node's loads and products made for each, 37.2 in the L2.
+template <typename T, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_constant__ AppendLaunch L, int page_shift,
                                                                    int nodes, int spread) {
-  constexpr int LANES = D / 8, PER_STEP = 32 / LANES;
+  constexpr int LANES = D / 16, PER_STEP = 32 / LANES;
   const int lane = threadIdx.x % LANES, sub = threadIdx.x % 32 / LANES;
   const int warp = blockIdx.x * (APPEND_THREADS / 32) + threadIdx.x / 32;
   const int node = warp / spread;
   if (node >= nodes) return;
   const int n_q = L.n_q_heads, n_kv = L.kv.n_kv_heads;
   const int b = node / L.nodes.count, i = node - b * L.nodes.count, n = L.nodes.begin + i;
-  // pairs are elements j and j + rot_dim / 2, `half` lanes apart, or neighbours
-  const int half = L.rot_dim / 16;
-  const bool in_rot = lane < 2 * half, first = lane < half;
-  const int partner = !in_rot || L.interleaved ? lane : (first ? lane + half : lane - half);
-  const T* q = static_cast<const T*>(L.q.data) + b * L.q.tree_stride + i * L.q.node_stride + lane * 8;
-  const T* k = static_cast<const T*>(L.k.data) + b * L.k.tree_stride + i * L.k.node_stride + lane * 8;
-  const T* w = static_cast<const T*>(L.v.data) + b * L.v.tree_stride + i * L.v.node_stride + lane * 8;
-  T* q_to = static_cast<T*>(L.q_out.data) + b * L.q_out.tree_stride + i * L.q_out.node_stride + lane * 8;
+  const int half = L.rot_dim / 16;  // lanes whose chunks turn
+  // the first elements of the lane's chunks
+  const int e0 = 8 * (!INTERLEAVED && lane < half ? lane : 2 * lane);
+  const int e1 = e0 + 8 * (!INTERLEAVED && lane < half ? half : 1);
+  const T* q = static_cast<const T*>(L.q.data) + b * L.q.tree_stride + i * L.q.node_stride;
+  const T* k = static_cast<const T*>(L.k.data) + b * L.k.tree_stride + i * L.k.node_stride;
+  const T* w = static_cast<const T*>(L.v.data) + b * L.v.tree_stride + i * L.v.node_stride;
+  T* q_to = static_cast<T*>(L.q_out.data) + b * L.q_out.tree_stride + i * L.q_out.node_stride;
   grid_dependency_wait();
   grid_dependents_launch();
 
@@ -75,18 +80,26 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
   // products lives at a time
   const int step0 = warp - node * spread, q_steps = (n_q + PER_STEP - 1) / PER_STEP;
   const int kv_step0 = (step0 < q_steps ? (q_steps - step0 + spread - 1) / spread * spread : 0) + step0 - q_steps;
-  uint4 raw[APPEND_BATCH];
+  uint4 raw[APPEND_BATCH][2];
+  auto load = [&](int u, const T* from) {
+    raw[u][0] = *reinterpret_cast<const uint4*>(from + e0);
+    raw[u][1] = *reinterpret_cast<const uint4*>(from + e1);
+  };
+  auto store = [&](T* to, const uint4 (&x)[2]) {
+    *reinterpret_cast<uint4*>(to + e0) = x[0];
+    *reinterpret_cast<uint4*>(to + e1) = x[1];
+  };
   auto fetch = [&](bool queries, int step) {
 #pragma unroll
     for (int u = 0; u < APPEND_BATCH; ++u) {
       const int head = (step + u * spread) * PER_STEP + sub;
-      raw[u] = make_uint4(0, 0, 0, 0);
+      raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
       if (queries) {
-        if (head < n_q) raw[u] = *reinterpret_cast<const uint4*>(q + head * L.q.head_stride);
+        if (head < n_q) load(u, q + head * L.q.head_stride);
       } else if (head < n_kv) {
-        raw[u] = *reinterpret_cast<const uint4*>(k + head * L.k.head_stride);
+        load(u, k + head * L.k.head_stride);
       } else if (head < 2 * n_kv) {
-        raw[u] = *reinterpret_cast<const uint4*>(w + (head - n_kv) * L.v.head_stride);
+        load(u, w + (head - n_kv) * L.v.head_stride);
       }
     }
   };
@@ -95,79 +108,72 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
   const int depth = L.nodes.depth ? L.nodes.depth[static_cast<int64_t>(b) * L.nodes.stride + n] : n;
   if (len < 0 && threadIdx.x % 32 == 0) set_status(L.status, SPEC_TREE_S_NODES);
   if (n >= cnt || len < 0) {
-    for (int step = step0; step * PER_STEP < n_q; step += spread)
-      if (step * PER_STEP + sub < n_q)
-        *reinterpret_cast<uint4*>(q_to + (step * PER_STEP + sub) * L.q_out.head_stride) = make_uint4(0, 0, 0, 0);
+    const uint4 zeros[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    for (int head = step0 * PER_STEP + sub; head < n_q; head += spread * PER_STEP)
+      store(q_to + head * L.q_out.head_stride, zeros);
     return;
   }
   const int64_t off = kv_slot_offset(L.kv, b, static_cast<int64_t>(len) + n, page_shift);
   if (off < 0 && threadIdx.x % 32 == 0) set_status(L.status, SPEC_TREE_S_PAGES);
 
-  // c and signed s of the lane's elements
+  // the lane's 8 pairs' part of the rotation row
   const int64_t pos = static_cast<int64_t>(len) + depth;
-  const bool turned = L.rot_dim > 0 && depth >= 0 && pos < L.rope_rows;
+  const bool turned = L.rot_dim > 0 && depth >= 0 && pos < L.rope_rows, turns = turned && lane < half;
   if (L.rot_dim > 0 && !turned && threadIdx.x % 32 == 0) set_status(L.status, SPEC_TREE_S_NODES);
-  F2 c[4], s[4];
+  float4 c[2], s[2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) c[e] = F2(1.0f, 1.0f), s[e] = F2(0.0f, 0.0f);
-  const bool turns = turned && in_rot;
-  if (turns) {
-    const float* row = L.rope + pos * L.rot_dim;
-    if (L.interleaved) {
-      const float4 x = *reinterpret_cast<const float4*>(row + lane * 4);
-      const float4 y = *reinterpret_cast<const float4*>(row + L.rot_dim / 2 + lane * 4);
-      c[0] = F2(x.x, x.x), c[1] = F2(x.y, x.y), c[2] = F2(x.z, x.z), c[3] = F2(x.w, x.w);
-      s[0] = F2(-y.x, y.x), s[1] = F2(-y.y, y.y), s[2] = F2(-y.z, y.z), s[3] = F2(-y.w, y.w);
+  for (int e = 0; e < 2; ++e) {
+    c[e] = make_float4(1.0f, 1.0f, 1.0f, 1.0f), s[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!turns) continue;
+    const float* row = L.rope + pos * L.rot_dim + lane * 8 + 4 * e;
+    c[e] = *reinterpret_cast<const float4*>(row);
+    s[e] = *reinterpret_cast<const float4*>(row + L.rot_dim / 2);
+  }
+  auto flip = [](F2 x) {  // the other element of a neighbouring pair
+    float lo, hi;
+    x.get(lo, hi);
+    return F2(hi, lo);
+  };
+  F2 cw[2][4], sw[2][4];  // with the weights of the heads in hand
+  auto weighted = [&](const void* weight) {
+    F2 x[2][4];
+    if (weight != nullptr) {
+      unpack_pairs<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(weight) + e0), x[0]);
+      unpack_pairs<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(weight) + e1), x[1]);
     } else {
-      const float* at = row + (first ? lane : lane - half) * 8;
-      const float sign = first ? -1.0f : 1.0f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float4 x = *reinterpret_cast<const float4*>(at + 4 * e);
-        const float4 y = *reinterpret_cast<const float4*>(at + L.rot_dim / 2 + 4 * e);
-        c[2 * e] = F2(x.x, x.y), c[2 * e + 1] = F2(x.z, x.w);
-        s[2 * e] = F2(sign * y.x, sign * y.y), s[2 * e + 1] = F2(sign * y.z, sign * y.w);
+      for (int e = 0; e < 4; ++e) x[0][e] = x[1][e] = F2(1.0f, 1.0f);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (INTERLEAVED) {
+        cw[e][0] = mul2(x[e][0], F2(c[e].x, c[e].x)), sw[e][0] = mul2(flip(x[e][0]), F2(-s[e].x, s[e].x));
+        cw[e][1] = mul2(x[e][1], F2(c[e].y, c[e].y)), sw[e][1] = mul2(flip(x[e][1]), F2(-s[e].y, s[e].y));
+        cw[e][2] = mul2(x[e][2], F2(c[e].z, c[e].z)), sw[e][2] = mul2(flip(x[e][2]), F2(-s[e].z, s[e].z));
+        cw[e][3] = mul2(x[e][3], F2(c[e].w, c[e].w)), sw[e][3] = mul2(flip(x[e][3]), F2(-s[e].w, s[e].w));
+      } else {
+        const F2 c0(c[e].x, c[e].y), c1(c[e].z, c[e].w), s0(s[e].x, s[e].y), s1(s[e].z, s[e].w);
+        const F2 m0(-s[e].x, -s[e].y), m1(-s[e].z, -s[e].w);
+        cw[0][2 * e] = mul2(x[0][2 * e], c0), cw[0][2 * e + 1] = mul2(x[0][2 * e + 1], c1);
+        cw[1][2 * e] = mul2(x[1][2 * e], c0), cw[1][2 * e + 1] = mul2(x[1][2 * e + 1], c1);
+        sw[0][2 * e] = mul2(x[1][2 * e], m0), sw[0][2 * e + 1] = mul2(x[1][2 * e + 1], m1);
+        sw[1][2 * e] = mul2(x[0][2 * e], s0), sw[1][2 * e + 1] = mul2(x[0][2 * e + 1], s1);
       }
     }
-  }
-  auto swapped = [&](uint4 x) {  // the other element of each neighbouring pair
-    return make_uint4(__byte_perm(x.x, 0, 0x1032), __byte_perm(x.y, 0, 0x1032), __byte_perm(x.z, 0, 0x1032),
-                      __byte_perm(x.w, 0, 0x1032));
   };
-  F2 cw[4], sw[4];  // with the weights of the heads in hand
-  auto weighted = [&](const void* weight) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) cw[e] = c[e], sw[e] = s[e];
-    if (weight == nullptr) return;
-    F2 x[4], y[4];
-    unpack_pairs<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(weight) + lane * 8), x);
-    const uint4 other = *reinterpret_cast<const uint4*>(static_cast<const T*>(weight) + partner * 8);
-    unpack_pairs<T>(L.interleaved ? swapped(other) : other, y);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) cw[e] = mul2(c[e], x[e]), sw[e] = mul2(s[e], y[e]);
-  };
-  // the vector normalised (if there are weights) and turned; the whole warp
-  // takes part in the shuffles, whatever its lanes hold
-  auto turn = [&](uint4 u, bool norm) {
-    uint4 other = u;
-    if (L.interleaved) {
-      other = swapped(other);
-    } else {
-      other.x = __shfl_sync(FULL, other.x, partner, LANES);
-      other.y = __shfl_sync(FULL, other.y, partner, LANES);
-      other.z = __shfl_sync(FULL, other.z, partner, LANES);
-      other.w = __shfl_sync(FULL, other.w, partner, LANES);
-    }
-    F2 x[4], y[4];
-    unpack_pairs<T>(u, x);
-    unpack_pairs<T>(other, y);
+  // the vector normalised (if there are weights) and turned, in place; the whole
+  // warp takes part in the sum, whatever its lanes hold
+  auto turn = [&](uint4 (&u)[2], bool norm) {
+    F2 x[2][4];
+    unpack_pairs<T>(u[0], x[0]);
+    unpack_pairs<T>(u[1], x[1]);
     F2 r(1.0f, 1.0f);
     if (norm) {
-      F2 sum = mul2(x[0], x[0]);
+      F2 sum = mul2(x[0][0], x[0][0]), more = mul2(x[1][0], x[1][0]);
 #pragma unroll
-      for (int e = 1; e < 4; ++e) sum = fma2(x[e], x[e], sum);
+      for (int e = 1; e < 4; ++e) sum = fma2(x[0][e], x[0][e], sum), more = fma2(x[1][e], x[1][e], more);
       float lo, hi;
-      sum.get(lo, hi);
+      add2(sum, more).get(lo, hi);
       lo += hi;
 #pragma unroll
       for (int o = LANES / 2; o > 0; o >>= 1) lo += __shfl_xor_sync(FULL, lo, o);
@@ -175,12 +181,17 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
       r = F2(lo, lo);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[e] = mul2(x[e], cw[e]);
-      if (turns) x[e] = fma2(y[e], sw[e], x[e]);  // elsewhere an infinity times the zero of s would be a NaN
-      x[e] = mul2(x[e], r);
+    for (int h = 0; h < 2; ++h) {
+      F2 y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[e] = mul2(x[h][e], cw[h][e]);
+        // elsewhere an infinity times the zero of s would be a NaN
+        if (turns) y[e] = fma2(INTERLEAVED ? flip(x[h][e]) : x[1 - h][e], sw[h][e], y[e]);
+        y[e] = mul2(y[e], r);
+      }
+      u[h] = pack_pairs<T>(y);
     }
-    return pack_pairs<T>(x);
   };
 
   weighted(L.q_weight);
@@ -189,25 +200,28 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
 #pragma unroll
     for (int u = 0; u < APPEND_BATCH; ++u) {
       const int head = (at + u * spread) * PER_STEP + sub;
-      const uint4 y = turn(raw[u], L.q_weight != nullptr);
-      if (head < n_q) *reinterpret_cast<uint4*>(q_to + head * L.q_out.head_stride) = y;
+      turn(raw[u], L.q_weight != nullptr);
+      if (head < n_q) store(q_to + head * L.q_out.head_stride, raw[u]);
     }
   }
   weighted(L.k_weight);
-  T* k_to = static_cast<T*>(L.kv.k) + L.layer * L.kv.layer_stride + off + lane * 8;
-  T* v_to = static_cast<T*>(L.kv.v) + L.layer * L.kv.layer_stride + off + lane * 8;
+  T* k_to = static_cast<T*>(L.kv.k) + L.layer * L.kv.layer_stride + off;
+  T* v_to = static_cast<T*>(L.kv.v) + L.layer * L.kv.layer_stride + off;
   for (int at = kv_step0; at * PER_STEP < 2 * n_kv; at += APPEND_BATCH * spread) {
     fetch(false, at);
 #pragma unroll
     for (int u = 0; u < APPEND_BATCH; ++u) {
       const int head = (at + u * spread) * PER_STEP + sub;
-      uint4 y = raw[u];
-      if ((at + u * spread) * PER_STEP < n_kv) y = turn(raw[u], L.k_weight != nullptr);  // uniform over the warp
+      if ((at + u * spread) * PER_STEP < n_kv) {  // uniform over the warp
+        const uint4 v0 = raw[u][0], v1 = raw[u][1];
+        turn(raw[u], L.k_weight != nullptr);
+        if (head >= n_kv) raw[u][0] = v0, raw[u][1] = v1;  // a value beside keys
+      }
       if (off >= 0) {
         if (head < n_kv)
-          *reinterpret_cast<uint4*>(k_to + head * L.kv.head_stride) = y;
+          store(k_to + head * L.kv.head_stride, raw[u]);
         else if (head < 2 * n_kv)
-          *reinterpret_cast<uint4*>(v_to + (head - n_kv) * L.kv.head_stride) = raw[u];
+          store(v_to + (head - n_kv) * L.kv.head_stride, raw[u]);
       }
     }
   }
@@ -267,17 +281,22 @@ __global__ void __launch_bounds__(COMMIT_THREADS) kv_commit_kernel(const CommitL
   }
 }
 
-template <typename T, int D>
-cudaError_t append(const AppendLaunch& L, cudaStream_t stream) {
-  constexpr int PER_STEP = 256 / D;
+template <typename T, int D, bool INTERLEAVED>
+cudaError_t append_as(const AppendLaunch& L, cudaStream_t stream) {
+  constexpr int PER_STEP = 512 / D;
   const int nodes = L.B * L.nodes.count;
   const int steps = (L.n_q_heads + PER_STEP - 1) / PER_STEP + (2 * L.kv.n_kv_heads + PER_STEP - 1) / PER_STEP;
   int spread = 1;  // warps per node
   while (spread < steps && static_cast<int64_t>(nodes) * spread < L.num_sms * APPEND_WARPS) spread *= 2;
   if (spread > steps) spread = steps;
   const int64_t ctas = (static_cast<int64_t>(nodes) * spread + APPEND_THREADS / 32 - 1) / (APPEND_THREADS / 32);
-  return launch_pdl(kv_append_kernel<T, D>, dim3(static_cast<unsigned>(ctas)), dim3(APPEND_THREADS), 0, stream, L,
+  return launch_pdl(kv_append_kernel<T, D, INTERLEAVED>, dim3(static_cast<unsigned>(ctas)), dim3(APPEND_THREADS), 0, stream, L,
                     log2_of(L.kv.page_size), nodes, spread);
+}
+
+template <typename T, int D>
+cudaError_t append(const AppendLaunch& L, cudaStream_t stream) {
+  return L.interleaved ? append_as<T, D, true>(L, stream) : append_as<T, D, false>(L, stream);
 }
 
 }  // namespace

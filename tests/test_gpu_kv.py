@@ -367,6 +367,7 @@ def test_append(dtype, D, rot, interleaved):
     dict(lens=[9, 300], N=8, Hq=7, Hkv=1, D=64, page=256, begin=17, layout="head"),
     dict(lens=[3], N=90, Hq=4, Hkv=2, D=128, page=64, tree=False, norm=True, layers=3, layer=1),
     dict(lens=[5, 6], N=10, Hq=8, Hkv=2, D=128, page=32, norm=True, in_place=True),
+    dict(lens=list(range(40)), N=32, Hq=20, Hkv=3, D=128, page=16, norm=True),  # a warp takes a node whole
 ])
 def test_append_shapes(kw):
     _check_append(51, **kw)
