@@ -85,12 +85,12 @@ struct Plan {
   int q_box;           // nodes of a copy of queries
 };
 
-// Parts of items: slot 0 of a CTA for one that began before it, slot 1 for one
-// that goes on after it.
 struct JoinRecord {
   int32_t parts, b, row0, head;  // parts = 0: nothing to join
 };
 
+// Parts of items: slot 0 of a CTA for one that began before it, slot 1 for one
+// that goes on after it.
 struct Workspace {
   uint32_t* arrived;    // [CTA where the item begins][softmax warp]: parts left; zero between calls
   JoinRecord* records;  // [CTA]: the item of which it has the first piece, for the join kernel

@@ -52,8 +52,8 @@ __device__ __forceinline__ uint4 pack_pairs(const F2 (&x)[4]) {
 // loads in flight.  At 64 trees of 61 nodes of 48 heads of 128, normalised (95 MB:
 // 14 us at the measured bandwidth): 19.6 us with inputs past the L2, 16 with them
 // in it.  One chunk per lane, the partner's got by shuffles, took 24.5 (21.2 in
-// the L2), with a warp per 32nd of an SM at most; one vector per thread, with a
-// node's loads and products made for each, 37.2 in the L2.
+// the L2); one vector per thread, with a node's loads and products made for
+// each, 37.2 in the L2.
 template <typename T, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_constant__ AppendLaunch L, int page_shift,
                                                                    int nodes, int spread) {
