@@ -381,7 +381,7 @@ class KVCache:
 
     k, v: [layers][pages][page_size][kv heads][head_dim], bf16 or f16, any strides with contiguous
     head_dim (a [layers][pages][heads][page_size][head_dim] pool is passed transposed);
-    page_table: int32 [B][max_pages]; seq_len: int32 [B], committed tokens.
+    page_table: int32 [B][max_pages], a row for each sequence (contiguous, none over another); seq_len: int32 [B], committed tokens.
     """
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor):
@@ -393,11 +393,14 @@ class KVCache:
             raise SpecTreeError("head_dim must be contiguous")
         if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1:
             raise SpecTreeError("page_table must be int32 [B][max_pages] with contiguous rows")
+        rows, width = page_table.shape
+        table_stride = page_table.stride(0) if rows > 1 else width  # the stride of a single row means nothing
+        if not width <= table_stride < 1 << 31:
+            raise SpecTreeError("rows of page_table overlap (an expanded table is to be copied) or lie too far apart")
         self.k, self.v, self.page_table, self.B = k, v, page_table, page_table.shape[0]
         layers, pages, size, heads, dim = k.shape
         c = c_kv(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), None, k.stride(0), k.stride(1), k.stride(2),
-                 k.stride(3), _HALF[k.dtype], layers, pages, size, heads, dim, page_table.shape[1],
-                 max(page_table.stride(0), page_table.shape[1]))
+                 k.stride(3), _HALF[k.dtype], layers, pages, size, heads, dim, width, table_stride)
         self._c, self.at = c, ctypes.addressof(c)
         self.shape = (self.B, heads, dim, k.dtype)
         self.set_lengths(seq_len)

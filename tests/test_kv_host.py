@@ -144,6 +144,20 @@ def test_binding_refuses_tensors_of_another_kind(B):
         B.spec_tree_attend(cache, 0, q, q.clone(), None, status, tree=B.NodeArrays(torch.zeros((3, 4), dtype=torch.int32)))
 
 
+def test_page_tables_whose_rows_overlap_are_refused(B):
+    """An expanded table holds one row: read as B rows, it would be read past its end."""
+    k, data = torch.zeros((1, 4, 16, 2, 64), dtype=torch.bfloat16), torch.arange(40, dtype=torch.int32)
+    lens = torch.zeros(4, dtype=torch.int32)
+    for bad in (data[:3].expand(4, -1), data[:3][None].expand(4, -1), data.as_strided((4, 3), (2, 1))):
+        with pytest.raises(B.SpecTreeError, match="overlap"):
+            B.KVCache(k, k.clone(), bad, lens)
+    for good, stride in ((data[:12].view(4, 3), 3), (data.view(4, 10)[:, 2:5], 10), (data[:4].view(4, 1), 1)):
+        c = B.KVCache(k, k.clone(), good, lens).c()
+        assert (c.max_pages, c.table_stride, c.page_table) == (good.shape[1], stride, good.data_ptr())
+    for one in (data[:3].expand(1, -1), data.as_strided((1, 3), (1, 1)), data.as_strided((1, 3), (1 << 40, 1))):
+        assert B.KVCache(k, k.clone(), one, lens[:1]).c().table_stride == 3  # the stride of a single row means nothing
+
+
 def test_structs_match_the_c_header(B, tmp_path):
     import shutil
     import subprocess
