@@ -870,6 +870,7 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
       uint32_t n = 0;
       if (lane == 0) n = load_acquire(arrived);
       rest_there = __shfl_sync(FULL, n, 0) + 1 == static_cast<uint32_t>(parts);
+      __syncwarp();  // a shuffle orders no memory: the lanes' loads of the parts behind lane 0's acquire
       if (rest_there) {
         if (lane == 0) *arrived = 0;
         float2 ms[JOIN_PARTS - 1];
@@ -958,14 +959,20 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
     if (both) warps_meet(5 + warp, 64);
     if (finish) continue;
     if (P.join_inside || !C.pieces) {
-      // this part is there; the last to say so for its rows puts them together
-      __threadfence();
+      // this part is there; the last to say so for its rows puts them together.
+      // Lane 0's fences stand between the lanes' stores and its count, and between
+      // its count and their loads of the other parts.
       __syncwarp();
       uint32_t before = 0;
-      if (lane == 0) before = atomicAdd(arrived, 1);
-      if (__shfl_sync(FULL, before, 0) + 1 == static_cast<uint32_t>(parts)) {
-        if (lane == 0) *arrived = 0;
+      if (lane == 0) {
         __threadfence();
+        before = atomicAdd(arrived, 1);
+        __threadfence();
+      }
+      const bool last = __shfl_sync(FULL, before, 0) + 1 == static_cast<uint32_t>(parts);
+      __syncwarp();
+      if (last) {
+        if (lane == 0) *arrived = 0;
         join_rows<T, D>(P, ws, JoinRecord{parts, s.b, s.row0, s.head}, s.cnt, from, local - lane,
                         min(32, P.half_rows - warp * 32), lane, 32);
       }
