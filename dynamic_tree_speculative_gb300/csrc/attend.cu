@@ -335,7 +335,8 @@ __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* map,
   Walk<Y::HALVES> walk(C);
   const Segment& s = walk.s;
   uint32_t n = 0;  // loads so far
-  while (walk.next(P)) {
+  bool ok = true;
+  while (ok && walk.next(P)) {
     const int32_t* table = P.L.kv.page_table + static_cast<int64_t>(s.b) * P.L.kv.table_stride;
     auto entry = [&](int t) {  // the page of this lane's copy of tile t
       const int slot = t * TILE + lane * P.box;
@@ -352,11 +353,8 @@ __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* map,
       const int off = uniform(P.box == TILE ? (t * TILE) & (P.L.kv.page_size - 1) : 0);
       const int used = s.end > 0 ? min(boxes, (s.end - t * TILE + P.box - 1) / P.box) : 0;
       const int slot = n % SLOTS;
-      if (!warp_wait(&empty[slot], ((n / SLOTS) & 1) ^ 1, C, P.L.status)) {
-        // copies in flight land before the CTA ends
-        for (uint32_t o = n > SLOTS ? n - SLOTS : 0; o < n; ++o) mbar_wait(&full[o % SLOTS], (o / SLOTS) & 1);
-        return;
-      }
+      ok = warp_wait(&empty[slot], ((n / SLOTS) & 1) ^ 1, C, P.L.status);
+      if (!ok) break;
       if (elect()) mbar_expect_tx(&full[slot], used * P.box * 128 * Y::PANELS);
       const uint32_t to = uniform(ring + slot * Y::KV_BYTES), head = uniform(s.head);
 #pragma unroll 1
@@ -377,12 +375,15 @@ __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* map,
       }
     }
   }
+  // copies in flight land before the CTA ends, whichever role has given up (if
+  // none has, the products have waited for them)
+  for (uint32_t o = n > SLOTS ? n - SLOTS : 0; o < n; ++o) mbar_wait(&full[o % SLOTS], (o / SLOTS) & 1);
 }
 
 // One warp: the products.  The halves take turns, so that while one half's
-// weights are made the other half's products run.  False: a wait gave up.
+// weights are made the other half's products run.  It ends early where a wait gives up.
 template <typename T, int D, bool PAIR>
-__device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem) {
+__device__ __forceinline__ void product_role(const Plan& P, Control& C, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem) {
   using Y = Layout<D, PAIR>;
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t ID_S = mma_descriptor(BF, TILE, false), ID_O = mma_descriptor(BF, D, true);
@@ -461,11 +462,11 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
 
   while (walk.next(P)) {
     const int count = s.last - s.first;
-    if (!warp_wait(&C.q_full, segment & 1, C, status) || !keys(n)) return false;
+    if (!warp_wait(&C.q_full, segment & 1, C, status) || !keys(n)) return;
     tmem_fence_after();
 #pragma unroll 1
     for (int h = 0; h < 2 && (!PAIR || h < count); ++h) {
-      if (PAIR && h == 1 && !keys(n + 1)) return false;
+      if (PAIR && h == 1 && !keys(n + 1)) return;
       scores(h, PAIR ? n + h : n);
       if (PAIR) give_back(&C.k_empty[(n + h) % Y::KS]);
     }
@@ -476,9 +477,9 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
 #pragma unroll 1
       for (int x = 0; x < count; ++x) {
         const bool more = x + 2 < count;
-        if (!values(s.first + x, n + x) || !output(x & 1, n + x, x < 2, !more)) return false;
+        if (!values(s.first + x, n + x) || !output(x & 1, n + x, x < 2, !more)) return;
         if (more) {
-          if (!keys(n + x + 2)) return false;
+          if (!keys(n + x + 2)) return;
           tmem_fence_after();
           scores(x & 1, n + x + 2);
           give_back(&C.k_empty[(n + x + 2) % Y::KS]);
@@ -489,10 +490,10 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
 #pragma unroll 1
       for (int x = 0; x < count; ++x) {
         const bool more = x + 1 < count;
-        if (!values(s.first + x, n + x) || (more && !keys(n + x + 1))) return false;
+        if (!values(s.first + x, n + x) || (more && !keys(n + x + 1))) return;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h)
-          if (!output(h, n + x, x == 0, !more)) return false;
+          if (!output(h, n + x, x == 0, !more)) return;
         if (more) give_back(&C.k_empty[(n + x + 1) % Y::KS]);
         if (x + 2 == count) give_back(&C.q_empty);
       }
@@ -500,7 +501,6 @@ __device__ __forceinline__ bool product_role(const Plan& P, Control& C, uint32_t
     n += count;
     ++segment;
   }
-  return true;
 }
 
 // Whether a 128-byte row holds an infinity or a NaN: those times zero are NaN.
@@ -532,9 +532,11 @@ __device__ __forceinline__ void side_role(const Plan& P, const CUtensorMap* mq, 
   uint32_t* status = P.L.status;
   Walk<Y::HALVES> walk(C);
   const Segment& s = walk.s;
-  uint32_t segment = 0, n = 0;  // segments, tiles so far
-  for (; walk.next(P); ++segment) {
-    if (!warp_wait(&C.q_empty, (segment & 1) ^ 1, C, status)) return;
+  uint32_t segment = 0, n = 0, asked = 0;  // segments, tiles, segments whose queries have been asked for so far
+  bool ok = true;
+  for (; ok && walk.next(P); ++segment) {
+    ok = warp_wait(&C.q_empty, (segment & 1) ^ 1, C, status);
+    if (!ok) break;
     const int node = node_of_row(P, s.row0);
     if (elect()) {
       mbar_expect_more(&C.q_full, Y::HALVES * Y::PANELS * P.q_box * P.group * 128);
@@ -556,11 +558,13 @@ __device__ __forceinline__ void side_role(const Plan& P, const CUtensorMap* mq, 
       }
     }
     warp_arrive(&C.q_full);
+    asked = segment + 1;
 
     const int first_masked = s.clear / TILE;
     for (int j = s.first; j < s.last; ++j, ++n) {
       const int slot = n % Y::VS;
-      if (!warp_wait(&C.v_full[slot], (n / Y::VS) & 1, C, status)) return;
+      ok = warp_wait(&C.v_full[slot], (n / Y::VS) & 1, C, status);
+      if (!ok) break;
       if (j >= first_masked) {
 #pragma unroll 1
         for (int part = 0; part < TILE / 32; ++part) {
@@ -593,6 +597,7 @@ __device__ __forceinline__ void side_role(const Plan& P, const CUtensorMap* mq, 
       warp_arrive(&C.v_empty[slot]);
     }
   }
+  if (asked > 0) mbar_wait(&C.q_full, (asked - 1) & 1);  // as load_role: queries in flight land before the CTA ends
 }
 
 // What the zeros in the place of values that are not finite have left out of a
@@ -1164,10 +1169,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == HELPERS + 1) {
       load_role<D, PAIR, false>(P, &mv, C, smem_u32(v_ring));
     } else if (warp == HELPERS + 2) {
-      if (!product_role<T, D, PAIR>(P, C, smem_u32(smem), smem_u32(k_ring), smem_u32(v_ring))) {
-        if (elect()) mma_commit(&C.drain);  // products in flight end before their memory is given back
-        mbar_wait(&C.drain, 0);
-      }
+      product_role<T, D, PAIR>(P, C, smem_u32(smem), smem_u32(k_ring), smem_u32(v_ring));
+      // products in flight end before their memory is given back, also where it
+      // is the softmax that has given up and no longer waits for them
+      if (elect()) mma_commit(&C.drain);
+      __syncwarp();
+      mbar_wait(&C.drain, 0);
     } else {
       side_role<T, D, PAIR>(P, &mq, C, smem_u32(smem), v_ring);
     }
