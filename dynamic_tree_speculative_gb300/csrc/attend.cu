@@ -41,8 +41,20 @@
 //
 // Tokens a row does not see get S = -inf.  Their values enter the product
 // with weight zero, so in tiles that not every row sees whole, infinities and
-// NaN among the values are replaced by zero in shared memory first, and added
-// at the end to the rows that do see them.
+// NaN among the values are replaced by zero in shared memory first.
+//
+// Values that are not finite.  A seen one counts whatever its weight: an element
+// of a row's output is the sum of the seen values there that are not finite, if
+// there are any.  The products say no more than that there are some: a weight or
+// a rescaling that is zero in its few bits makes NaN of an infinity.  So a row
+// whose output is not finite though its weights are has the segment's values
+// read again (settle), each part of an item carries its own sum, and the join
+// adds those of the parts (settle_joined).  Where all is finite that costs a
+// product with zero per element of the output: 0.2 to 0.5 us of 10 to 38 us where
+// segments are few (one token of one short sequence 9.7 -> 10.1, frontier 34.9 ->
+// 35.5, 32 key heads 37.3 -> 37.6), nothing where they are many.  With an infinity
+// in every page, calls take 4 to 10 times as long (one token of 64 sequences 166
+// -> 1610 us, 8 trees 38 -> 141); where all elements are NaN the reading stops.
 #include <cuda.h>
 #include <math.h>
 
@@ -600,34 +612,128 @@ __device__ __forceinline__ void side_role(const Plan& P, const CUtensorMap* mq, 
   if (asked > 0) mbar_wait(&C.q_full, (asked - 1) & 1);  // as load_role: queries in flight land before the CTA ends
 }
 
-// What the zeros in the place of values that are not finite have left out of a
-// row, added to what the row's thread has just written (`out`, or `partial` in
-// the workspace's order).
+// Whether some of the numbers taken are not finite: those times zero are NaN.
+struct Finite {
+  F2 acc[4];
+  __device__ __forceinline__ Finite() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = F2(0.0f, 0.0f);
+  }
+  template <int N>
+  __device__ __forceinline__ void take(const uint32_t (&x)[N]) {
+    const F2 zero(0.0f, 0.0f);
+#pragma unroll
+    for (int e = 0; e < N; e += 2)
+      acc[e / 2 % 4] = fma2(F2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), zero, acc[e / 2 % 4]);
+  }
+  __device__ __forceinline__ bool all() const {
+    float a, b;
+    add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])).get(a, b);
+    return !isnan(a + b);
+  }
+};
+
+// A whole warp, a row each: the elements where the row sees values of the segment
+// that are not finite become their sum, in what the row's thread has just written
+// (`out`, or `partial` in the workspace's order) if the row `counts`.  `again`:
+// values that every row sees may be among them, and are read again, 32 tokens at
+// a time; the others are those that `odd` names.
 template <typename T, int D>
-__device__ __noinline__ void add_odd(const Plan& P, const Segment& s, const uint32_t* odd, int from, int node, T* out,
-                                     float* partial) {
-  const int first_masked = s.clear / TILE;
+__device__ __noinline__ void settle(const Plan& P, const Segment& s, const uint32_t* odd, bool again, bool counts, int node,
+                                    T* out, float* partial) {
+  const int lane = threadIdx.x % 32, first_masked = s.clear / TILE;
+  const T* values = static_cast<const T*>(P.L.kv.v) + P.L.layer * P.L.kv.layer_stride + s.head * P.L.kv.head_stride;
+  auto element = [&](int d) { return partial + static_cast<int64_t>(d / 4) * P.ws_rows * 4 + d % 4; };
+  if (again) {
+    // lane x of a token's LANES neighbouring ones has its elements 8 x .. 8 x + 7
+    constexpr int LANES = D / 8;
+    float sum[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+    const int end = min(s.last * TILE, min(s.clear, s.end));
+    auto place = [&](int t) { return t < end ? kv_slot_offset(P.L.kv, s.b, t, P.page_shift) : -1; };
+    int64_t next = place(s.first * TILE + lane);
+#pragma unroll 1
+    for (int t0 = s.first * TILE; t0 < end; t0 += 32) {
+      const int64_t off = next;
+      uint4 w[LANES];
+#pragma unroll
+      for (int x = 0; x < LANES; ++x) {
+        const int64_t at = __shfl_sync(FULL, off, x * (32 / LANES) + lane / LANES);
+        w[x] = at < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(values + at + lane % LANES * 8);
+      }
+      next = place(t0 + 32 + lane);
+#pragma unroll
+      for (int x = 0; x < LANES; ++x) {
+        float y[8];
+        unpack8<T>(w[x], y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (!isfinite(y[e])) sum[e] += y[e];
+      }
+      bool done = true;  // NaN everywhere: it stays so
+#pragma unroll
+      for (int e = 0; e < 8; ++e) done = done && isnan(sum[e]);
+      if (__all_sync(FULL, done)) break;
+    }
+#pragma unroll
+    for (int o = LANES; o < 32; o *= 2)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor_sync(FULL, sum[e], o);
+#pragma unroll 1
+    for (int x = 0; x < LANES; ++x) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = __shfl_sync(FULL, sum[e], x);
+        if (!counts || y == 0.0f) continue;
+        if (out)
+          out[x * 8 + e] = T(y);
+        else
+          *element(x * 8 + e) = y;
+      }
+    }
+  }
+  if (!counts) return;
   const int32_t* parent = P.L.nodes.parent + static_cast<int64_t>(s.b) * P.L.nodes.stride;
-  for (int j = from; j < s.last; ++j) {
+#pragma unroll 1
+  for (int j = max(s.first, first_masked); j < s.last; ++j) {
+    const uint32_t* words = odd + (j - first_masked) * (TILE / 32);
+    if ((words[0] | words[1] | words[2] | words[3]) == 0) continue;
     const Seen v = seen_of(P, s, node, j * TILE, [&](int n) { return parent[n] < n ? parent[n] : -1; });
     for (int w = 0; w < TILE / 32; ++w) {
-      for (uint32_t left = odd[(j - first_masked) * (TILE / 32) + w] & v.get(w); left; left &= left - 1) {
+      for (uint32_t left = words[w] & v.get(w); left; left &= left - 1) {
         const int64_t off = kv_slot_offset(P.L.kv, s.b, j * TILE + w * 32 + __ffs(left) - 1, P.page_shift);
         if (off < 0) continue;
-        const T* value = static_cast<const T*>(P.L.kv.v) + P.L.layer * P.L.kv.layer_stride + off +
-                         s.head * P.L.kv.head_stride;
 #pragma unroll 1
         for (int d = 0; d < D; ++d) {
-          const float x = static_cast<float>(value[d]);
+          const float x = static_cast<float>(values[off + d]);
           if (isfinite(x)) continue;
           if (out)
             out[d] = T(static_cast<float>(out[d]) + x);
           else
-            partial[static_cast<int64_t>(d / 4) * P.ws_rows * 4 + d % 4] += x;
+            *element(d) += x;
         }
       }
     }
   }
+}
+
+// The same for four elements of a row of an item in parts: those of CTA slots 0
+// and 1 are `stride` apart, `first` is the first CTA's slot 0.
+template <typename T>
+__device__ __noinline__ void settle_joined(const float4* first, int64_t stride, int parts, T* out) {
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+  for (int p = 0; p < parts; ++p) {
+    const float4 y = __ldcg(first + (p == 0 ? 1 : 2 * p) * stride);
+    if (!isfinite(y.x)) sum[0] += y.x;
+    if (!isfinite(y.y)) sum[1] += y.y;
+    if (!isfinite(y.z)) sum[2] += y.z;
+    if (!isfinite(y.w)) sum[3] += y.w;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (sum[e] != 0.0f) out[e] = T(sum[e]);
 }
 
 // Rows local0 .. local0 + rows - 1 of an item from its parts, which the CTAs
@@ -690,13 +796,26 @@ __device__ __forceinline__ void join_rows(const Plan& P, const Workspace& ws, co
           acc[e].z = fmaf(y[p][e].z, f, acc[e].z), acc[e].w = fmaf(y[p][e].w, f, acc[e].w);
       }
     }
-    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;  // no sum: zeros, as acc is
+    const bool some = sum != 0.0f;  // else zeros, also where acc is not finite
+    const float inv = some ? 1.0f / sum : 0.0f;
+    uint32_t y[4 * BATCH];
 #pragma unroll
     for (int e = 0; e < BATCH; ++e) {
       const int q = q0 + e * step;
+      y[4 * e] = __float_as_uint(acc[e].x), y[4 * e + 1] = __float_as_uint(acc[e].y);
+      y[4 * e + 2] = __float_as_uint(acc[e].z), y[4 * e + 3] = __float_as_uint(acc[e].w);
       if (q < D / 4)
-        *reinterpret_cast<uint2*>(out + q * 4) = make_uint2(Pair<T>::pack(acc[e].x * inv, acc[e].y * inv),
-                                                            Pair<T>::pack(acc[e].z * inv, acc[e].w * inv));
+        *reinterpret_cast<uint2*>(out + q * 4) = some ? make_uint2(Pair<T>::pack(acc[e].x * inv, acc[e].y * inv),
+                                                                   Pair<T>::pack(acc[e].z * inv, acc[e].w * inv))
+                                                      : make_uint2(0, 0);
+    }
+    Finite finite;
+    finite.take(y);
+    if (__builtin_expect(!finite.all(), 0) && some && !isnan(sum)) {
+#pragma unroll 1
+      for (int q = q0; q < min(q0 + BATCH * step, D / 4); q += step)
+        settle_joined<T>(ws.out + (static_cast<int64_t>(from) * 2 * (D / 4) + q) * P.ws_rows + local,
+                         static_cast<int64_t>(D / 4) * P.ws_rows, rec.parts, out + q * 4);
     }
   }
 }
@@ -877,7 +996,6 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
       rest_there = __shfl_sync(FULL, n, 0) + 1 == static_cast<uint32_t>(parts);
       __syncwarp();  // a shuffle orders no memory: the lanes' loads of the parts behind lane 0's acquire
       if (rest_there) {
-        if (lane == 0) *arrived = 0;
         float2 ms[JOIN_PARTS - 1];
 #pragma unroll
         for (int p = 1; p < JOIN_PARTS; ++p)
@@ -891,73 +1009,83 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
         for (int p = 1; p < JOIN_PARTS; ++p) total = fmaf(ms[p - 1].y, ex2(ms[p - 1].x - sub), total);
       }
     }
-    const bool finish = whole || rest_there;
+    bool finish = whole || rest_there;
     const float top0 = top == -INFINITY ? 0.0f : top, own = rest_there ? ex2(ref - top0) : 1.0f;
     const bool some = live && total != 0.0f;
     const float inv = some ? 1.0f / total : 0.0f;
     T* out = static_cast<T*>(P.L.out.data) + s.b * P.L.out.tree_stride + i * P.L.out.node_stride +
              (static_cast<int64_t>(s.head) * P.group + g) * P.L.out.head_stride;
     float4* partial = ws.out + part * (D / 4) * P.ws_rows + local;
+    bool counts, again;  // the row's values count; some row's output is not finite though they do
 #pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-      uint32_t o[32];
-      __syncwarp();
-      tmem_ld32(tm_o + c * 32, o);
-      if (both) {
-        uint32_t o1[32];
-        tmem_ld32(tm_o + D + c * 32, o1);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
-      } else {
-        tmem_wait_ld();
-      }
-      if (rest_there && live) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * own);
+    for (;;) {
+      Finite finite;
 #pragma unroll 1
-        for (int p = 1; p < parts; ++p) {
-          const int64_t at = static_cast<int64_t>(from + p) * 2;
-          const float4* theirs = ws.out + (at * (D / 4) + c * 8) * P.ws_rows + local;
-          const float f = ex2(__ldcg(&ws.sums[at * P.ws_rows + local].x) - top0);
-          float4 y[8];
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        __syncwarp();
+        tmem_ld32(tm_o + c * 32, o);
+        if (both) {
+          uint32_t o1[32];
+          tmem_ld32(tm_o + D + c * 32, o1);
+          tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 8; ++q) y[q] = __ldcg(theirs + q * P.ws_rows);
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
+        } else {
+          tmem_wait_ld();
+        }
+        if (rest_there && live) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            o[q * 4] = __float_as_uint(fmaf(y[q].x, f, __uint_as_float(o[q * 4])));
-            o[q * 4 + 1] = __float_as_uint(fmaf(y[q].y, f, __uint_as_float(o[q * 4 + 1])));
-            o[q * 4 + 2] = __float_as_uint(fmaf(y[q].z, f, __uint_as_float(o[q * 4 + 2])));
-            o[q * 4 + 3] = __float_as_uint(fmaf(y[q].w, f, __uint_as_float(o[q * 4 + 3])));
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * own);
+#pragma unroll 1
+          for (int p = 1; p < parts; ++p) {
+            const int64_t at = static_cast<int64_t>(from + p) * 2;
+            const float4* theirs = ws.out + (at * (D / 4) + c * 8) * P.ws_rows + local;
+            const float f = ex2(__ldcg(&ws.sums[at * P.ws_rows + local].x) - top0);
+            float4 y[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y[q] = __ldcg(theirs + q * P.ws_rows);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              o[q * 4] = __float_as_uint(fmaf(y[q].x, f, __uint_as_float(o[q * 4])));
+              o[q * 4 + 1] = __float_as_uint(fmaf(y[q].y, f, __uint_as_float(o[q * 4 + 1])));
+              o[q * 4 + 2] = __float_as_uint(fmaf(y[q].z, f, __uint_as_float(o[q * 4 + 2])));
+              o[q * 4 + 3] = __float_as_uint(fmaf(y[q].w, f, __uint_as_float(o[q * 4 + 3])));
+            }
+          }
+        }
+        finite.take(o);
+        if (!finish) {
+          if (live) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              partial[(c * 8 + q) * P.ws_rows] = make_float4(__uint_as_float(o[q * 4]), __uint_as_float(o[q * 4 + 1]),
+                                                             __uint_as_float(o[q * 4 + 2]), __uint_as_float(o[q * 4 + 3]));
+          }
+        } else if (in_call) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = some ? __uint_as_float(o[q * 8 + e]) * inv : 0.0f;
+            *reinterpret_cast<uint4*>(out + c * 32 + q * 8) = pack8<T>(y);
           }
         }
       }
-      if (!finish) {
-        if (live) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            partial[(c * 8 + q) * P.ws_rows] = make_float4(__uint_as_float(o[q * 4]), __uint_as_float(o[q * 4 + 1]),
-                                                           __uint_as_float(o[q * 4 + 2]), __uint_as_float(o[q * 4 + 3]));
-        }
-      } else if (in_call) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float y[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = some ? __uint_as_float(o[q * 8 + e]) * inv : 0.0f;
-          *reinterpret_cast<uint4*>(out + c * 32 + q * 8) = pack8<T>(y);
-        }
-      }
+      // no weights, or NaN among them: the row is all zeros or all NaN, whatever the values
+      counts = live && (finish ? total != 0.0f && !isnan(total) : !isnan(sum));
+      again = __any_sync(FULL, counts && !finite.all());
+      if (__builtin_expect(!again || !rest_there, 1)) break;
+      rest_there = finish = false;  // parts that are not finite are left to join_rows alone
     }
-    if (s.last > first_masked) {
-      const int masked0 = max(s.first, first_masked);
-      uint32_t odd = 0;
-      for (int x = (masked0 - first_masked) * (TILE / 32); x < (s.last - first_masked) * (TILE / 32); ++x)
-        odd |= C.odd[segment % 3][x];
+    if (rest_there && lane == 0) *arrived = 0;
+    uint32_t odd = 0;
+    for (int x = (max(s.first, first_masked) - first_masked) * (TILE / 32); x < (s.last - first_masked) * (TILE / 32); ++x)
+      odd |= C.odd[segment % 3][x];
+    if (__builtin_expect(again || odd, 0)) {
       const Segment copy = s;  // the callee takes its address, and s is to stay in registers
-      if (odd && live)
-        add_odd<T, D>(P, copy, C.odd[segment % 3], masked0, node, finish ? out : nullptr, reinterpret_cast<float*>(partial));
+      settle<T, D>(P, copy, C.odd[segment % 3], again, counts, node, finish ? out : nullptr, reinterpret_cast<float*>(partial));
     }
     if (!finish && live) ws.sums[part * P.ws_rows + local] = make_float2(ref, sum);
     tmem_fence_before();

@@ -534,8 +534,10 @@ int spec_tree_kv_append(int B, const spec_tree_kv_t* kv, int layer, const spec_t
  * summed, and the statistics of the softmax held, in float32; the weights are
  * rounded to kv->dtype for their product with the values.  What a node does
  * not see has no influence on it, whatever it holds (NaN and infinities
- * included).  A node that does not exist, or that sees no score above -inf,
- * gets zeros.
+ * included).  A value that it does see and that is not finite counts whatever
+ * its weight, however small: that element of the output is the sum of such
+ * values (an infinity; NaN for a NaN or for both infinities).  A node that does
+ * not exist, or that sees no score above -inf, gets zeros.
  *   q, out: n_q_heads vectors per node of kv->dtype, n_q_heads a multiple of
  *           n_kv_heads, 1 to 128 times it; out must not overlap q.
  *   scale:  finite, usually head_dim^-0.5.

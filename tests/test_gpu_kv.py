@@ -563,3 +563,126 @@ def test_items_split_between_ranges():
                                                   c3.parent.numpy(), c3.counts, 0, 64 ** -0.5)
     bound = kv_cases.attend_bound(c.dtype, want, mean_abs, score_abs, sum_abs, 64, 1533)
     assert (np.abs(outs[0].cpu()[sub].double().numpy() - want) <= bound).all()
+
+
+# ------------------------------------------------------- values that are not finite ---
+
+INF, NAN = float("inf"), float("nan")
+
+
+def _ramp(c, q, at_slot):
+    """The case with keys (and the queries) whose first element adds at_slot(b, slot) to every score."""
+    D, k = c.k.shape[4], c.k.clone()
+    size = c.k.shape[2]
+    for b, n in enumerate(c.seq_len.tolist()):
+        for s in range(n + min(c.counts[b], c.begin + c.N)):
+            k[0, int(c.table[b, s // size]), s % size, :, 0] = at_slot(b, s) * D ** 0.5 / 16
+    q = q.clone()
+    q[..., 0] = 16
+    return kv_cases.dataclasses.replace(c, k=k), q
+
+
+def _check_marks(c, q, marks, repeats=1):
+    """marks: (tree, slot, element, value): that element of that slot's value, all heads. Every node that sees it gets
+    the value there (NaN for both infinities), whatever its weight; all else is as without marks, to the bit, every time."""
+    size = c.v.shape[2]
+    v, felt = c.v.clone(), {}
+    for b, s, d, value in marks:
+        v[0, int(c.table[b, s // size]), s % size, :, d] = value
+    clean, status = _run_attend(c, q)
+    assert status == 0 and torch.isfinite(clean.float()).all()
+    want = clean.float()
+    for b, length in enumerate(c.seq_len.tolist()):
+        mine = [(s, d, value) for tree, s, d, value in marks if tree == b]
+        for i in range(c.N):
+            if c.begin + i >= c.counts[b]:
+                continue
+            seen = set(O.sees(None if c.parent is None else c.parent[b].numpy(), c.begin + i))
+            for s, d, value in mine:
+                if s < length or s - length in seen:
+                    old = want[b, i, :, d]
+                    want[b, i, :, d] = torch.where(torch.isfinite(old), value, old + value)
+    marked = kv_cases.dataclasses.replace(c, v=v)
+    cache, qd, nodes, status = _cache(marked), q.cuda(), _nodes(c), _status()
+    ws = B.AttendWorkspace(cache.B, c.N, q.shape[2], c.k.shape[3], c.k.shape[4])
+    outs = [torch.zeros_like(qd) for _ in range(3)]
+    for _ in range(repeats):
+        for out in outs:
+            B.spec_tree_attend(cache, 0, qd, out, ws, status, tree=nodes, node_begin=c.begin)
+        torch.cuda.synchronize()
+        for out in outs:
+            got = out.cpu().float()
+            off = ~((got == want) | (got.isnan() & want.isnan()))
+            assert not off.any(), (int(off.sum()), off.nonzero()[:4].tolist(), got[off][:4], want[off][:4])
+    assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N,tree", [(1, False), (20, True), (70, True), (150, False)])
+@pytest.mark.parametrize("light", [-28, -300])
+def test_infinite_values_of_light_tokens(dtype, D, N, tree, light):
+    """Seen tokens of next to no weight (2^-40, below f16's least; 2^-433, below float32's): their infinities count
+    wherever they lie, in tiles that every node sees whole and in others."""
+    c = kv_cases.make(70, [300], N, 2, D, 16, dtype, tree=tree, stale=NAN)
+    slots = [10, 130, 255, 256, 261, 299]
+    c, q = _ramp(c, _queries(71, c, 8, 0.5), lambda b, s: light if s in slots else 0.0)
+    _check_marks(c, q, [(0, s, 3 + 2 * i, INF if i % 2 else -INF) for i, s in enumerate(slots)])
+    _check_marks(c, q, [(0, 10, 3, INF), (0, 299, 3, -INF), (0, 130, 4, NAN), (0, 10, 5, INF), (0, 256, 5, INF)])
+
+
+@pytest.mark.parametrize("N,tree", [(20, True), (70, True), (150, False)])
+def test_infinite_values_of_light_nodes(N, tree):
+    c = kv_cases.make(72, [250, 70], N, 2, 64, 16, tree=tree, counts=[N, N - 3], stale=NAN)
+    hit = [3, 9, 12]
+    c, q = _ramp(c, _queries(73, c, 8, 0.5), lambda b, s: -300.0 if s - (250, 70)[b] in hit else 0.0)
+    _check_marks(c, q, [(b, (250, 70)[b] + n, 5 + n, INF) for b in range(2) for n in hit] + [(0, 40, 6, -INF)])
+
+
+@pytest.mark.parametrize("first,last", [(0.0, 300.0), (300.0, 0.0)])
+@pytest.mark.parametrize("N,tree", [(1, False), (20, True), (70, True)])
+def test_infinite_values_before_and_after_the_maximum_moves(first, last, N, tree):
+    """Two tiles far apart in score, one CTA: the output is rescaled by zero when the second one comes, or the second
+    one's weights are zero."""
+    c = kv_cases.make(74, [400], N, 1, 128, 16, tree=tree)
+    c, q = _ramp(c, _queries(75, c, 4, 0.5), lambda b, s: first if s < 200 else last)
+    _check_marks(c, q, [(0, 20, 3, INF), (0, 390, 5, INF), (0, 20, 7, -INF), (0, 390, 7, INF), (0, 150, 8, -INF)])
+
+
+def _split(name):
+    rng = np.random.RandomState(5)
+    if name == "one":        # pieces, joined by the last to come
+        return kv_cases.make(76, [5000], 1, 1, 64, 32, tree=False), 4
+    if name == "tree":       # pieces, joined by a kernel of its own
+        return kv_cases.make(77, [6000], 61, 1, 128, 64), 4
+    if name == "ones":       # ranges of single tokens
+        return kv_cases.make(78, rng.randint(200, 900, 170).tolist(), 1, 1, 64, 32, tree=False), 4
+    if name == "frontiers":  # ranges, the halves taking turns at the tiles
+        return kv_cases.make(79, rng.randint(200, 900, 60).tolist(), 33, 4, 64, 64), 8
+    return kv_cases.make(80, rng.randint(200, 900, 80).tolist(), 61, 2, 64, 64), 8  # ranges, 244 rows
+
+
+@pytest.mark.parametrize("up", [True, False])
+@pytest.mark.parametrize("name", ["one", "tree", "ones", "frontiers", "trees"])
+def test_infinite_values_in_split_items(name, up):
+    """Items in parts whose references lie hundreds of binary orders apart, either way round: whoever joins them, an
+    infinity in any part counts, launch after launch."""
+    c, Hq = _split(name)
+    lens = c.seq_len.tolist()
+    c, q = _ramp(c, _queries(81, c, Hq, 0.5), lambda b, s: 1500.0 * (s if up else lens[b] - s) / lens[b])
+    marks = []
+    for b, n in enumerate(lens):
+        if b % 3 == 0:
+            marks += [(b, 2, 3, INF), (b, n // 2, 5, -INF), (b, n - 1, 7, NAN), (b, 4, 9, INF), (b, n - 2, 9, -INF),
+                      (b, n, 11, INF), (b, n // 3, 13, -INF), (b, 2 * n // 3, 13, -INF)]
+        elif b % 3 == 1 and c.N > 12:
+            marks += [(b, n + 5, 3, INF), (b, n + 12, 4, -INF)]
+    _check_marks(c, q, marks, repeats=8)
+
+
+@pytest.mark.parametrize("lens,N", [([6], 4), ([300], 1), ([300], 40), ([5000], 1), ([5000], 61)])
+def test_infinite_values_where_no_score_is_above_minus_infinity(lens, N):
+    c = kv_cases.make(82, lens, N, 1, 64, 16, tree=False)
+    c = kv_cases.dataclasses.replace(c, k=torch.full_like(c.k, -INF), v=torch.full_like(c.v, INF))
+    got, status = _run_attend(c, torch.ones((1, N, 4, 64)).to(c.dtype))
+    assert status == 0 and (got == 0).all()
