@@ -374,6 +374,23 @@ def spec_tree_wait_selftest(polls: int, status: torch.Tensor, result: torch.Tens
 # --------------------------------------------------- the model's side of a step ---
 
 _HALF = {torch.bfloat16: BF16, torch.float16: F16}
+_I32, _U32 = torch.int32, torch.uint32
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # looked up once: calls are made once per layer
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _ready(device: int, status: torch.Tensor, stream) -> int:
+    """The stream's handle, if `status` and the cache (of that device) are where a kernel can reach them."""
+    kind = status.dtype
+    if (kind is not _I32 and kind is not _U32) or status.numel() < 1 or status.get_device() != device:
+        raise SpecTreeError("status must be an int32 tensor on the cache's device")
+    if device < 0 or _current_device() != device:
+        raise SpecTreeError("the cache must be on the current GPU")
+    if stream is None:
+        return _raw_stream(device)
+    if stream.device.index != device:
+        raise SpecTreeError("the stream must be of the cache's device")
+    return stream.cuda_stream
 
 
 class KVCache:
@@ -381,7 +398,9 @@ class KVCache:
 
     k, v: [layers][pages][page_size][kv heads][head_dim], bf16 or f16, any strides with contiguous
     head_dim (a [layers][pages][heads][page_size][head_dim] pool is passed transposed);
-    page_table: int32 [B][max_pages], a row for each sequence (contiguous, none over another); seq_len: int32 [B], committed tokens.
+    page_table: int32 [B][max_pages], a row for each sequence (contiguous, none over another);
+    seq_len: int32 [B], committed tokens.  All are on one device, as is whatever a call takes with them; a call
+    wants it to be the current GPU.
     """
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor):
@@ -397,17 +416,20 @@ class KVCache:
         table_stride = page_table.stride(0) if rows > 1 else width  # the stride of a single row means nothing
         if not width <= table_stride < 1 << 31:
             raise SpecTreeError("rows of page_table overlap (an expanded table is to be copied) or lie too far apart")
-        self.k, self.v, self.page_table, self.B = k, v, page_table, page_table.shape[0]
+        device = k.get_device()
+        if v.get_device() != device or page_table.get_device() != device:
+            raise SpecTreeError("k, v and page_table must be on one device")
+        self.k, self.v, self.page_table, self.B, self.device = k, v, page_table, rows, device
         layers, pages, size, heads, dim = k.shape
         c = c_kv(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), None, k.stride(0), k.stride(1), k.stride(2),
                  k.stride(3), _HALF[k.dtype], layers, pages, size, heads, dim, width, table_stride)
         self._c, self.at = c, ctypes.addressof(c)
-        self.shape = (self.B, heads, dim, k.dtype)
+        self.shape = (self.B, heads, dim, k.dtype, device)
         self.set_lengths(seq_len)
 
     def set_lengths(self, seq_len: torch.Tensor):
         """Committed tokens from now on, e.g. the new_len of spec_tree_kv_commit."""
-        self._c.seq_len = _int_rows("seq_len", seq_len, (self.B,))
+        self._c.seq_len = _int_rows("seq_len", seq_len, (self.B,), self.device)
         self.seq_len = seq_len
 
     def c(self) -> c_kv:
@@ -423,10 +445,10 @@ class NodeArrays:
     n_nodes: Optional[torch.Tensor] = None
 
 
-def _int_rows(name: str, t: torch.Tensor, shape) -> int:
-    """Address of a contiguous int32 tensor of that shape."""
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise SpecTreeError(f"{name} must be contiguous int32 {list(shape)}")
+def _int_rows(name: str, t: torch.Tensor, shape, device: int) -> int:
+    """Address of a contiguous int32 tensor of that shape and device."""
+    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise SpecTreeError(f"{name} must be contiguous int32 {list(shape)} on the cache's device")
     return t.data_ptr()
 
 
@@ -440,7 +462,7 @@ class _Packed(threading.local):
         self.nodes_at = ctypes.addressof(self.buf)
         self.heads_at = tuple(self.nodes_at + 64 + i * (self.HEADS4.size // 4) for i in range(4))
 
-    def nodes(self, tree, B: int, begin: int, count: int) -> int:
+    def nodes(self, tree, B: int, begin: int, count: int, device: int) -> int:
         """A TreeBuffers, a NodeArrays or None (a chain of which every node exists)."""
         if tree is None:
             self.NODES.pack_into(self.buf, 0, 0, 0, 0, 0, begin, count)
@@ -449,30 +471,32 @@ class _Packed(threading.local):
         at, stride = 0, 0
         if parent is not None:
             stride = parent.shape[-1]
-            at = _int_rows("node_parent", parent, (B, stride))
+            at = _int_rows("node_parent", parent, (B, stride), device)
         elif depth is not None:
             raise SpecTreeError("node_depth without node_parent")
-        self.NODES.pack_into(self.buf, 0, at, 0 if depth is None else _int_rows("node_depth", depth, (B, stride)),
-                             0 if n is None else _int_rows("n_nodes", n, (B,)), stride, begin, count)
+        self.NODES.pack_into(self.buf, 0, at,
+                             0 if depth is None else _int_rows("node_depth", depth, (B, stride), device),
+                             0 if n is None else _int_rows("n_nodes", n, (B,), device), stride, begin, count)
         return self.nodes_at
 
-    def heads2(self, a: torch.Tensor, b: torch.Tensor):
-        """Two tensors of vectors; their addresses in the buffer."""
-        (a0, a1, a2, _), (b0, b1, b2, _) = a.stride(), b.stride()
-        self.HEADS2.pack_into(self.buf, 64, a.data_ptr(), a0, a1, a2, b.data_ptr(), b0, b1, b2)
+    def heads2(self, a, b):
+        """Two tensors' _vectors; their addresses in the buffer."""
+        self.HEADS2.pack_into(self.buf, 64, *a, *b)
         return self.heads_at
 
-    def heads4(self, a: torch.Tensor, b: torch.Tensor, c: torch.Tensor, d: torch.Tensor):
-        (a0, a1, a2, _), (b0, b1, b2, _), (c0, c1, c2, _), (d0, d1, d2, _) = a.stride(), b.stride(), c.stride(), d.stride()
-        self.HEADS4.pack_into(self.buf, 64, a.data_ptr(), a0, a1, a2, b.data_ptr(), b0, b1, b2, c.data_ptr(), c0, c1, c2,
-                              d.data_ptr(), d0, d1, d2)
+    def heads4(self, a, b, c, d):
+        self.HEADS4.pack_into(self.buf, 64, *a, *b, *c, *d)
         return self.heads_at
 
 
-def _vectors(name: str, x: torch.Tensor, dtype, shape):
-    """Refuse what is not [B][nodes][heads][head_dim] of that shape and dtype with contiguous head_dim."""
-    if x.dtype is not dtype or x.shape != shape or x.stride(3) != 1:
-        raise SpecTreeError(f"{name} must be {list(shape)} of {dtype}, head_dim contiguous")
+def _vectors(name: str, x: torch.Tensor, dtype, shape, device: int):
+    """Address and strides of x; refuses what is not [B][nodes][heads][head_dim] of that shape, dtype and device
+    with contiguous head_dim."""
+    if x.dtype is dtype and x.shape == shape and x.get_device() == device:
+        tree, node, head, element = x.stride()
+        if element == 1:
+            return x.data_ptr(), tree, node, head
+    raise SpecTreeError(f"{name} must be {list(shape)} of {dtype}, head_dim contiguous, on the cache's device")
 
 
 _packed = _Packed()
@@ -500,26 +524,25 @@ def spec_tree_kv_append(cache: KVCache, layer: int, q: torch.Tensor, k: torch.Te
                         stream=None):
     """Nodes node_begin .. node_begin + q.shape[1] - 1 of every tree: head norms (with weights), rotation
     (with a rope table [rows][rot_dim]), keys and values into the cache, queries to q_out."""
-    (n, hq), (B, hkv, dim, dtype), pack = _count(q), cache.shape, _packed
+    (n, hq), (B, hkv, dim, dtype, device), pack = _count(q), cache.shape, _packed
     rows = rot = rope_at = 0
     if rope is not None:
-        if rope.dim() != 2 or rope.dtype is not torch.float32 or not rope.is_contiguous():
-            raise SpecTreeError("rope must be contiguous float32 [rows][rot_dim]")
+        if rope.dim() != 2 or rope.dtype is not torch.float32 or not rope.is_contiguous() or rope.get_device() != device:
+            raise SpecTreeError("rope must be contiguous float32 [rows][rot_dim] on the cache's device")
         rows, rot = rope.shape
         rope_at = rope.data_ptr()
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and (w.dtype is not dtype or w.shape != (dim,) or not w.is_contiguous()):
-            raise SpecTreeError(f"{name} must be [head_dim] of the cache's dtype")
+        if w is not None and (w.dtype is not dtype or w.shape != (dim,) or not w.is_contiguous()
+                              or w.get_device() != device):
+            raise SpecTreeError(f"{name} must be [head_dim] of the cache's dtype on its device")
     qs, ks = (B, n, hq, dim), (B, n, hkv, dim)
-    _vectors("q", q, dtype, qs)
-    _vectors("k", k, dtype, ks)
-    _vectors("v", v, dtype, ks)
-    _vectors("q_out", q_out, dtype, qs)
-    q_at, k_at, v_at, out_at = pack.heads4(q, k, v, q_out)
-    _check(_lib.spec_tree_kv_append(B, cache.at, layer, pack.nodes(tree, B, node_begin, n), hq, q_at, k_at, v_at, out_at,
-                                    rope_at, rows, rot, interleaved, None if q_weight is None else q_weight.data_ptr(),
-                                    None if k_weight is None else k_weight.data_ptr(), eps, status.data_ptr(),
-                                    _stream(stream)))
+    q_at, k_at, v_at, out_at = pack.heads4(_vectors("q", q, dtype, qs, device), _vectors("k", k, dtype, ks, device),
+                                           _vectors("v", v, dtype, ks, device), _vectors("q_out", q_out, dtype, qs, device))
+    nodes_at = pack.nodes(tree, B, node_begin, n, device)
+    stream = _ready(device, status, stream)
+    _check(_lib.spec_tree_kv_append(B, cache.at, layer, nodes_at, hq, q_at, k_at, v_at, out_at, rope_at, rows, rot,
+                                    interleaved, None if q_weight is None else q_weight.data_ptr(),
+                                    None if k_weight is None else k_weight.data_ptr(), eps, status.data_ptr(), stream))
 
 
 class AttendWorkspace:
@@ -531,7 +554,7 @@ class AttendWorkspace:
         if n == 0:
             raise SpecTreeError("spec_tree_attend takes no such heads or nodes")
         self.data = torch.zeros(n, dtype=torch.uint8, device=device)
-        self.at, self.bytes = self.data.data_ptr(), n
+        self.at, self.bytes, self.device = self.data.data_ptr(), n, self.data.get_device()
 
 
 def spec_tree_attend(cache: KVCache, layer: int, q: torch.Tensor, out: torch.Tensor, workspace: AttendWorkspace,
@@ -539,24 +562,27 @@ def spec_tree_attend(cache: KVCache, layer: int, q: torch.Tensor, out: torch.Ten
                      stream=None):
     """Nodes node_begin .. node_begin + q.shape[1] - 1 of every tree attend to the committed tokens, their
     ancestors and themselves; scale defaults to head_dim ** -0.5."""
-    (n, hq), (B, _, dim, dtype), pack = _count(q), cache.shape, _packed
+    (n, hq), (B, _, dim, dtype, device), pack = _count(q), cache.shape, _packed
     qs = (B, n, hq, dim)
-    _vectors("q", q, dtype, qs)
-    _vectors("out", out, dtype, qs)
-    q_at, out_at, _, _ = pack.heads2(q, out)
-    _check(_lib.spec_tree_attend(B, cache.at, layer, pack.nodes(tree, B, node_begin, n), hq, q_at, out_at,
-                                 dim ** -0.5 if scale is None else scale, workspace.at, workspace.bytes,
-                                 status.data_ptr(), _stream(stream)))
+    q_at, out_at, _, _ = pack.heads2(_vectors("q", q, dtype, qs, device), _vectors("out", out, dtype, qs, device))
+    nodes_at = pack.nodes(tree, B, node_begin, n, device)
+    stream = _ready(device, status, stream)
+    if workspace.device != device:
+        raise SpecTreeError("the workspace must be on the cache's device")
+    _check(_lib.spec_tree_attend(B, cache.at, layer, nodes_at, hq, q_at, out_at, dim ** -0.5 if scale is None else scale,
+                                 workspace.at, workspace.bytes, status.data_ptr(), stream))
 
 
 def spec_tree_kv_commit(cache: KVCache, accept_len: torch.Tensor, out_node: torch.Tensor, new_len: torch.Tensor,
                         status: torch.Tensor, stream=None):
     """Move the accepted path (spec_tree_verify's accept_len and out_node) behind the committed tokens in
     every layer; new_len [B] receives the new committed lengths (then cache.set_lengths(new_len))."""
-    B = (cache.B,)
+    B, device = (cache.B,), cache.device
     if out_node.dim() != 2:
         raise SpecTreeError("out_node must be [B][depth + 1]")
     stride = out_node.shape[1]
-    _check(_lib.spec_tree_kv_commit(cache.B, cache.at, _int_rows("accept_len", accept_len, B),
-                                    _int_rows("out_node", out_node, (cache.B, stride)), stride,
-                                    _int_rows("new_len", new_len, B), status.data_ptr(), _stream(stream)))
+    accept_at = _int_rows("accept_len", accept_len, B, device)
+    node_at = _int_rows("out_node", out_node, (cache.B, stride), device)
+    new_at = _int_rows("new_len", new_len, B, device)
+    stream = _ready(device, status, stream)
+    _check(_lib.spec_tree_kv_commit(cache.B, cache.at, accept_at, node_at, stride, new_at, status.data_ptr(), stream))

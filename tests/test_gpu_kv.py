@@ -686,3 +686,37 @@ def test_infinite_values_where_no_score_is_above_minus_infinity(lens, N):
     c = kv_cases.dataclasses.replace(c, k=torch.full_like(c.k, -INF), v=torch.full_like(c.v, INF))
     got, status = _run_attend(c, torch.ones((1, N, 4, 64)).to(c.dtype))
     assert status == 0 and (got == 0).all()
+
+
+def test_arguments_on_the_cpu_are_refused():
+    """Nothing is launched; the same call with all of them on the GPU is."""
+    c = kv_cases.make(83, [30, 12], 6, 2, 64, 16)
+    cache, nodes, status, ws = _cache(c), _nodes(c), _status(), B.AttendWorkspace(2, 6, 4, 2, 64)
+    q = _queries(84, c, 4)
+    k = _queries(85, c, 2)
+    rope, path = B.rope_table(64, 64), torch.zeros((2, 9), dtype=torch.int32)
+    acc, new = torch.zeros((2, 2), dtype=torch.int32)
+    here = dict(q=q.cuda(), k=k.cuda(), v=k.cuda(), q_out=torch.zeros_like(q, device="cuda"), rope=rope, status=status)
+    B.spec_tree_kv_append(cache, 0, tree=nodes, **here)
+    B.spec_tree_attend(cache, 0, here["q"], here["q_out"], ws, status, tree=nodes)
+    B.spec_tree_kv_commit(cache, acc.cuda(), path.cuda(), new.cuda(), status)
+    torch.cuda.synchronize()
+    before = cache.k.clone(), cache.v.clone()
+    for name in here:
+        with pytest.raises(B.SpecTreeError):
+            B.spec_tree_kv_append(cache, 0, tree=nodes, **dict(here, **{name: here[name].cpu()}))
+    for qq, out, st in ((q, here["q_out"], status), (here["q"], q, status), (here["q"], here["q_out"], status.cpu())):
+        with pytest.raises(B.SpecTreeError):
+            B.spec_tree_attend(cache, 0, qq, out, ws, st, tree=nodes)
+    cpu = B.NodeArrays(c.parent, c.depth, c.n_nodes)
+    with pytest.raises(B.SpecTreeError):
+        B.spec_tree_attend(cache, 0, here["q"], here["q_out"], ws, status, tree=cpu)
+    with pytest.raises(B.SpecTreeError):
+        B.KVCache(cache.k, cache.v, c.table, cache.seq_len)
+    with pytest.raises(B.SpecTreeError):
+        cache.set_lengths(c.seq_len)
+    for bad in ((acc, path.cuda(), new.cuda()), (acc.cuda(), path, new.cuda()), (acc.cuda(), path.cuda(), new)):
+        with pytest.raises(B.SpecTreeError):
+            B.spec_tree_kv_commit(cache, *bad, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and torch.equal(cache.k, before[0]) and torch.equal(cache.v, before[1])

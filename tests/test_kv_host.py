@@ -158,6 +158,103 @@ def test_page_tables_whose_rows_overlap_are_refused(B):
         assert B.KVCache(k, k.clone(), one, lens[:1]).c().table_stride == 3  # the stride of a single row means nothing
 
 
+class _OnCard(torch.Tensor):
+    """A CPU tensor that says it lies on GPU 0."""
+
+    def get_device(self):
+        return 0
+
+
+class _Recorder:
+    """Takes the library's place: counts the calls that get through."""
+
+    def __init__(self):
+        self.calls = 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls += 1
+            return 0
+        return call
+
+
+@pytest.fixture
+def card(B, monkeypatch):
+    """(binding, recorder, calls): the entry points' arguments by name, all on GPU 0, and a function for each."""
+    rec = _Recorder()
+    monkeypatch.setattr(B, "_lib", rec)
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    monkeypatch.setattr(B, "_raw_stream", lambda device: 0)
+    on = lambda *shape, dtype=torch.int32: torch.zeros(shape, dtype=dtype).as_subclass(_OnCard)  # noqa: E731
+    bf = torch.bfloat16
+    pool = dict(kp=on(1, 4, 16, 2, 64, dtype=bf), vp=on(1, 4, 16, 2, 64, dtype=bf), table=on(2, 3), lens=on(2))
+    ws = B.AttendWorkspace.__new__(B.AttendWorkspace)
+    ws.at, ws.bytes, ws.device = 4096, 1 << 30, 0
+    tree = dict(parent=on(2, 9), depth=on(2, 9), n=on(2))
+
+    def cache(a):
+        return B.KVCache(a["kp"], a["vp"], a["table"], a["lens"])
+
+    def nodes(a):
+        return B.NodeArrays(a["parent"], a["depth"], a["n"])
+
+    append = dict(pool, **tree, q=on(2, 3, 4, 64, dtype=bf), k=on(2, 3, 2, 64, dtype=bf), v=on(2, 3, 2, 64, dtype=bf),
+                  out=on(2, 3, 4, 64, dtype=bf), rope=on(9, 64, dtype=torch.float32), qw=on(64, dtype=bf),
+                  kw=on(64, dtype=bf), status=on(1))
+    attend = dict(pool, **tree, q=append["q"], out=append["out"], ws=ws, status=on(1))
+    commit = dict(pool, acc=on(2), node=on(2, 9), new=on(2), status=on(1))
+    return rec, [
+        (append, lambda a: B.spec_tree_kv_append(cache(a), 0, a["q"], a["k"], a["v"], a["out"], a["rope"], a["status"],
+                                                 tree=nodes(a), q_weight=a["qw"], k_weight=a["kw"])),
+        (attend, lambda a: B.spec_tree_attend(cache(a), 0, a["q"], a["out"], a["ws"], a["status"], tree=nodes(a))),
+        (commit, lambda a: B.spec_tree_kv_commit(cache(a), a["acc"], a["node"], a["new"], a["status"]))]
+
+
+def test_tensors_on_another_device_are_refused(B, card):
+    """Each tensor in turn on the CPU, or the workspace on another GPU: refused before the library is called."""
+    rec, calls = card
+    for args, call in calls:
+        before = rec.calls
+        call(args)
+        assert rec.calls == before + 1
+        for name, x in args.items():
+            if name == "ws":
+                there = B.AttendWorkspace.__new__(B.AttendWorkspace)
+                there.at, there.bytes, there.device = x.at, x.bytes, 1
+            else:
+                there = x.as_subclass(torch.Tensor)
+            with pytest.raises(B.SpecTreeError):
+                call(dict(args, **{name: there}))
+            assert rec.calls == before + 1, name
+
+
+def test_caches_off_the_current_gpu_are_refused(B, card, monkeypatch):
+    rec, calls = card
+    for args, call in calls:
+        plain = {k: x if k == "ws" else x.as_subclass(torch.Tensor) for k, x in args.items()}
+        with pytest.raises(B.SpecTreeError, match="current GPU"):
+            call(plain)                                   # all on the CPU
+    monkeypatch.setattr(B, "_current_device", lambda: 1)
+    for args, call in calls:
+        with pytest.raises(B.SpecTreeError, match="current GPU"):
+            call(args)
+    assert rec.calls == 0
+
+
+def test_status_words_of_another_kind_are_refused(B, card):
+    """The kernels add bits to a 32-bit word."""
+    rec, calls = card
+    for args, call in calls:
+        for bad in (torch.zeros(1, dtype=torch.uint8), torch.zeros(1, dtype=torch.int64), torch.zeros(1),
+                    torch.zeros(0, dtype=torch.int32)):
+            with pytest.raises(B.SpecTreeError, match="status"):
+                call(dict(args, status=bad.as_subclass(_OnCard)))
+        assert rec.calls == 0
+    for args, call in calls:
+        call(dict(args, status=torch.zeros(3, dtype=torch.uint32).as_subclass(_OnCard)))
+    assert rec.calls == 3
+
+
 def test_structs_match_the_c_header(B, tmp_path):
     import shutil
     import subprocess
