@@ -18,9 +18,9 @@
 //     ranges.  A long cache is split over the card and a ragged batch is
 //     balanced; a CTA begins and ends inside items;
 //   - pieces, where the items are fewer than the CTAs: each item cut into
-//     equal pieces, one per CTA, their length the least for which there are
-//     CTAs enough.  Taken where the length and one segment's fixed cost are
-//     below a range's length and two.
+//     equal pieces, one per CTA, their length the least of 32 tried for which
+//     there are CTAs enough (find_piece).  Taken where the length and one
+//     segment's fixed cost are below a range's length and two.
 // An item that one CTA has whole is finished there; otherwise each CTA leaves
 // its sums, their reference and its unnormalised output in the workspace, and
 // the parts are put together in the item's order:
@@ -30,7 +30,8 @@
 //     not, and for calls of up to 16 rows, whoever is the last to leave a part
 //     does it;
 //   - pieces, of more rows: they end together, and one CTA would be long about
-//     it: attend_join_kernel, over all SMs.
+//     it: attend_join_kernel, over all SMs.  It is launched behind every call that
+//     may be dealt in pieces, as the lengths are known on the device alone.
 //
 // Tile.  S = Q K^T in tensor memory (128 lanes: one row per softmax thread);
 // weights w = 2^(scale S - ref), rounded to the cache's type and stored over
@@ -81,7 +82,13 @@ constexpr int HELPERS = 2 * TILE / 32;          // the helpers' first warp
 constexpr int COLUMNS = 512;                    // tensor memory: S of both halves, then O of both
 constexpr int MAX_PIECE_ITEMS = 256;            // (tree, rows) of calls that may be dealt in pieces
 constexpr int JOIN_PARTS = 4;                   // parts of an item joined at a time
-constexpr int JOIN_INSIDE_ROWS = 16;            // rows of calls that need no join kernel
+// Rows of calls that need no join kernel.  By the last CTA to come, and by the
+// kernel: 4 rows, one sequence of 500 tokens 9.9 and 11.4 us, of 16384 19.8 and
+// 21.5, 4 of 4000 16.5 and 18.0; 32 rows over 8192 25.0 and 20.0; 244 rows over
+// 8192 46.0 and 34.4.  Many parts are the exception: one warp walks them, four at
+// a time, and 8 rows over 16384 tokens of one key head (129 parts) take 54.4 and
+// 46.0.
+constexpr int JOIN_INSIDE_ROWS = 16;
 // Weights are handed to the product in two parts, so that it works on the first
 // while the second is made.
 constexpr int EARLY = 64;
@@ -1165,7 +1172,12 @@ __device__ __forceinline__ void find_range(const Plan& P, Control& C, int warp, 
 }
 
 // In tiles of 128 rows (a tile of 256 counts for two): what leaving and joining
-// parts costs, and the second segment that a range has.
+// parts costs, and the second segment that a range has.  Estimates: a tile of 256
+// rows takes 1.45 us, joining 7 us and a segment's end 5 us of 8 trees' calls.  The
+// first weighs against items left whole, the second against ranges.  Pieces and
+// ranges, each forced: one token of 4 sequences of 4000 tokens 16.5 and 21.8 us, of
+// 16 of 2300 28.2 and 32.6, one tree of 61 nodes over 8192 tokens 34.3 and 55.5,
+// 8 over 2300 35.0 and 38.4, 16 over 2300 44.7 and 51.5.
 constexpr float JOIN_COST = 6.0f, ENDS_COST = 10.0f;
 
 // Pieces of an item of `tiles` tiles when a piece is to have about 1 / inv.
@@ -1174,9 +1186,13 @@ __device__ __forceinline__ int pieces_of(int tiles, float inv) {
 }
 
 // For no more items than CTAs: the length of equal pieces that costs least, of
-// those for which there are CTAs enough (one lane tries one of 32 lengths), and
-// this CTA's piece.  False: ranges, which always have parts to join and begin
-// and end inside items, cost less.
+// those for which there are CTAs enough, and this CTA's piece.  False: ranges,
+// which always have parts to join and begin and end inside items, cost less.
+// One lane tries one of 32 lengths, evenly spaced between a range's and the longest
+// item's.  Few items of very many tiles lie between two of them, leave CTAs idle
+// or go to ranges with more parts than these can join early: 131072 tokens of one
+// key head take 66 us, and 44 if pieces are forced; one tree over 65000 tokens of
+// one key head 275 and 64, of eight 96.6 and 89.1.
 template <int HALVES>
 __device__ __forceinline__ bool find_piece(const Plan& P, Control& C, int warp, int cta) {
   const int items = P.L.B * P.row_tiles, heads = P.L.kv.n_kv_heads, lane = threadIdx.x % 32;
