@@ -37,7 +37,9 @@ EXPORTS = ("spec_tree_rows_needed", "spec_tree_check_params", "spec_tree_select_
            "spec_tree_build", "spec_tree_verify", "spec_tree_layer_state_bytes", "spec_tree_layer_rows",
            "spec_tree_layer", "spec_tree_finish", "spec_tree_layer_static", "spec_tree_smart_fit",
            "spec_tree_wait_selftest", "spec_tree_verify_dense", "spec_tree_kv_append", "spec_tree_attend",
-           "spec_tree_attend_workspace_bytes", "spec_tree_kv_commit", "spec_tree_strerror")
+           "spec_tree_attend_workspace_bytes", "spec_tree_kv_commit", "spec_tree_kv4_append", "spec_tree_kv4_attend",
+           "spec_tree_kv4_commit", "spec_tree_kv4_read", "spec_tree_kv_reserve", "spec_tree_kv_release",
+           "spec_tree_strerror")
 
 
 class SpecTreeError(RuntimeError):
@@ -65,6 +67,16 @@ class c_kv(ctypes.Structure):
         (n, ctypes.c_int64) for n in ("layer_stride", "page_stride", "token_stride", "head_stride")] + [
         (n, ctypes.c_int32) for n in ("dtype", "n_layers", "n_pages", "page_size", "n_kv_heads", "head_dim",
                                       "max_pages", "table_stride")]
+
+
+class c_kv4(ctypes.Structure):
+    _fields_ = [("kv", c_kv), ("scale", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("scale_layer_stride", "scale_page_stride", "scale_head_stride")]
+
+
+class c_pages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("page_table", "held", "free_pages", "n_free", "scratch")] + [
+        (n, ctypes.c_int32) for n in ("n_pages", "page_size", "max_pages", "table_stride")]
 
 
 class c_heads(ctypes.Structure):
@@ -105,6 +117,12 @@ def _load():
     lib.spec_tree_attend_workspace_bytes.argtypes = [i32] * 5
     lib.spec_tree_attend_workspace_bytes.restype = ctypes.c_size_t
     lib.spec_tree_kv_commit.argtypes = [i32, vp, vp, vp, i32, vp, vp, vp]
+    lib.spec_tree_kv4_append.argtypes = lib.spec_tree_kv_append.argtypes
+    lib.spec_tree_kv4_attend.argtypes = lib.spec_tree_attend.argtypes
+    lib.spec_tree_kv4_commit.argtypes = lib.spec_tree_kv_commit.argtypes
+    lib.spec_tree_kv4_read.argtypes = [i32, vp, i32, vp, vp, i32, vp, vp, vp, vp]
+    lib.spec_tree_kv_reserve.argtypes = [i32, vp, vp, vp, i32, vp, vp, vp]
+    lib.spec_tree_kv_release.argtypes = [i32, vp, vp, vp, vp]
     lib.spec_tree_strerror.argtypes = [i32]
     lib.spec_tree_strerror.restype = ctypes.c_char_p
     for name in EXPORTS:
@@ -393,6 +411,17 @@ def _ready(device: int, status: torch.Tensor, stream) -> int:
     return stream.cuda_stream
 
 
+def _table_shape(page_table: torch.Tensor):
+    """Entries of a row, and from one row to the next."""
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1:
+        raise SpecTreeError("page_table must be int32 [B][max_pages] with contiguous rows")
+    rows, width = page_table.shape
+    table_stride = page_table.stride(0) if rows > 1 else width  # the stride of a single row means nothing
+    if not width <= table_stride < 1 << 31:
+        raise SpecTreeError("rows of page_table overlap (an expanded table is to be copied) or lie too far apart")
+    return width, table_stride
+
+
 class KVCache:
     """A paged key-value cache (the spec_tree_kv_t of the C ABI).
 
@@ -410,13 +439,8 @@ class KVCache:
             raise SpecTreeError(f"unsupported cache dtype {k.dtype}")
         if k.stride(4) != 1:
             raise SpecTreeError("head_dim must be contiguous")
-        if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1:
-            raise SpecTreeError("page_table must be int32 [B][max_pages] with contiguous rows")
-        rows, width = page_table.shape
-        table_stride = page_table.stride(0) if rows > 1 else width  # the stride of a single row means nothing
-        if not width <= table_stride < 1 << 31:
-            raise SpecTreeError("rows of page_table overlap (an expanded table is to be copied) or lie too far apart")
-        device = k.get_device()
+        width, table_stride = _table_shape(page_table)
+        rows, device = page_table.shape[0], k.get_device()
         if v.get_device() != device or page_table.get_device() != device:
             raise SpecTreeError("k, v and page_table must be on one device")
         self.k, self.v, self.page_table, self.B, self.device = k, v, page_table, rows, device
@@ -524,6 +548,12 @@ def spec_tree_kv_append(cache: KVCache, layer: int, q: torch.Tensor, k: torch.Te
                         stream=None):
     """Nodes node_begin .. node_begin + q.shape[1] - 1 of every tree: head norms (with weights), rotation
     (with a rope table [rows][rot_dim]), keys and values into the cache, queries to q_out."""
+    _kind(cache, KVCache)
+    _append(_lib.spec_tree_kv_append, cache, layer, q, k, v, q_out, rope, status, tree, node_begin, q_weight, k_weight, eps,
+            interleaved, stream)
+
+
+def _append(entry, cache, layer, q, k, v, q_out, rope, status, tree, node_begin, q_weight, k_weight, eps, interleaved, stream):
     (n, hq), (B, hkv, dim, dtype, device), pack = _count(q), cache.shape, _packed
     rows = rot = rope_at = 0
     if rope is not None:
@@ -540,9 +570,9 @@ def spec_tree_kv_append(cache: KVCache, layer: int, q: torch.Tensor, k: torch.Te
                                            _vectors("v", v, dtype, ks, device), _vectors("q_out", q_out, dtype, qs, device))
     nodes_at = pack.nodes(tree, B, node_begin, n, device)
     stream = _ready(device, status, stream)
-    _check(_lib.spec_tree_kv_append(B, cache.at, layer, nodes_at, hq, q_at, k_at, v_at, out_at, rope_at, rows, rot,
-                                    interleaved, None if q_weight is None else q_weight.data_ptr(),
-                                    None if k_weight is None else k_weight.data_ptr(), eps, status.data_ptr(), stream))
+    _check(entry(B, cache.at, layer, nodes_at, hq, q_at, k_at, v_at, out_at, rope_at, rows, rot, interleaved,
+                 None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps,
+                 status.data_ptr(), stream))
 
 
 class AttendWorkspace:
@@ -562,6 +592,11 @@ def spec_tree_attend(cache: KVCache, layer: int, q: torch.Tensor, out: torch.Ten
                      stream=None):
     """Nodes node_begin .. node_begin + q.shape[1] - 1 of every tree attend to the committed tokens, their
     ancestors and themselves; scale defaults to head_dim ** -0.5."""
+    _kind(cache, KVCache)
+    _attend(_lib.spec_tree_attend, cache, layer, q, out, workspace, status, tree, node_begin, scale, stream)
+
+
+def _attend(entry, cache, layer, q, out, workspace, status, tree, node_begin, scale, stream):
     (n, hq), (B, _, dim, dtype, device), pack = _count(q), cache.shape, _packed
     qs = (B, n, hq, dim)
     q_at, out_at, _, _ = pack.heads2(_vectors("q", q, dtype, qs, device), _vectors("out", out, dtype, qs, device))
@@ -569,14 +604,19 @@ def spec_tree_attend(cache: KVCache, layer: int, q: torch.Tensor, out: torch.Ten
     stream = _ready(device, status, stream)
     if workspace.device != device:
         raise SpecTreeError("the workspace must be on the cache's device")
-    _check(_lib.spec_tree_attend(B, cache.at, layer, nodes_at, hq, q_at, out_at, dim ** -0.5 if scale is None else scale,
-                                 workspace.at, workspace.bytes, status.data_ptr(), stream))
+    _check(entry(B, cache.at, layer, nodes_at, hq, q_at, out_at, dim ** -0.5 if scale is None else scale, workspace.at,
+                 workspace.bytes, status.data_ptr(), stream))
 
 
 def spec_tree_kv_commit(cache: KVCache, accept_len: torch.Tensor, out_node: torch.Tensor, new_len: torch.Tensor,
                         status: torch.Tensor, stream=None):
     """Move the accepted path (spec_tree_verify's accept_len and out_node) behind the committed tokens in
     every layer; new_len [B] receives the new committed lengths (then cache.set_lengths(new_len))."""
+    _kind(cache, KVCache)
+    _commit(_lib.spec_tree_kv_commit, cache, accept_len, out_node, new_len, status, stream)
+
+
+def _commit(entry, cache, accept_len, out_node, new_len, status, stream):
     B, device = (cache.B,), cache.device
     if out_node.dim() != 2:
         raise SpecTreeError("out_node must be [B][depth + 1]")
@@ -585,4 +625,167 @@ def spec_tree_kv_commit(cache: KVCache, accept_len: torch.Tensor, out_node: torc
     node_at = _int_rows("out_node", out_node, (cache.B, stride), device)
     new_at = _int_rows("new_len", new_len, B, device)
     stream = _ready(device, status, stream)
-    _check(_lib.spec_tree_kv_commit(cache.B, cache.at, accept_at, node_at, stride, new_at, status.data_ptr(), stream))
+    _check(entry(cache.B, cache.at, accept_at, node_at, stride, new_at, status.data_ptr(), stream))
+
+
+# ------------------------------------------------------------- a cache in 4 bits ---
+
+def _strides(x: torch.Tensor):
+    """Strides of x; the stride of a single entry means nothing."""
+    return [0 if n == 1 else s for n, s in zip(x.shape, x.stride())]
+
+
+class KVCache4:
+    """A paged key-value cache in 4 bits (the spec_tree_kv4_t of the C ABI): spec_tree_kv4_append, _attend, _commit and
+    _read take it where the calls without the 4 take a KVCache.
+
+    k, v: uint8 [layers][pages][page_size][kv heads][head_dim / 2], two codes a byte, any strides with contiguous
+    bytes of a head (a [layers][pages][heads][page_size][head_dim / 2] pool, passed transposed, is read best);
+    scale: [layers][pages][kv heads][page_size][4], key scale, key zero, value scale and value zero of every entry, in the
+    model's type (bf16 or f16), the last two dimensions contiguous;
+    page_table, seq_len: as a KVCache's.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, scale: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor):
+        if k.dim() != 5 or k.shape != v.shape or _strides(k) != _strides(v):
+            raise SpecTreeError("k and v must be alike, [layers][pages][page_size][kv heads][head_dim / 2]")
+        if k.dtype is not torch.uint8 or v.dtype is not torch.uint8:
+            raise SpecTreeError("k and v must be uint8, two codes a byte")
+        if k.stride(4) != 1:
+            raise SpecTreeError("the bytes of a head must be contiguous")
+        layers, pages, size, heads, half = k.shape
+        if scale.dtype not in _HALF:
+            raise SpecTreeError(f"unsupported scale dtype {scale.dtype}")
+        if scale.shape != (layers, pages, heads, size, 4) or scale.stride(4) != 1 or scale.stride(3) != 4:
+            raise SpecTreeError("scale must be [layers][pages][kv heads][page_size][4], the last two dimensions contiguous")
+        width, table_stride = _table_shape(page_table)
+        device = k.get_device()
+        if v.get_device() != device or scale.get_device() != device or page_table.get_device() != device:
+            raise SpecTreeError("k, v, scale and page_table must be on one device")
+        self.k, self.v, self.scale, self.page_table, self.B, self.device = k, v, scale, page_table, page_table.shape[0], device
+        st, sc = [2 * x for x in _strides(k)], _strides(scale)
+        c = c_kv4(c_kv(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), None, st[0], st[1], st[2], st[3],
+                       _HALF[scale.dtype], layers, pages, size, heads, 2 * half, width, table_stride),
+                  scale.data_ptr(), sc[0], sc[1], sc[2])
+        self._c, self.at = c, ctypes.addressof(c)
+        self.shape = (self.B, heads, 2 * half, scale.dtype, device)
+        self.set_lengths(seq_len)
+
+    @classmethod
+    def zeros(cls, layers: int, pages: int, page_size: int, kv_heads: int, head_dim: int, page_table: torch.Tensor,
+              seq_len: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> "KVCache4":
+        """A cache on the page table's device with pools of its own, in the order that is read best."""
+        device = page_table.device
+        k, v = (torch.zeros((layers, pages, kv_heads, page_size, head_dim // 2), dtype=torch.uint8, device=device).transpose(2, 3)
+                for _ in range(2))
+        scale = torch.zeros((layers, pages, kv_heads, page_size, 4), dtype=dtype, device=device)
+        return cls(k, v, scale, page_table, seq_len)
+
+    def set_lengths(self, seq_len: torch.Tensor):
+        """Committed tokens from now on, e.g. the new_len of spec_tree_kv4_commit."""
+        self._c.kv.seq_len = _int_rows("seq_len", seq_len, (self.B,), self.device)
+        self.seq_len = seq_len
+
+    def c(self) -> c_kv4:
+        return self._c
+
+
+def _kind(cache, cls):
+    if type(cache) is not cls and not isinstance(cache, cls):
+        raise SpecTreeError(f"the cache must be a {cls.__name__}")
+
+
+def spec_tree_kv4_append(cache: KVCache4, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                         q_out: torch.Tensor, rope: Optional[torch.Tensor], status: torch.Tensor, tree=None,
+                         node_begin: int = 0, q_weight: Optional[torch.Tensor] = None,
+                         k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                         stream=None):
+    """spec_tree_kv_append into a cache in 4 bits: the same arguments; the entries are quantised."""
+    _kind(cache, KVCache4)
+    _append(_lib.spec_tree_kv4_append, cache, layer, q, k, v, q_out, rope, status, tree, node_begin, q_weight, k_weight, eps,
+            interleaved, stream)
+
+
+def spec_tree_kv4_attend(cache: KVCache4, layer: int, q: torch.Tensor, out: torch.Tensor, workspace: AttendWorkspace,
+                         status: torch.Tensor, tree=None, node_begin: int = 0, scale: Optional[float] = None,
+                         stream=None):
+    """spec_tree_attend over a cache in 4 bits: the same arguments, the same workspace."""
+    _kind(cache, KVCache4)
+    _attend(_lib.spec_tree_kv4_attend, cache, layer, q, out, workspace, status, tree, node_begin, scale, stream)
+
+
+def spec_tree_kv4_commit(cache: KVCache4, accept_len: torch.Tensor, out_node: torch.Tensor, new_len: torch.Tensor,
+                         status: torch.Tensor, stream=None):
+    """spec_tree_kv_commit of a cache in 4 bits."""
+    _kind(cache, KVCache4)
+    _commit(_lib.spec_tree_kv4_commit, cache, accept_len, out_node, new_len, status, stream)
+
+
+def spec_tree_kv4_read(cache: KVCache4, layer: int, k: torch.Tensor, v: torch.Tensor, status: torch.Tensor,
+                       first: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None, stream=None):
+    """What slots first[b] .. first[b] + k.shape[1] - 1 of every sequence hold (first: int32 [B], None: from slot 0),
+    as keys and values [B][entries][kv heads][head_dim]; zeros from entry counts[b] on (int32 [B], None: all there)."""
+    _kind(cache, KVCache4)
+    (n, _), (B, hkv, dim, dtype, device), pack = _count(k), cache.shape, _packed
+    shape = (B, n, hkv, dim)
+    k_at, v_at, _, _ = pack.heads2(_vectors("k", k, dtype, shape, device), _vectors("v", v, dtype, shape, device))
+    first_at = None if first is None else _int_rows("first", first, (B,), device)
+    counts_at = None if counts is None else _int_rows("counts", counts, (B,), device)
+    stream = _ready(device, status, stream)
+    _check(_lib.spec_tree_kv4_read(B, cache.at, layer, first_at, counts_at, n, k_at, v_at, status.data_ptr(), stream))
+
+
+# --------------------------------------------------------- pages of the sequences ---
+
+class PagePool:
+    """The pages of a cache of B sequences (the spec_tree_pages_t of the C ABI): `page_table` [B][max_pages] is the
+    cache's, `held` [B] counts each sequence's pages, the first n_free[0] of `free` are nobody's.  All int32 on one
+    device, made here (every page free, the lowest handed out first) or given."""
+
+    def __init__(self, n_pages: int, page_size: int, B: int, max_pages: int, page_table: Optional[torch.Tensor] = None,
+                 held: Optional[torch.Tensor] = None, free: Optional[torch.Tensor] = None,
+                 n_free: Optional[torch.Tensor] = None, device="cuda"):
+        given = [t is not None for t in (page_table, held, free, n_free)]
+        if any(given) and not all(given):
+            raise SpecTreeError("page_table, held, free and n_free are given together")
+        if not any(given):
+            kind = dict(dtype=torch.int32, device=device)
+            page_table, held = torch.full((B, max_pages), -1, **kind), torch.zeros(B, **kind)
+            free, n_free = torch.arange(n_pages - 1, -1, -1, **kind), torch.full((1,), n_pages, **kind)
+        width, table_stride = _table_shape(page_table)
+        if page_table.shape != (B, max_pages):
+            raise SpecTreeError("page_table must be [B][max_pages]")
+        self.page_table, self.held, self.free, self.n_free = page_table, held, free, n_free
+        self.n_pages, self.page_size, self.B, self.device = n_pages, page_size, B, page_table.get_device()
+        self.scratch = torch.zeros(B + 1, dtype=torch.int32, device=page_table.device)
+        c = c_pages(page_table.data_ptr(), _int_rows("held", held, (B,), self.device),
+                    _int_rows("free", free, (n_pages,), self.device), _int_rows("n_free", n_free, (1,), self.device),
+                    self.scratch.data_ptr(), n_pages, page_size, max_pages, table_stride)
+        self._c, self.at = c, ctypes.addressof(c)
+
+    def c(self) -> c_pages:
+        return self._c
+
+
+def spec_tree_kv_reserve(pool: PagePool, seq_len: torch.Tensor, count: int, status: torch.Tensor,
+                         n_nodes: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None, stream=None):
+    """Pages for slots 0 .. seq_len[b] + count - 1 of every sequence (count at most n_nodes[b] where given); slots
+    (int64 [B][count]) receives page * page_size + entry of the last `count`, -1 where there is none."""
+    device, B = pool.device, pool.B
+    at = None
+    if slots is not None:
+        if slots.dtype is not torch.int64 or slots.shape != (B, count) or not slots.is_contiguous() or slots.get_device() != device:
+            raise SpecTreeError(f"slots must be contiguous int64 {[B, count]} on the pool's device")
+        at = slots.data_ptr()
+    len_at = _int_rows("seq_len", seq_len, (B,), device)
+    nodes_at = None if n_nodes is None else _int_rows("n_nodes", n_nodes, (B,), device)
+    stream = _ready(device, status, stream)
+    _check(_lib.spec_tree_kv_reserve(B, pool.at, len_at, nodes_at, count, at, status.data_ptr(), stream))
+
+
+def spec_tree_kv_release(pool: PagePool, keep: torch.Tensor, status: torch.Tensor, stream=None):
+    """Every sequence keeps the pages of its first keep[b] slots (int32 [B]; 0: none) and gives the rest back."""
+    device = pool.device
+    keep_at = _int_rows("keep", keep, (pool.B,), device)
+    stream = _ready(device, status, stream)
+    _check(_lib.spec_tree_kv_release(pool.B, pool.at, keep_at, status.data_ptr(), stream))

@@ -1,6 +1,7 @@
 // The paged key-value cache's writes: appending a tree's nodes with the head
-// norms and the rotation on the way (spec_tree_kv_append), and moving the
-// accepted path behind the committed tokens (spec_tree_kv_commit).
+// norms and the rotation on the way (spec_tree_kv_append, and into a cache of 4
+// bits spec_tree_kv4_append), and moving the accepted path behind the committed
+// tokens (spec_tree_kv_commit).
 #include "st_kernels.h"
 #include "st_kv.cuh"
 
@@ -37,6 +38,52 @@ __device__ __forceinline__ uint4 pack_pairs(const F2 (&x)[4]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+__device__ __forceinline__ __nv_bfloat16 low_of(__nv_bfloat162 x) { return __low2bfloat16(x); }
+__device__ __forceinline__ __nv_bfloat16 high_of(__nv_bfloat162 x) { return __high2bfloat16(x); }
+__device__ __forceinline__ __half low_of(__half2 x) { return __low2half(x); }
+__device__ __forceinline__ __half high_of(__half2 x) { return __high2half(x); }
+__device__ __forceinline__ float round_down(__nv_bfloat16, float x) { return __bfloat162float(__float2bfloat16_rz(x)); }
+__device__ __forceinline__ float round_down(__half, float x) { return __half2float(__float2half_rz(x)); }
+
+// A vector in 4 bits: the LANES lanes that share it hold 16 elements each, u; w
+// are their codes, and each lane gets (scale, zero).  The range over 15 and the
+// quotients are float32's, correctly rounded, so that ties fall as they are
+// defined to: of vectors of 16-bit numbers a few in a thousand elements lie
+// exactly between two codes.
+template <typename T, int LANES>
+__device__ __forceinline__ uint32_t quantise(const uint4 (&u)[2], uint32_t (&w)[2]) {
+  const uint32_t in[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+  auto low = Pair<T>::pair(in[0]), high = low;
+#pragma unroll
+  for (int e = 1; e < 8; ++e) low = __hmin2_nan(low, Pair<T>::pair(in[e])), high = __hmax2_nan(high, Pair<T>::pair(in[e]));
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) {
+    low = __hmin2_nan(low, __shfl_xor_sync(FULL, low, o));
+    high = __hmax2_nan(high, __shfl_xor_sync(FULL, high, o));
+  }
+  const float z = static_cast<float>(__hmin_nan(low_of(low), high_of(low)));
+  const float range = static_cast<float>(__hmax_nan(low_of(high), high_of(high))) - z;
+  const bool fine = isfinite(range);
+  const float s = round_down(T(), __fdiv_rn(range, 15.0f));
+  // 1.5 * 2^23 + n holds n in its lowest bits, n rounded to the nearest even
+  constexpr float MAGIC = 12582912.0f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t sum = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 x = Pair<T>::unpack(in[4 * h + e]);
+      sum += __float_as_uint(fminf(__fdiv_rn(x.x - z, s), 15.0f) + MAGIC) << (8 * e);
+      sum += __float_as_uint(fminf(__fdiv_rn(x.y - z, s), 15.0f) + MAGIC) << (8 * e + 4);
+    }
+    uint32_t magics = 0;  // the bits of MAGIC, shifted and added up alike
+#pragma unroll
+    for (int e = 0; e < 8; ++e) magics += 0x4b400000u << (4 * e);
+    w[h] = fine && s > 0.0f ? sum - magics : 0u;
+  }
+  return fine ? Pair<T>::pack(s, z) : Pair<T>::pack(NAN, NAN);
+}
+
 // One or more warps per node.  A head vector belongs to D / 16 neighbouring
 // lanes, two chunks of 8 elements (16 bytes) each: the two that turn with each
 // other (elements j and j + rot_dim / 2), or two neighbours where pairs are
@@ -54,7 +101,7 @@ __device__ __forceinline__ uint4 pack_pairs(const F2 (&x)[4]) {
 // in it.  One chunk per lane, the partner's got by shuffles, took 24.5 (21.2 in
 // the L2); one vector per thread, with a node's loads and products made for
 // each, 37.2 in the L2.
-template <typename T, int D, bool INTERLEAVED>
+template <typename T, int D, bool INTERLEAVED, bool CODES>
 __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_constant__ AppendLaunch L, int page_shift,
                                                                    int nodes, int spread) {
   constexpr int LANES = D / 16, PER_STEP = 32 / LANES;
@@ -207,6 +254,23 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
   weighted(L.k_weight);
   T* k_to = static_cast<T*>(L.kv.k) + L.layer * L.kv.layer_stride + off;
   T* v_to = static_cast<T*>(L.kv.v) + L.layer * L.kv.layer_stride + off;
+  T* scale_to = nullptr;
+  if (CODES && off >= 0)
+    scale_to = static_cast<T*>(L.scales.data) + L.layer * L.scales.layer_stride +
+               kv_scale_offset(L.kv, L.scales, b, static_cast<int64_t>(len) + n, page_shift);
+  // a key (head < n_kv) or value in 4 bits, whatever the other lanes hold
+  auto store_codes = [&](int head, const uint4 (&x)[2]) {
+    uint32_t w[2];
+    const uint32_t pair = quantise<T, LANES>(x, w);
+    if (off < 0 || head >= 2 * n_kv) return;
+    const bool value = head >= n_kv;
+    const int h = value ? head - n_kv : head;
+    uint8_t* to = static_cast<uint8_t*>(value ? L.kv.v : L.kv.k);
+    const int64_t at = L.layer * L.kv.layer_stride + off + h * L.kv.head_stride;
+    *reinterpret_cast<uint32_t*>(to + (at + e0) / 2) = w[0];
+    *reinterpret_cast<uint32_t*>(to + (at + e1) / 2) = w[1];
+    if (lane == 0) *reinterpret_cast<uint32_t*>(scale_to + h * L.scales.head_stride + (value ? 2 : 0)) = pair;
+  };
   for (int at = kv_step0; at * PER_STEP < 2 * n_kv; at += APPEND_BATCH * spread) {
     fetch(false, at);
 #pragma unroll
@@ -217,7 +281,9 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const __grid_
         turn(raw[u], L.k_weight != nullptr);
         if (head >= n_kv) raw[u][0] = v0, raw[u][1] = v1;  // a value beside keys
       }
-      if (off >= 0) {
+      if (CODES) {
+        if ((at + u * spread) * PER_STEP < 2 * n_kv) store_codes(head, raw[u]);
+      } else if (off >= 0) {
         if (head < n_kv)
           store(k_to + head * L.kv.head_stride, raw[u]);
         else if (head < 2 * n_kv)
@@ -281,7 +347,7 @@ __global__ void __launch_bounds__(COMMIT_THREADS) kv_commit_kernel(const CommitL
   }
 }
 
-template <typename T, int D, bool INTERLEAVED>
+template <typename T, int D, bool INTERLEAVED, bool CODES>
 cudaError_t append_as(const AppendLaunch& L, cudaStream_t stream) {
   constexpr int PER_STEP = 512 / D;
   const int nodes = L.B * L.nodes.count;
@@ -290,13 +356,14 @@ cudaError_t append_as(const AppendLaunch& L, cudaStream_t stream) {
   while (spread < steps && static_cast<int64_t>(nodes) * spread < L.num_sms * APPEND_WARPS) spread *= 2;
   if (spread > steps) spread = steps;
   const int64_t ctas = (static_cast<int64_t>(nodes) * spread + APPEND_THREADS / 32 - 1) / (APPEND_THREADS / 32);
-  return launch_pdl(kv_append_kernel<T, D, INTERLEAVED>, dim3(static_cast<unsigned>(ctas)), dim3(APPEND_THREADS), 0, stream, L,
+  return launch_pdl(kv_append_kernel<T, D, INTERLEAVED, CODES>, dim3(static_cast<unsigned>(ctas)), dim3(APPEND_THREADS), 0, stream, L,
                     log2_of(L.kv.page_size), nodes, spread);
 }
 
 template <typename T, int D>
 cudaError_t append(const AppendLaunch& L, cudaStream_t stream) {
-  return L.interleaved ? append_as<T, D, true>(L, stream) : append_as<T, D, false>(L, stream);
+  if (L.scales.data) return L.interleaved ? append_as<T, D, true, true>(L, stream) : append_as<T, D, false, true>(L, stream);
+  return L.interleaved ? append_as<T, D, true, false>(L, stream) : append_as<T, D, false, false>(L, stream);
 }
 
 }  // namespace

@@ -67,6 +67,12 @@ struct VerifyLaunch {
   int64_t draft_row_stride;  // elements
 };
 
+// Scales and zeros of a cache of 4 bits; data = NULL: a cache of 16 bits.
+struct KvScale {
+  void* data = nullptr;
+  int64_t layer_stride = 0, page_stride = 0, head_stride = 0;  // elements
+};
+
 struct AppendLaunch {
   int B, layer, n_q_heads;
   spec_tree_kv_t kv;
@@ -80,6 +86,7 @@ struct AppendLaunch {
   float eps;
   uint32_t* status;
   int num_sms;
+  KvScale scales;
 };
 
 struct AttendLaunch {
@@ -91,6 +98,7 @@ struct AttendLaunch {
   void* workspace;
   uint32_t* status;
   int num_sms;
+  KvScale scales;
 };
 
 struct CommitLaunch {
@@ -100,6 +108,33 @@ struct CommitLaunch {
   const int32_t* out_node;
   int path_stride;
   int32_t* new_len;
+  uint32_t* status;
+  KvScale scales;
+};
+
+struct ReadLaunch {
+  int B, layer, count;
+  spec_tree_kv_t kv;
+  KvScale scales;
+  const int32_t* first;
+  const int32_t* counts;
+  spec_tree_heads_t k, v;
+  uint32_t* status;
+};
+
+struct ReserveLaunch {
+  int B, count;
+  spec_tree_pages_t pages;
+  const int32_t* seq_len;
+  const int32_t* n_nodes;
+  int64_t* slots;
+  uint32_t* status;
+};
+
+struct ReleaseLaunch {
+  int B;
+  spec_tree_pages_t pages;
+  const int32_t* keep;
   uint32_t* status;
 };
 
@@ -127,5 +162,10 @@ cudaError_t launch_kv_append(const AppendLaunch& L, cudaStream_t stream);
 cudaError_t launch_kv_commit(const CommitLaunch& L, cudaStream_t stream);
 size_t attend_workspace_bytes(int num_sms, int64_t rows, int head_dim);
 cudaError_t launch_attend(const AttendLaunch& L, cudaStream_t stream);
+cudaError_t launch_kv4_commit(const CommitLaunch& L, cudaStream_t stream);
+cudaError_t launch_kv4_read(const ReadLaunch& L, cudaStream_t stream);
+cudaError_t launch_kv4_attend(const AttendLaunch& L, cudaStream_t stream);
+cudaError_t launch_kv_reserve(const ReserveLaunch& L, cudaStream_t stream);
+cudaError_t launch_kv_release(const ReleaseLaunch& L, cudaStream_t stream);
 
 }  // namespace st

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "st_common.cuh"
+#include "st_kernels.h"
 
 namespace st {
 
@@ -89,6 +90,14 @@ __device__ __forceinline__ int64_t kv_slot_offset(const spec_tree_kv_t& kv, int 
   const int page = kv.page_table[static_cast<int64_t>(b) * kv.table_stride + idx];
   if (page < 0 || page >= kv.n_pages) return -1;
   return page * kv.page_stride + (slot & (kv.page_size - 1)) * kv.token_stride;
+}
+
+// Element offset, inside one layer, of the four scales and zeros of head 0 of a
+// slot that has a page (kv_slot_offset was not negative).
+__device__ __forceinline__ int64_t kv_scale_offset(const spec_tree_kv_t& kv, const KvScale& scales, int b, int64_t slot,
+                                                   int page_shift) {
+  const int page = kv.page_table[static_cast<int64_t>(b) * kv.table_stride + (slot >> page_shift)];
+  return page * scales.page_stride + (slot & (kv.page_size - 1)) * 4;
 }
 
 // Nodes of tree b that exist.

@@ -578,6 +578,134 @@ size_t spec_tree_attend_workspace_bytes(int B, int count, int n_q_heads, int n_k
 int spec_tree_kv_commit(int B, const spec_tree_kv_t* kv, const int32_t* accept_len, const int32_t* out_node,
                         int path_stride, int32_t* new_len, uint32_t* status, spec_tree_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The same cache held in 4 bits: append, attention and commit as above, and
+ * reading entries back.  Per head, a token's key or value takes head_dim / 2
+ * bytes and two numbers of the model's type (head_dim 128: 136 bytes for both
+ * instead of 512).
+ *
+ * A vector x of head_dim elements of kv.dtype is held as
+ *   zero  z = min x
+ *   scale s = (max x - min x) / 15 in float32, rounded towards zero to kv.dtype
+ *   codes n = (x - z) / s in float32, rounded to the nearest whole number (ties
+ *         to even), 15 where that is more; 0 where s is 0
+ * and stands for z + s n, which lies within half a step s of x, but for its
+ * largest elements (within s / 2 and what the scale lost).  A vector with an
+ * element that is not finite, or whose range is past float32, is held with
+ * NaN in both z and s and stands for NaN.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * kv: as above, with k and v the codes, two a byte: element d is the low
+ *   (d even) or high (d odd) half of byte
+ *     (l * layer_stride + g * page_stride + o * token_stride + h * head_stride + d) / 2,
+ *   strides in elements (codes) and multiples of 32; kv.dtype is the model's type
+ *   (queries, keys, values, outputs, scales and zeros).
+ * scale: kv.dtype, the four numbers of entry o, page g, head h, layer l
+ *   (key scale, key zero, value scale, value zero) at
+ *     l * scale_layer_stride + g * scale_page_stride + h * scale_head_stride + 4 * o;
+ *   16-byte aligned, strides (in elements) multiples of 8.
+ */
+typedef struct spec_tree_kv4_t {
+  spec_tree_kv_t kv;
+  void* scale;
+  int64_t scale_layer_stride, scale_page_stride, scale_head_stride;
+} spec_tree_kv4_t;
+
+/* spec_tree_kv_append into a cache of 4 bits: the entries are those that a
+ * cache of kv.dtype would have got, quantised.  Arguments, rounding and status
+ * bits are the same. */
+int spec_tree_kv4_append(int B, const spec_tree_kv4_t* kv, int layer, const spec_tree_nodes_t* nodes, int n_q_heads,
+                         const spec_tree_heads_t* q, const spec_tree_heads_t* k, const spec_tree_heads_t* v,
+                         const spec_tree_heads_t* q_out, const float* rope, int rope_rows, int rot_dim,
+                         int interleaved, const void* q_weight, const void* k_weight, float eps, uint32_t* status,
+                         spec_tree_stream_t stream);
+
+/*
+ * spec_tree_attend over a cache of 4 bits; arguments, workspace (the same one
+ * serves both), status bits and repeatability are the same.  Calls of up to
+ * SPEC_TREE_KV4_FEW_ROWS rows (nodes times query heads per key head) multiply
+ * the codes as they are and apply scales and zeros in float32; the weights,
+ * times the values' scales, are rounded to bf16.  Calls of more rows round keys
+ * and values, once, to kv.dtype.  A key or value that stands for NaN makes NaN
+ * of every row that sees it, whatever its weight, and has no influence on the
+ * others.
+ */
+#define SPEC_TREE_KV4_FEW_ROWS 16
+int spec_tree_kv4_attend(int B, const spec_tree_kv4_t* kv, int layer, const spec_tree_nodes_t* nodes, int n_q_heads,
+                         const spec_tree_heads_t* q, const spec_tree_heads_t* out, float scale, void* workspace,
+                         size_t workspace_bytes, uint32_t* status, spec_tree_stream_t stream);
+
+/* spec_tree_kv_commit of a cache of 4 bits: codes, scales and zeros as they are. */
+int spec_tree_kv4_commit(int B, const spec_tree_kv4_t* kv, const int32_t* accept_len, const int32_t* out_node,
+                         int path_stride, int32_t* new_len, uint32_t* status, spec_tree_stream_t stream);
+
+/*
+ * Reads entries of layer `layer` back: keys and values z + s n, rounded once to
+ * kv.dtype, of slots first[b] .. first[b] + count - 1 of every sequence into k
+ * and v (kv.n_kv_heads vectors of [B][count] entries, not overlapping).
+ *   first:  device [B] int32, or NULL: slot 0 on;
+ *   counts: device [B] int32, or NULL: all; entries from counts[b] on are not
+ *           read and get zeros.
+ * kv.seq_len is not read and may be NULL.  A slot without a page (or before
+ * the first) sets SPEC_TREE_S_PAGES and gets zeros.
+ */
+int spec_tree_kv4_read(int B, const spec_tree_kv4_t* kv, int layer, const int32_t* first, const int32_t* counts, int count,
+                       const spec_tree_heads_t* k, const spec_tree_heads_t* v, uint32_t* status, spec_tree_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Pages for the sequences of a cache (of either kind), handed out and taken
+ * back on the device, so that a step needs no host in between.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * A pool of n_pages pages (device pointers, caller-owned).
+ *   page_table: [B][table_stride] int32, as in spec_tree_kv_t: a sequence's
+ *               first held[b] entries are its pages;
+ *   held:       [B] int32, 0 .. max_pages;
+ *   free_pages: [n_pages] int32: its first n_free[0] entries are the pages
+ *               that no sequence holds, the last of them handed out first;
+ *   n_free:     [1] int32;
+ *   scratch:    [B + 1] int32, zero before the first call that uses it; every
+ *               call leaves what the next one needs.
+ * To begin: held all 0, free_pages any order of all pages, n_free n_pages.
+ * Every page is in one place: one row's held part, or the free part.
+ */
+typedef struct spec_tree_pages_t {
+  int32_t* page_table;
+  int32_t* held;
+  int32_t* free_pages;
+  int32_t* n_free;
+  int32_t* scratch;
+  int32_t n_pages, page_size, max_pages, table_stride;
+} spec_tree_pages_t;
+
+/*
+ * Every sequence gets the pages that its slots 0 .. seq_len[b] + n_b - 1 need
+ * and that it does not hold; n_b = count, or min(count, n_nodes[b]) (n_nodes:
+ * device [B] int32 or NULL).  Sequences are served in order; the first for
+ * which the free pages do not suffice gets none, nor does any behind it that
+ * needs some (SPEC_TREE_S_PAGES).  One that would need more than max_pages gets
+ * none and stands in nobody's way (SPEC_TREE_S_PAGES); one of negative length
+ * gets none (SPEC_TREE_S_NODES).
+ *   slots: device [B][count] int64, or NULL: page * page_size + entry of slot
+ *          seq_len[b] + i for i < n_b, -1 for one without a page and for i >= n_b.
+ * page_size a power of two, 8 to 65536; count 1 to 2^20.
+ */
+int spec_tree_kv_reserve(int B, const spec_tree_pages_t* pages, const int32_t* seq_len, const int32_t* n_nodes, int count,
+                         int64_t* slots, uint32_t* status, spec_tree_stream_t stream);
+
+/*
+ * Every sequence keeps the pages of its first keep[b] slots (none: it is
+ * finished; new_len of a commit: what rejected nodes alone took) and gives the
+ * rest back; their table entries become -1.  Pages come back in an order in
+ * which the same reservation takes them out again.  keep[b] < 0 keeps all
+ * (SPEC_TREE_S_NODES).  Nothing changes where more pages would come back than
+ * the pool has (SPEC_TREE_S_PAGES).
+ */
+int spec_tree_kv_release(int B, const spec_tree_pages_t* pages, const int32_t* keep, uint32_t* status,
+                         spec_tree_stream_t stream);
+
 /* Message for a return code (static string). */
 const char* spec_tree_strerror(int code);
 
