@@ -14,7 +14,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libspec_tree.so")
 SOURCES = ["api.cu", "select_expand.cu", "rank_tree.cu", "verify_walk.cu", "select_wide.cu", "smart_fit.cpp",
            "layer_static.cu", "wait_selftest.cu", "verify_dense.cu", "kv_api.cu", "kv_cache.cu", "attend.cu",
-           "kv4.cu", "attend4.cu", "kv_pages.cu"]
+           "kv4.cu", "attend4.cu", "attend4_few.cu", "kv_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

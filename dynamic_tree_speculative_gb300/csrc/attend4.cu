@@ -106,6 +106,7 @@ cudaError_t attend(const AttendLaunch& L, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_kv4_attend(const AttendLaunch& L, cudaStream_t stream) {
+  if (L.nodes.count * (L.n_q_heads / L.kv.n_kv_heads) <= SPEC_TREE_KV4_FEW_ROWS) return launch_kv4_attend_few(L, stream);
   if (L.kv.dtype == SPEC_TREE_BF16)
     return L.kv.head_dim == 128 ? attend<__nv_bfloat16, 128>(L, stream) : attend<__nv_bfloat16, 64>(L, stream);
   return L.kv.head_dim == 128 ? attend<__half, 128>(L, stream) : attend<__half, 64>(L, stream);

@@ -164,6 +164,8 @@ size_t attend_workspace_bytes(int num_sms, int64_t rows, int head_dim);
 cudaError_t launch_attend(const AttendLaunch& L, cudaStream_t stream);
 cudaError_t launch_kv4_commit(const CommitLaunch& L, cudaStream_t stream);
 cudaError_t launch_kv4_read(const ReadLaunch& L, cudaStream_t stream);
+// up to SPEC_TREE_KV4_FEW_ROWS rows, and any number
+cudaError_t launch_kv4_attend_few(const AttendLaunch& L, cudaStream_t stream);
 cudaError_t launch_kv4_attend(const AttendLaunch& L, cudaStream_t stream);
 cudaError_t launch_kv_reserve(const ReserveLaunch& L, cudaStream_t stream);
 cudaError_t launch_kv_release(const ReleaseLaunch& L, cudaStream_t stream);
