@@ -4,11 +4,17 @@
 // With a token's key s n + z and value s' n' + z' (n, n' codes), the scores are
 // s (q . n) + z sum(q) and the outputs sum (w s') n' + sum w z': the codes
 // themselves are multiplied, and scales and zeros are applied to the few products
-// that leave.  A code's four bits, put into the mantissa of 16, are the 16-bit
-// number 16 + n without any conversion: a shift and one three-input logic
-// operation for two codes.  q . 16 goes back out with the zero; the values' 16,
-// and 8 more so that what the weights' rounding multiplies is small, come out as
-// 24 times the sum of the rounded weights, which a row of ones gives.
+// that leave.  A code in the lowest four bits of a 16-bit word is the f16 number
+// n 2^-24, in the next four 16 n 2^-24: two codes of two of the eight in a word
+// take one logic operation, and a shift by 8 serves the other four.  The factor 16
+// goes into the queries, and out of the outputs at the end.  (As bf16 numbers 16 + n,
+// each pair shifted to its place: 8 operations instead of 5 for 8 codes, and 121 us
+// instead of NEW for 64 sequences of up to 5000 tokens; the integer pipe bounds it.)
+//
+// So queries and weights are f16 too, whatever the model's type.  Queries carry a
+// power of two that brings the call's largest element near f16's; weights times
+// values' scales one for each row, which goes down as larger scales come: both
+// keep at least f16's 11 bits down to 2^-29 of the largest.
 //
 // Products are mma.sync, tokens (of keys) or elements (of values) in the rows and
 // the call's rows in the columns, so that 8 rows fill a product: the codes go
@@ -51,28 +57,21 @@ struct FewShared : Deal<WARPS> {
   int last;
 };
 
-// Codes J and J + 4 of eight as a pair of 16-bit numbers 16 + n.
-template <typename T, int J>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  if (std::is_same<T, __half>::value) {
-    w = J == 0 ? w << 6 : J == 1 ? w << 2 : J == 2 ? w >> 2 : w >> 6;
-    return (w & 0x03c003c0u) | 0x4c004c00u;
-  }
-  w = J == 0 ? w << 3 : J == 1 ? w >> 1 : J == 2 ? w >> 5 : w >> 9;
-  return (w & 0x00780078u) | 0x41804180u;
-}
-
-template <typename T>
+// f16 products with float32 sums, 16 x 8 += 16 x 16 times 16 x 8.
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  if (std::is_same<T, __half>::value)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+constexpr uint32_t LOW = 0x000f000fu, NEXT = 0x00f000f0u;  // codes n 2^-24 and 16 n 2^-24
+
+__device__ __forceinline__ float power2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// The least e with x <= 2^e, of 2^-100 or more.
+__device__ __forceinline__ int exponent_above(float x) {
+  return static_cast<int>((__float_as_uint(fmaxf(x, power2(-100))) + 0x007fffffu) >> 23) - 127;
 }
 
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {  // an 8 x 8 matrix of 16-bit numbers over the warp
@@ -132,60 +131,68 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
   __syncthreads();
 
   // ------------------------------------------------------------------- loads ---
+  // A lane's copies of a chunk: the same place in the page (or the two halves' pages), moved on from tile to tile.
   Walk<1> ahead(S);
   bool more = ahead.next(P);
   int tile = more ? ahead.s.first : 0;
+  const int c = lane % LANES, token0 = lane / LANES;  // its first token, the others 32 / LANES apart
+  const int64_t token_bytes = kv.token_stride / 2, page_bytes = kv.page_stride / 2, scale_page = P.L.scales.page_stride * 2;
+  const bool small_pages = kv.page_size < CHUNK;  // 8 tokens: a chunk has two
+  const uint8_t* key_at;                          // of page 0, entry 0 of the segment's head
+  const uint8_t* scale_at;
+  const int64_t to_values = static_cast<const uint8_t*>(kv.v) - static_cast<const uint8_t*>(kv.k);
+  const int32_t* table;
+  auto enter = [&] {  // a new segment
+    key_at = static_cast<const uint8_t*>(kv.k) + (P.L.layer * kv.layer_stride + ahead.s.head * kv.head_stride) / 2 + c * 16;
+    scale_at = static_cast<const uint8_t*>(P.L.scales.data) +
+               (P.L.layer * P.L.scales.layer_stride + ahead.s.head * P.L.scales.head_stride) * 2;
+    table = kv.page_table + static_cast<int64_t>(ahead.s.b) * kv.table_stride;
+  };
+  enter();
   int page[2] = {-1, -1};  // of the chunk's first and last 8 tokens
   auto look_up = [&] {
-    page[0] = page[1] = -1;
-    if (!more) return;
     const int slot = tile * TILE + warp * CHUNK;
-    const int32_t* table = kv.page_table + static_cast<int64_t>(ahead.s.b) * kv.table_stride;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (slot + 8 * h < ahead.s.end) page[h] = table[(slot + 8 * h) >> P.page_shift];
+    page[0] = page[1] = -1;
+    if (more && slot < ahead.s.end) page[0] = page[1] = table[slot >> P.page_shift];
+    if (small_pages && more) page[1] = slot + 8 < ahead.s.end ? table[(slot + 8) >> P.page_shift] : -1;
   };
   look_up();
+  const uint32_t to_lane = smem_u32(ring) + token0 * (D / 2) + c * 16;
+  // values: tokens in the order in which the products' lanes read them, so that these meet in few banks
+  uint32_t to_value[STEPS];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int token = token0 + i * (32 / LANES), row = (token & 8) | ((token & 1) << 2) | ((token >> 1) & 3);
+    const int turn = D == 128 ? ((row >> 1) & 1) << 1 : 0;
+    to_value[i] = smem_u32(ring) + F::CODE_BYTES + row * (D / 2) + ((c ^ turn) * 16);
+  }
   auto load = [&](int stage) {  // the next chunk, if there is one; counts as a group in any case
     if (more) {
-      const int slot = tile * TILE + warp * CHUNK, end = ahead.s.end;
-      const uint32_t to = smem_u32(ring + stage * F::STAGE_BYTES);
-      bool there[2];
-      int64_t base[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        there[h] = page[h] >= 0 && page[h] < kv.n_pages;
-        if (!there[h] && slot + 8 * h < end) set_status(P.L.status, SPEC_TREE_S_PAGES);
-        base[h] = there[h] ? page[h] : 0;
-      }
-      const int in_page = slot & (kv.page_size - 1), c = lane % LANES;
-      const int64_t head = P.L.layer * kv.layer_stride + ahead.s.head * kv.head_stride;
+      const int slot = tile * TILE + warp * CHUNK, left = ahead.s.end - slot;  // tokens of the chunk and behind it
+      const uint32_t skip = stage * F::STAGE_BYTES;
+      const int entry = slot & (kv.page_size - 1);
+      const bool ok[2] = {page[0] >= 0 && page[0] < kv.n_pages, page[1] >= 0 && page[1] < kv.n_pages};
+      if ((!ok[0] && left > 0) || (!ok[1] && left > 8)) set_status(P.L.status, SPEC_TREE_S_PAGES);
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
-        const int token = i * (32 / LANES) + lane / LANES;
-        const bool second = token >= 8;
-        const bool ok = (second ? there[1] : there[0]) && slot + token < end;
-        // entry of the token in its page: pages of 8 tokens begin anew with the second half
-        const int entry = (in_page + token) & (kv.page_size - 1);
-        const int64_t at = head + (second ? base[1] : base[0]) * kv.page_stride + entry * kv.token_stride + c * 32;
-        const uint32_t place = token * (D / 2) + c * 16;
-        copy16(to + place, static_cast<const uint8_t*>(kv.k) + at / 2, ok);
-        // values: tokens in the order in which the products' lanes read them, so that these meet in few banks
-        const int row = (token & 8) | ((token & 1) << 2) | ((token >> 1) & 3);
-        const int turn = D == 128 ? ((row >> 1) & 1) << 1 : 0;
-        copy16(to + F::CODE_BYTES + row * (D / 2) + ((c ^ turn) * 16), static_cast<const uint8_t*>(kv.v) + at / 2, ok);
+        const int token = token0 + i * (32 / LANES);
+        const int h = STEPS == 2 ? i : token / 8;  // two steps: a half each
+        const bool there = (h ? ok[1] : ok[0]) && token < left;
+        const uint8_t* from = key_at + (there ? (h ? page[1] : page[0]) : 0) * page_bytes +
+                              (small_pages ? token % 8 : entry + token) * token_bytes;
+        copy16(to_lane + skip + i * (32 / LANES) * (D / 2), from, there);
+        copy16(to_value[i] + skip, from + to_values, there);
       }
       if (lane < CHUNK / 2) {
-        const bool second = lane >= CHUNK / 4;
-        const int token = 2 * lane, entry = (in_page + token) & (kv.page_size - 1);
-        const int64_t at = P.L.layer * P.L.scales.layer_stride + (second ? base[1] : base[0]) * P.L.scales.page_stride +
-                           ahead.s.head * P.L.scales.head_stride + entry * 4;
-        copy16(to + 2 * F::CODE_BYTES + lane * 16, static_cast<const T*>(P.L.scales.data) + at,
-               (second ? there[1] : there[0]) && slot + token < end);
+        const int token = 2 * lane;
+        const bool second = lane >= CHUNK / 4, there = (second ? ok[1] : ok[0]) && token < left;
+        copy16(smem_u32(ring) + skip + 2 * F::CODE_BYTES + lane * 16,
+               scale_at + (there ? (second ? page[1] : page[0]) : 0) * scale_page + (small_pages ? token % 8 : entry + token) * 8, there);
       }
       if (++tile >= ahead.s.last) {
         more = ahead.next(P);
         tile = ahead.s.first;
+        enter();
       }
       look_up();
     }
@@ -215,63 +222,74 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
           S.sees[threadIdx.x][at / 32] |= 1u << (at % 32);
       __syncthreads();
     }
-    // queries: lane (g, t) has a quarter of row g's elements, in the codes' order
+    // queries: lane (g, t) has a quarter of row g's elements, in the codes' order; those that meet 16 n are divided by 16
     uint32_t q[NT][2 * KEY_WORDS][2];
     float sum_q[NT][2];  // of rows 2 t and 2 t + 1
     int node[NT][2];     // theirs, among those of the call
+    float scale_q;       // what a score's codes are multiplied by beside their scale
+    {
+      uint4 raw[NT][KEY_WORDS];
+      float largest = 0.0f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = nt * 8 + g, i = node_of_row(P, row);
-      const T* from = static_cast<const T*>(P.L.q.data) + s.b * P.L.q.tree_stride + i * P.L.q.node_stride +
-                      (static_cast<int64_t>(s.head) * P.group + row - i * P.group) * P.L.q.head_stride + t * 8 * KEY_WORDS;
-      float sum = 0.0f;
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = nt * 8 + g, i = node_of_row(P, row);
+        const T* from = static_cast<const T*>(P.L.q.data) + s.b * P.L.q.tree_stride + i * P.L.q.node_stride +
+                        (static_cast<int64_t>(s.head) * P.group + row - i * P.group) * P.L.q.head_stride + t * 8 * KEY_WORDS;
+        float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < KEY_WORDS; ++w) {
-        const uint4 x = row < P.rows ? *reinterpret_cast<const uint4*>(from + 8 * w) : make_uint4(0, 0, 0, 0);
-        float e[8];
-        unpack8<T>(x, e);
+        for (int w = 0; w < KEY_WORDS; ++w) {
+          raw[nt][w] = row < P.rows ? *reinterpret_cast<const uint4*>(from + 8 * w) : make_uint4(0, 0, 0, 0);
+          float e[8];
+          unpack8<T>(raw[nt][w], e);
 #pragma unroll
-        for (int d = 0; d < 8; ++d) sum += e[d];
-        q[nt][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);
-        q[nt][2 * w][1] = __byte_perm(x.x, x.z, 0x7632);
-        q[nt][2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);
-        q[nt][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);
+          for (int d = 0; d < 8; ++d) sum += e[d], largest = fmaxf(largest, fabsf(e[d]));
+        }
+        sum += __shfl_xor_sync(FULL, sum, 1);
+        sum += __shfl_xor_sync(FULL, sum, 2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sum_q[nt][e] = __shfl_sync(FULL, sum, (2 * t + e) * 4) * scale2;
+          node[nt][e] = node_of_row(P, nt * 8 + 2 * t + e);
+        }
       }
-      sum += __shfl_xor_sync(FULL, sum, 1);
-      sum += __shfl_xor_sync(FULL, sum, 2);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        sum_q[nt][e] = __shfl_sync(FULL, sum, (2 * t + e) * 4);
-        node[nt][e] = node_of_row(P, nt * 8 + 2 * t + e);
-      }
+      for (int o = 16; o > 0; o /= 2) largest = fmaxf(largest, __shfl_xor_sync(FULL, largest, o));
+      const int e = min(exponent_above(largest), 126);
+      const float up = power2(14 - e), up16 = power2(10 - e);
+      scale_q = scale2 * power2(e - 14) * 16777216.0f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int w = 0; w < KEY_WORDS; ++w) {
+          float x[8];
+          unpack8<T>(raw[nt][w], x);
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            q[nt][2 * w + d / 2][d % 2] = Pair<__half>::pack(x[d] * (d % 2 ? up16 : up), x[d + 4] * (d % 2 ? up16 : up));
+        }
     }
-    float acc[NT][MT][4], ones[NT][4];       // outputs of elements x rows, sums of the rounded weights
-    float sum[NT][2], middle[NT][2];         // of this lane's tokens: weights, weights times values' middles
-    float sub[NT][2], allowed[NT][2];        // weights' reference, and what a score may exceed it by
+    float acc[NT][MT][4];               // outputs of elements x rows
+    float sum[NT][2], middle[NT][2];    // of this lane's tokens: weights, weights times zeros
+    float sub[NT][2], fit[NT][2];       // weights' reference; the power of two that goes with the values' scales
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) sum[nt][e] = middle[nt][e] = sub[nt][e] = 0.0f, allowed[nt][e] = -INFINITY;
+      for (int e = 0; e < 2; ++e) sum[nt][e] = middle[nt][e] = 0.0f, sub[nt][e] = -INFINITY, fit[nt][e] = power2(107);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        ones[nt][e] = 0.0f;
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[nt][m][e] = 0.0f;
-      }
+        for (int e = 0; e < 4; ++e) acc[nt][m][e] = 0.0f;
     }
 
     auto chunk = [&](auto is_masked, const uint8_t* at, int slot) {
       constexpr bool MASKED = decltype(is_masked)::value;
       // scales and zeros of tokens g and g + 8
-      float ks[2], kz[2], vs[2], vm[2];
+      float ks[2], kz[2], vs[2], vz[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint2 w = *reinterpret_cast<const uint2*>(at + 2 * F::CODE_BYTES + (g + 8 * h) * 8);
         const float2 a = Pair<T>::unpack(w.x), b = Pair<T>::unpack(w.y);
-        ks[h] = a.x * scale2;
-        kz[h] = fmaf(-16.0f, ks[h], a.y * scale2);
-        vs[h] = b.x;
-        vm[h] = fmaf(8.0f, b.x, b.y);
+        ks[h] = a.x * scale_q, kz[h] = a.y, vs[h] = b.x, vz[h] = b.y;
       }
       float dot[NT][2][4];
 #pragma unroll
@@ -284,12 +302,11 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
         lds<KEY_WORDS>(b, at + (g + 8) * (D / 2) + t * (4 * KEY_WORDS));
 #pragma unroll
         for (int w = 0; w < KEY_WORDS; ++w) {
-          const uint32_t a0 = code_pair<T, 0>(a[w]), a1 = code_pair<T, 1>(a[w]), a2 = code_pair<T, 2>(a[w]), a3 = code_pair<T, 3>(a[w]);
-          const uint32_t b0 = code_pair<T, 0>(b[w]), b1 = code_pair<T, 1>(b[w]), b2 = code_pair<T, 2>(b[w]), b3 = code_pair<T, 3>(b[w]);
+          const uint32_t a8 = a[w] >> 8, b8 = b[w] >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma16816<T>(dot[nt][0], a0, b0, a1, b1, q[nt][2 * w][0], q[nt][2 * w][1]);
-            mma16816<T>(dot[nt][1], a2, b2, a3, b3, q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
+            mma16816(dot[nt][0], a[w] & LOW, b[w] & LOW, a[w] & NEXT, b[w] & NEXT, q[nt][2 * w][0], q[nt][2 * w][1]);
+            mma16816(dot[nt][1], a8 & LOW, b8 & LOW, a8 & NEXT, b8 & NEXT, q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
           }
         }
       }
@@ -298,57 +315,84 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
       for (int nt = 0; nt < NT; ++nt) {
         // x[2 h + e]: token g + 8 h, row 2 t + e
         float x[4];
-        bool grow = false;
+        bool seen[4];
+        auto score = [&](int h, int e, float less) {
+          return fmaf(ks[h], dot[nt][0][2 * h + e] + dot[nt][1][2 * h + e], fmaf(kz[h], sum_q[nt][e], -less));
+        };
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            x[2 * h + e] = fmaf(ks[h], dot[nt][0][2 * h + e] + dot[nt][1][2 * h + e], fmaf(kz[h], sum_q[nt][e], -sub[nt][e]));
+            x[2 * h + e] = score(h, e, sub[nt][e]);  // infinity where there is no reference yet
             if (MASKED) {
               const int off = slot + g + 8 * h - s.len;
-              bool seen = off < 0;
-              if (!seen) {
+              bool see = off < 0;
+              if (!see) {
                 if (parent)
-                  seen = off < SPEC_TREE_MAX_NODES && ((S.sees[min(node[nt][e], MAX_NODES_FEW - 1)][off / 32] >> (off % 32)) & 1);
+                  see = off < SPEC_TREE_MAX_NODES && ((S.sees[min(node[nt][e], MAX_NODES_FEW - 1)][off / 32] >> (off % 32)) & 1);
                 else
-                  seen = off <= P.L.nodes.begin + node[nt][e];
+                  see = off <= P.L.nodes.begin + node[nt][e];
               }
-              if (!seen) x[2 * h + e] = -INFINITY;
+              if (!see) x[2 * h + e] = -INFINITY;
+              seen[2 * h + e] = see;
             }
-            grow |= x[2 * h + e] > allowed[nt][e];
           }
-        if (__any_sync(FULL, grow)) {
+        if (__any_sync(FULL, max3(x[0], x[1], fmaxf(x[2], x[3])) > LAZY)) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            const bool fresh = sub[nt][e] == -INFINITY;
+            if (fresh) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (!MASKED || seen[2 * h + e]) x[2 * h + e] = score(h, e, 0.0f);
+            }
             float top = fmaxf(x[e], x[2 + e]);
 #pragma unroll
             for (int o = 4; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-            if (top > allowed[nt][e]) {
-              const float f = allowed[nt][e] == -INFINITY ? 0.0f : ex2(-top);
-              sub[nt][e] += top;
-              allowed[nt][e] = LAZY;
+            if (fresh ? top > -INFINITY : top > LAZY) {
+              const float f = fresh ? 0.0f : ex2(-top);
+              sub[nt][e] = fresh ? top : sub[nt][e] + top;
               x[e] -= top, x[2 + e] -= top;
               sum[nt][e] *= f, middle[nt][e] *= f;
-              ones[nt][e] *= f, ones[nt][2 + e] *= f;
 #pragma unroll
               for (int m = 0; m < MT; ++m) acc[nt][m][e] *= f, acc[nt][m][2 + e] *= f;
             }
           }
         }
+        float w[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float w[2];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float y = ex2(x[2 * h + e]);
             // what is not seen may hold anything
-            const bool skip = MASKED && x[2 * h + e] == -INFINITY;
+            const bool skip = MASKED && !seen[2 * h + e];
             sum[nt][e] += y;
-            middle[nt][e] = skip ? middle[nt][e] : fmaf(y, vm[h], middle[nt][e]);
-            w[e] = skip ? 0.0f : y * vs[h];
+            if (!skip) middle[nt][e] = fmaf(y, vz[h], middle[nt][e]);
+            w[2 * h + e] = skip ? 0.0f : y * fit[nt][e] * vs[h];
           }
-          p[nt][h] = transposed(Pair<__nv_bfloat16>::pack(w[0], w[1]));
+        if (__any_sync(FULL, max3(w[0], w[1], fmaxf(w[2], w[3])) > 32768.0f)) {
+          // larger scales than before: at most 2^7 after this, weights at most 2^8
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = 0.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (!MASKED || seen[2 * h + e]) top = fmaxf(top, vs[h]);
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+            const float next = fminf(fit[nt][e], power2(7 - exponent_above(top)));
+            const float f = next / fit[nt][e];
+            fit[nt][e] = next;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              w[2 * h + e] = MASKED && !seen[2 * h + e] ? 0.0f : ex2(x[2 * h + e]) * next * vs[h];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[nt][m][e] *= f, acc[nt][m][2 + e] *= f;
+          }
         }
+        p[nt][0] = transposed(Pair<__half>::pack(w[0], w[1]));
+        p[nt][1] = transposed(Pair<__half>::pack(w[2], w[3]));
       }
       // values: lane (g, t) has elements D / 8 g on of tokens 2 t, 2 t + 1, 2 t + 8 and 2 t + 9
       uint32_t v[4][VALUE_WORDS];
@@ -358,7 +402,6 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
         const int turn = D == 128 ? ((row >> 1) & 1) << 1 : 0;
         lds<VALUE_WORDS>(v[x], at + F::CODE_BYTES + row * (D / 2) + (D == 128 ? (((g >> 1) ^ turn) * 16 + (g & 1) * 8) : g * 4));
       }
-      using H = __nv_bfloat16;
       uint32_t a[MT][4];  // two rows of each product, two pairs of tokens
 #pragma unroll
       for (int w = 0; w < VALUE_WORDS; ++w)
@@ -367,17 +410,13 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
           const uint32_t lo = __byte_perm(v[2 * h][w], v[2 * h + 1][w], 0x5410), hi = __byte_perm(v[2 * h][w], v[2 * h + 1][w], 0x7632);
           // word w of two, elements 0 .. 7: row g + 8 w of products 0 .. 7; of one word, elements 0 .. 3 and 4 .. 7: rows g, g + 8
           const int r = 2 * h + w, r2 = VALUE_WORDS == 2 ? r : 2 * h + 1, up = VALUE_WORDS == 2 ? 4 : 0;
-          a[0][r] = code_pair<H, 0>(lo), a[1][r] = code_pair<H, 1>(lo), a[2][r] = code_pair<H, 2>(lo), a[3][r] = code_pair<H, 3>(lo);
-          a[up][r2] = code_pair<H, 0>(hi), a[up + 1][r2] = code_pair<H, 1>(hi);
-          a[up + 2][r2] = code_pair<H, 2>(hi), a[up + 3][r2] = code_pair<H, 3>(hi);
+          a[0][r] = lo & LOW, a[1][r] = lo & NEXT, a[2][r] = (lo >> 8) & LOW, a[3][r] = (lo >> 8) & NEXT;
+          a[up][r2] = hi & LOW, a[up + 1][r2] = hi & NEXT, a[up + 2][r2] = (hi >> 8) & LOW, a[up + 3][r2] = (hi >> 8) & NEXT;
         }
-      constexpr uint32_t ONES = 0x3f803f80u;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) mma16816<H>(acc[nt][m], a[m][0], a[m][1], a[m][2], a[m][3], p[nt][0], p[nt][1]);
-        mma16816<H>(ones[nt], ONES, ONES, ONES, ONES, p[nt][0], p[nt][1]);
-      }
+        for (int m = 0; m < MT; ++m) mma16816(acc[nt][m], a[m][0], a[m][1], a[m][2], a[m][3], p[nt][0], p[nt][1]);
     };
 
     for (int j = s.first; j < s.last; ++j) {
@@ -403,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
           sum[nt][e] += __shfl_xor_sync(FULL, sum[nt][e], o);
           middle[nt][e] += __shfl_xor_sync(FULL, middle[nt][e], o);
         }
-        if (g == 0) S.ref[warp][nt * 8 + 2 * t + e] = allowed[nt][e] == -INFINITY ? -INFINITY : sub[nt][e];
+        if (g == 0) S.ref[warp][nt * 8 + 2 * t + e] = sub[nt][e];
       }
     __syncthreads();
 #pragma unroll
@@ -414,20 +453,21 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) top = fmaxf(top, S.ref[w][row]);
-        const float f = allowed[nt][e] == -INFINITY ? (isnan(sum[nt][e]) ? 1.0f : 0.0f) : ex2(sub[nt][e] - top);
+        const float f = sub[nt][e] == -INFINITY ? (isnan(sum[nt][e]) ? 1.0f : 0.0f) : ex2(sub[nt][e] - top);
         if (g == 0) {
           S.sum[warp][row] = sum[nt][e] * f;
           if (warp == 0) S.top[row] = top;
         }
-        const float out = middle[nt][e] - 24.0f * ones[nt][e];
+        // products of even numbers are of n 2^-24, odd ones of 16 n 2^-24
+        const float out = middle[nt][e] * f, low = f * (16777216.0f / fit[nt][e]), next = f * (1048576.0f / fit[nt][e]);
         float* to = S.out[warp][row] + g * (D / 8);
 #pragma unroll
-        for (int m = 0; m < MT; m += 4) {
-          *reinterpret_cast<float4*>(to + m) = make_float4((acc[nt][m][e] + out) * f, (acc[nt][m + 1][e] + out) * f,
-                                                           (acc[nt][m + 2][e] + out) * f, (acc[nt][m + 3][e] + out) * f);
-          *reinterpret_cast<float4*>(to + MT + m) = make_float4((acc[nt][m][2 + e] + out) * f, (acc[nt][m + 1][2 + e] + out) * f,
-                                                                (acc[nt][m + 2][2 + e] + out) * f, (acc[nt][m + 3][2 + e] + out) * f);
-        }
+        for (int m = 0; m < MT; m += 4)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            *reinterpret_cast<float4*>(to + r * MT + m) =
+                make_float4(fmaf(acc[nt][m][2 * r + e], low, out), fmaf(acc[nt][m + 1][2 * r + e], next, out),
+                            fmaf(acc[nt][m + 2][2 * r + e], low, out), fmaf(acc[nt][m + 3][2 * r + e], next, out));
       }
     __syncthreads();
     const bool whole = s.first == 0 && s.last == s.tiles;

@@ -626,7 +626,8 @@ int spec_tree_kv4_append(int B, const spec_tree_kv4_t* kv, int layer, const spec
  * serves both), status bits and repeatability are the same.  Calls of up to
  * SPEC_TREE_KV4_FEW_ROWS rows (nodes times query heads per key head) multiply
  * the codes as they are and apply scales and zeros in float32; the weights,
- * times the values' scales, are rounded to bf16.  Calls of more rows round keys
+ * times the values' scales, are rounded to f16's 11 bits (queries too, which
+ * bf16 ones survive).  Calls of more rows round keys
  * and values, once, to kv.dtype.  A key or value that stands for NaN makes NaN
  * of every row that sees it, whatever its weight, and has no influence on the
  * others.

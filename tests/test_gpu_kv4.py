@@ -61,12 +61,12 @@ def _expected(c, q, codes, scale, layer=0):
     qn = q.double().numpy()
     out, mean_v, _, sum_v = call(qn, kp, vp)
     wide = lambda x: np.repeat(x[..., None], D, -1)  # noqa: E731
-    # sums over the tokens with the outputs' own weights: |v| + |middle|, and 8 steps
-    mean_m = call(qn, kp, wide(np.abs(vm)))[0]
-    steps_v = call(qn, kp, wide(8 * np.abs(vs)))[0]
+    # sums over the tokens with the outputs' own weights: |v| + |middle| + |zero|, and 15 steps
+    mean_m = call(qn, kp, wide(np.abs(vm) + np.abs(vm - 8 * vs)))[0]
+    steps_v = call(qn, kp, wide(15 * np.abs(vs)))[0]
     # the largest scale * sum |q| x over what a row sees
     q_k = call(np.abs(qn), np.abs(kp) + wide(np.abs(km)), vp)[2]
-    k_abs = call(np.abs(qn), wide(48 * np.abs(ks) + np.abs(km - 8 * ks)), vp)[2]
+    k_abs = call(np.abs(qn), wide(15 * np.abs(ks) + np.abs(km - 8 * ks)), vp)[2]
     tokens = int(c.seq_len.max()) + c.begin + c.N
     return out, kv4_cases.attend_bound(c.dtype, out, k_abs, q_k, None, mean_v + mean_m, steps_v, sum_v, D, tokens, few)
 
