@@ -23,8 +23,8 @@
 // own bytes to write and read, and pays off with rows to share that
 // (attend4.cu).
 //
-// A warp takes 16 tokens of each tile of 128 into a ring of its own (cp.async, no
-// barriers); at the end of a segment the CTA's 8 warps put their sums together,
+// A warp takes 32 tokens of every other tile of 128 into a ring of its own (cp.async,
+// no barriers); at the end of a segment the CTA's 8 warps put their sums together,
 // while the next segment's loads are under way.  Tiles are dealt as in the
 // attention over a cache of 16 bits.
 #include <type_traits>
@@ -35,16 +35,58 @@ namespace st {
 namespace {
 
 constexpr int WARPS = 8, THREADS = 32 * WARPS;
-constexpr int CHUNK = TILE / WARPS;  // tokens of a warp's step: the rows of a product
+constexpr int BLOCK = 16;             // tokens of a product: its rows
+constexpr int CHUNK = 2 * BLOCK;      // tokens of a warp's step
+constexpr int SIDES = CHUNK * WARPS / TILE;  // half the warps take the even tiles of a segment, half the odd ones
 constexpr int MAX_NODES_FEW = SPEC_TREE_KV4_FEW_ROWS;
 
 template <int D, int NT>  // NT: products side by side, of 8 rows each
 struct Few {
   static constexpr int CTAS = NT == 1 ? MAX_SPREAD : 1;  // on an SM
-  static constexpr int STAGES = NT == 1 ? 4 : 8;
+  static constexpr int STAGES = NT == 1 ? 2 : 4;
   static constexpr int CODE_BYTES = CHUNK * D / 2;             // of keys, and of values
   static constexpr int STAGE_BYTES = 2 * CODE_BYTES + CHUNK * 8;  // and scales and zeros
   static constexpr int RING_BYTES = WARPS * STAGES * STAGE_BYTES;
+};
+
+struct FewPlan : Plan {
+  uint64_t token_bytes, page_bytes, scale_page_bytes;
+  int64_t to_values;  // bytes from a key's codes to its value's
+};
+
+// The tiles that a side's warps load, one after the other.
+struct Loads {
+  int b, head, tile, last, tiles, end;
+  int64_t left;  // tiles of the segments behind this one
+
+  __device__ __forceinline__ Loads(const Plan& P, const Deal<WARPS>& C, int side) {
+    const Segment& s = C.start;
+    left = C.count;
+    b = s.b, head = s.head, tiles = s.tiles, end = s.end;
+    if (left <= 0) {
+      last = 0, tile = 0;
+      return;
+    }
+    const int n = static_cast<int>(min64(left, s.tiles - s.first));
+    left -= n;
+    tile = s.first + side, last = s.first + n;
+    settle(P, side);
+  }
+  // on to the next segment that has a tile of the side, if there is one
+  __device__ __forceinline__ void settle(const Plan& P, int side) {
+    while (tile >= last && left > 0) {
+      if (++head == P.L.kv.n_kv_heads) {
+        head = 0, ++b;
+        int len, cnt;
+        tree_of(P, b, len, cnt);
+        item_tiles<1>(P, len, cnt, 0, end, tiles);
+      }
+      last = static_cast<int>(min64(left, tiles));
+      left -= last;
+      tile = side;
+    }
+  }
+  __device__ __forceinline__ bool more() const { return tile < last; }
 };
 
 template <int D, int NT>
@@ -80,8 +122,11 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {  // an 8 x 8 matrix
   return y;
 }
 
-// 16 bytes into shared memory, or zeros.
-__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {  // 16 bytes into shared memory
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+__device__ __forceinline__ void copy16_or_zeros(uint32_t to, const void* from, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
 
@@ -106,10 +151,11 @@ __device__ __forceinline__ void lds(uint32_t (&w)[N], const uint8_t* at) {
 }
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(const __grid_constant__ Plan P) {
+__global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(const __grid_constant__ FewPlan P) {
   using F = Few<D, NT>;
   constexpr int LANES = D / 32;          // that load a token's codes
-  constexpr int STEPS = D / 64;          // loads of a chunk
+  constexpr int TOKENS = 32 / LANES;     // of one step of loads
+  constexpr int STEPS = BLOCK / TOKENS;  // of a block
   constexpr int KEY_WORDS = D / 32;      // of a token, per lane
   constexpr int VALUE_WORDS = D / 64;
   constexpr int MT = D / 16;             // products of the outputs
@@ -131,67 +177,84 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
   __syncthreads();
 
   // ------------------------------------------------------------------- loads ---
-  // A lane's copies of a chunk: the same place in the page (or the two halves' pages), moved on from tile to tile.
-  Walk<1> ahead(S);
-  bool more = ahead.next(P);
-  int tile = more ? ahead.s.first : 0;
-  const int c = lane % LANES, token0 = lane / LANES;  // its first token, the others 32 / LANES apart
-  const int64_t token_bytes = kv.token_stride / 2, page_bytes = kv.page_stride / 2, scale_page = P.L.scales.page_stride * 2;
-  const bool small_pages = kv.page_size < CHUNK;  // 8 tokens: a chunk has two
-  const uint8_t* key_at;                          // of page 0, entry 0 of the segment's head
-  const uint8_t* scale_at;
-  const int64_t to_values = static_cast<const uint8_t*>(kv.v) - static_cast<const uint8_t*>(kv.k);
+  const int side = warp / (WARPS / SIDES), place = warp % (WARPS / SIDES) * CHUNK;  // the warp's tokens in a tile
+  Loads ahead(P, S, side);
+  const int c = lane % LANES, token0 = lane / LANES;  // a lane's first token; the others are TOKENS apart
+  const uint8_t* key_at;    // the lane's part of token0, page 0, of the segment's head
+  const uint8_t* scale_at;  // the lane's part of the scales of block 0 or 1
   const int32_t* table;
   auto enter = [&] {  // a new segment
-    key_at = static_cast<const uint8_t*>(kv.k) + (P.L.layer * kv.layer_stride + ahead.s.head * kv.head_stride) / 2 + c * 16;
+    key_at = static_cast<const uint8_t*>(kv.k) + (P.L.layer * kv.layer_stride + ahead.head * kv.head_stride) / 2 +
+             token0 * P.token_bytes + c * 16;
     scale_at = static_cast<const uint8_t*>(P.L.scales.data) +
-               (P.L.layer * P.L.scales.layer_stride + ahead.s.head * P.L.scales.head_stride) * 2;
-    table = kv.page_table + static_cast<int64_t>(ahead.s.b) * kv.table_stride;
+               (P.L.layer * P.L.scales.layer_stride + ahead.head * P.L.scales.head_stride) * 2 + lane % (BLOCK / 2) * 16;
+    table = kv.page_table + static_cast<int64_t>(ahead.b) * kv.table_stride;
   };
   enter();
-  int page[2] = {-1, -1};  // of the chunk's first and last 8 tokens
+  uint32_t page[2] = {0, 0};  // of the chunk's two blocks
   auto look_up = [&] {
-    const int slot = tile * TILE + warp * CHUNK;
-    page[0] = page[1] = -1;
-    if (more && slot < ahead.s.end) page[0] = page[1] = table[slot >> P.page_shift];
-    if (small_pages && more) page[1] = slot + 8 < ahead.s.end ? table[(slot + 8) >> P.page_shift] : -1;
+    const int slot = ahead.tile * TILE + place;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (ahead.more() && slot + u * BLOCK < ahead.end) page[u] = table[(slot + u * BLOCK) >> P.page_shift];
   };
   look_up();
-  const uint32_t to_lane = smem_u32(ring) + token0 * (D / 2) + c * 16;
+  const uint32_t ring_at = smem_u32(ring), to_key = ring_at + token0 * (D / 2) + c * 16;
   // values: tokens in the order in which the products' lanes read them, so that these meet in few banks
-  uint32_t to_value[STEPS];
-#pragma unroll
-  for (int i = 0; i < STEPS; ++i) {
-    const int token = token0 + i * (32 / LANES), row = (token & 8) | ((token & 1) << 2) | ((token >> 1) & 3);
-    const int turn = D == 128 ? ((row >> 1) & 1) << 1 : 0;
-    to_value[i] = smem_u32(ring) + F::CODE_BYTES + row * (D / 2) + ((c ^ turn) * 16);
-  }
+  const int value_row = (token0 & 8) | ((token0 & 1) << 2) | ((token0 >> 1) & 3);
+  const int value_turn = D == 128 ? ((value_row >> 1) & 1) << 1 : 0;
+  const uint32_t to_value = ring_at + F::CODE_BYTES + value_row * (D / 2) + ((c ^ value_turn) * 16);
   auto load = [&](int stage) {  // the next chunk, if there is one; counts as a group in any case
-    if (more) {
-      const int slot = tile * TILE + warp * CHUNK, left = ahead.s.end - slot;  // tokens of the chunk and behind it
-      const uint32_t skip = stage * F::STAGE_BYTES;
-      const int entry = slot & (kv.page_size - 1);
-      const bool ok[2] = {page[0] >= 0 && page[0] < kv.n_pages, page[1] >= 0 && page[1] < kv.n_pages};
-      if ((!ok[0] && left > 0) || (!ok[1] && left > 8)) set_status(P.L.status, SPEC_TREE_S_PAGES);
+    if (ahead.more()) {
+      const int slot = ahead.tile * TILE + place, left = ahead.end - slot;  // tokens of the chunk and behind it
+      const uint32_t skip = stage * F::STAGE_BYTES, mask = kv.page_size - 1;
+      const uint32_t pages = kv.n_pages;
+      if (__builtin_expect(left >= CHUNK && page[0] < pages && page[1] < pages && kv.page_size >= BLOCK, 1)) {
 #pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        const int token = token0 + i * (32 / LANES);
-        const int h = STEPS == 2 ? i : token / 8;  // two steps: a half each
-        const bool there = (h ? ok[1] : ok[0]) && token < left;
-        const uint8_t* from = key_at + (there ? (h ? page[1] : page[0]) : 0) * page_bytes +
-                              (small_pages ? token % 8 : entry + token) * token_bytes;
-        copy16(to_lane + skip + i * (32 / LANES) * (D / 2), from, there);
-        copy16(to_value[i] + skip, from + to_values, there);
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t entry = (slot + u * BLOCK) & mask;
+          const uint8_t* from = key_at + page[u] * P.page_bytes + entry * P.token_bytes;
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i) {
+            const uint32_t to = skip + (u * STEPS + i) * TOKENS * (D / 2);
+            copy16(to_key + to, from);
+            copy16(to_value + to, from + P.to_values);
+            from += TOKENS * P.token_bytes;
+          }
+        }
+        if (lane < CHUNK / 2) {
+          const int u = lane / (BLOCK / 2);
+          copy16(ring_at + skip + 2 * F::CODE_BYTES + lane * 16,
+                 scale_at + (u ? page[1] : page[0]) * P.scale_page_bytes + ((slot + u * BLOCK) & mask) * 8);
+        }
+      } else {
+        // the end of the item, pages that are not in the pool, pages of 8 tokens
+        auto page_of = [&](int token, bool& there) {
+          const uint32_t x = token < left ? table[(slot + token) >> P.page_shift] : pages;
+          if (x >= pages && token < left) set_status(P.L.status, SPEC_TREE_S_PAGES);
+          there = x < pages;
+          return there ? x : 0u;
+        };
+#pragma unroll
+        for (int i = 0; i < 2 * STEPS; ++i) {
+          bool there;
+          const uint64_t from_page = page_of(token0 + i * TOKENS, there) * P.page_bytes;
+          const uint32_t to = skip + i * TOKENS * (D / 2), entry = (slot + token0 + i * TOKENS) & mask;
+          const uint8_t* from = key_at + from_page + (static_cast<int64_t>(entry) - token0) * P.token_bytes;
+          copy16_or_zeros(to_key + to, from, there);
+          copy16_or_zeros(to_value + to, from + P.to_values, there);
+        }
+        if (lane < CHUNK / 2) {
+          bool there;
+          const uint64_t from_page = page_of(2 * lane, there) * P.scale_page_bytes;
+          const int64_t entry = (slot + 2 * lane) & mask;
+          copy16_or_zeros(ring_at + skip + 2 * F::CODE_BYTES + lane * 16,
+                          scale_at + from_page + entry * 8 - lane % (BLOCK / 2) * 16, there);
+        }
       }
-      if (lane < CHUNK / 2) {
-        const int token = 2 * lane;
-        const bool second = lane >= CHUNK / 4, there = (second ? ok[1] : ok[0]) && token < left;
-        copy16(smem_u32(ring) + skip + 2 * F::CODE_BYTES + lane * 16,
-               scale_at + (there ? (second ? page[1] : page[0]) : 0) * scale_page + (small_pages ? token % 8 : entry + token) * 8, there);
-      }
-      if (++tile >= ahead.s.last) {
-        more = ahead.next(P);
-        tile = ahead.s.first;
+      ahead.tile += SIDES;
+      if (!ahead.more()) {
+        ahead.settle(P, side);
         enter();
       }
       look_up();
@@ -271,8 +334,10 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
     float acc[NT][MT][4];               // outputs of elements x rows
     float sum[NT][2], middle[NT][2];    // of this lane's tokens: weights, weights times zeros
     float sub[NT][2], fit[NT][2];       // weights' reference; the power of two that goes with the values' scales
+    float most[NT];                     // what a scale may be without a change of these
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      most[nt] = 128.0f / power2(107);
 #pragma unroll
       for (int e = 0; e < 2; ++e) sum[nt][e] = middle[nt][e] = 0.0f, sub[nt][e] = -INFINITY, fit[nt][e] = power2(107);
 #pragma unroll
@@ -283,47 +348,48 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
 
     auto chunk = [&](auto is_masked, const uint8_t* at, int slot) {
       constexpr bool MASKED = decltype(is_masked)::value;
-      // scales and zeros of tokens g and g + 8
-      float ks[2], kz[2], vs[2], vz[2];
+      // scales and zeros of tokens g and g + 8 of both blocks
+      float ks[4], kz[4], vs[4], vz[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 4; ++h) {
         const uint2 w = *reinterpret_cast<const uint2*>(at + 2 * F::CODE_BYTES + (g + 8 * h) * 8);
         const float2 a = Pair<T>::unpack(w.x), b = Pair<T>::unpack(w.y);
         ks[h] = a.x * scale_q, kz[h] = a.y, vs[h] = b.x, vz[h] = b.y;
       }
       float dot[NT][2][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dot[nt][0][e] = dot[nt][1][e] = 0.0f;
-      {
+      for (int u = 0; u < 2; ++u) {
         uint32_t a[KEY_WORDS], b[KEY_WORDS];
-        lds<KEY_WORDS>(a, at + g * (D / 2) + t * (4 * KEY_WORDS));
-        lds<KEY_WORDS>(b, at + (g + 8) * (D / 2) + t * (4 * KEY_WORDS));
+        lds<KEY_WORDS>(a, at + (u * BLOCK + g) * (D / 2) + t * (4 * KEY_WORDS));
+        lds<KEY_WORDS>(b, at + (u * BLOCK + g + 8) * (D / 2) + t * (4 * KEY_WORDS));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dot[nt][u][e] = 0.0f;
 #pragma unroll
         for (int w = 0; w < KEY_WORDS; ++w) {
           const uint32_t a8 = a[w] >> 8, b8 = b[w] >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma16816(dot[nt][0], a[w] & LOW, b[w] & LOW, a[w] & NEXT, b[w] & NEXT, q[nt][2 * w][0], q[nt][2 * w][1]);
-            mma16816(dot[nt][1], a8 & LOW, b8 & LOW, a8 & NEXT, b8 & NEXT, q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
+            mma16816(dot[nt][u], a[w] & LOW, b[w] & LOW, a[w] & NEXT, b[w] & NEXT, q[nt][2 * w][0], q[nt][2 * w][1]);
+            mma16816(dot[nt][u], a8 & LOW, b8 & LOW, a8 & NEXT, b8 & NEXT, q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
           }
         }
       }
-      uint32_t p[NT][2];  // the weights times scales, rows in the lanes
+      uint32_t p[NT][4];  // the weights times scales, rows in the lanes
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        // x[2 h + e]: token g + 8 h, row 2 t + e
-        float x[4];
-        bool seen[4];
+        // x[h][e]: token g + 8 h, row 2 t + e
+        float x[4][2];
+        bool seen[4][2];
         auto score = [&](int h, int e, float less) {
-          return fmaf(ks[h], dot[nt][0][2 * h + e] + dot[nt][1][2 * h + e], fmaf(kz[h], sum_q[nt][e], -less));
+          return fmaf(ks[h], dot[nt][h / 2][h % 2 * 2 + e], fmaf(kz[h], sum_q[nt][e], -less));
         };
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 4; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            x[2 * h + e] = score(h, e, sub[nt][e]);  // infinity where there is no reference yet
+            x[h][e] = score(h, e, sub[nt][e]);  // infinity where there is no reference yet
             if (MASKED) {
               const int off = slot + g + 8 * h - s.len;
               bool see = off < 0;
@@ -333,98 +399,116 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
                 else
                   see = off <= P.L.nodes.begin + node[nt][e];
               }
-              if (!see) x[2 * h + e] = -INFINITY;
-              seen[2 * h + e] = see;
+              if (!see) x[h][e] = -INFINITY;
+              seen[h][e] = see;
             }
           }
-        if (__any_sync(FULL, max3(x[0], x[1], fmaxf(x[2], x[3])) > LAZY)) {
+        const float top_x = max3(max3(x[0][0], x[0][1], x[1][0]), max3(x[1][1], x[2][0], x[2][1]), fmaxf(x[3][0], x[3][1]));
+        float top_s = max3(vs[0], vs[1], fmaxf(vs[2], vs[3]));
+        if (MASKED) {
+          top_s = 0.0f;
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            if (seen[h][0] || seen[h][1]) top_s = fmaxf(top_s, vs[h]);
+        }
+        if (__any_sync(FULL, top_x > LAZY || top_s > most[nt])) {
+          most[nt] = INFINITY;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const bool fresh = sub[nt][e] == -INFINITY;
-            if (fresh) {
+            float top = -INFINITY, larger = 0.0f;
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (!MASKED || seen[2 * h + e]) x[2 * h + e] = score(h, e, 0.0f);
+            for (int h = 0; h < 4; ++h) {
+              if (MASKED && !seen[h][e]) continue;
+              if (fresh) x[h][e] = score(h, e, 0.0f);
+              top = fmaxf(top, x[h][e]);
+              larger = fmaxf(larger, vs[h]);
             }
-            float top = fmaxf(x[e], x[2 + e]);
 #pragma unroll
-            for (int o = 4; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+            for (int o = 4; o < 32; o *= 2) {
+              top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+              larger = fmaxf(larger, __shfl_xor_sync(FULL, larger, o));
+            }
+            float f = 1.0f;
             if (fresh ? top > -INFINITY : top > LAZY) {
-              const float f = fresh ? 0.0f : ex2(-top);
+              f = fresh ? 0.0f : ex2(-top);
               sub[nt][e] = fresh ? top : sub[nt][e] + top;
-              x[e] -= top, x[2 + e] -= top;
+#pragma unroll
+              for (int h = 0; h < 4; ++h) x[h][e] -= top;
               sum[nt][e] *= f, middle[nt][e] *= f;
-#pragma unroll
-              for (int m = 0; m < MT; ++m) acc[nt][m][e] *= f, acc[nt][m][2 + e] *= f;
             }
-          }
-        }
-        float w[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float y = ex2(x[2 * h + e]);
-            // what is not seen may hold anything
-            const bool skip = MASKED && !seen[2 * h + e];
-            sum[nt][e] += y;
-            if (!skip) middle[nt][e] = fmaf(y, vz[h], middle[nt][e]);
-            w[2 * h + e] = skip ? 0.0f : y * fit[nt][e] * vs[h];
-          }
-        if (__any_sync(FULL, max3(w[0], w[1], fmaxf(w[2], w[3])) > 32768.0f)) {
-          // larger scales than before: at most 2^7 after this, weights at most 2^8
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = 0.0f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (!MASKED || seen[2 * h + e]) top = fmaxf(top, vs[h]);
-#pragma unroll
-            for (int o = 4; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-            const float next = fminf(fit[nt][e], power2(7 - exponent_above(top)));
-            const float f = next / fit[nt][e];
-            fit[nt][e] = next;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              w[2 * h + e] = MASKED && !seen[2 * h + e] ? 0.0f : ex2(x[2 * h + e]) * next * vs[h];
+            // values' scales go up to 2^7, so weights times scales up to 2^15
+            if (larger * fit[nt][e] > 128.0f) {
+              const float next = power2(7 - exponent_above(larger));
+              f *= next / fit[nt][e];
+              fit[nt][e] = next;
+            }
+            most[nt] = fminf(most[nt], 128.0f / fit[nt][e]);
 #pragma unroll
             for (int m = 0; m < MT; ++m) acc[nt][m][e] *= f, acc[nt][m][2 + e] *= f;
           }
         }
-        p[nt][0] = transposed(Pair<__half>::pack(w[0], w[1]));
-        p[nt][1] = transposed(Pair<__half>::pack(w[2], w[3]));
-      }
-      // values: lane (g, t) has elements D / 8 g on of tokens 2 t, 2 t + 1, 2 t + 8 and 2 t + 9
-      uint32_t v[4][VALUE_WORDS];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int row = (x & 2) * 4 + (x & 1) * 4 + t;
-        const int turn = D == 128 ? ((row >> 1) & 1) << 1 : 0;
-        lds<VALUE_WORDS>(v[x], at + F::CODE_BYTES + row * (D / 2) + (D == 128 ? (((g >> 1) ^ turn) * 16 + (g & 1) * 8) : g * 4));
-      }
-      uint32_t a[MT][4];  // two rows of each product, two pairs of tokens
+        for (int h = 0; h < 4; ++h) {
+          float w[2];
 #pragma unroll
-      for (int w = 0; w < VALUE_WORDS; ++w)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t lo = __byte_perm(v[2 * h][w], v[2 * h + 1][w], 0x5410), hi = __byte_perm(v[2 * h][w], v[2 * h + 1][w], 0x7632);
-          // word w of two, elements 0 .. 7: row g + 8 w of products 0 .. 7; of one word, elements 0 .. 3 and 4 .. 7: rows g, g + 8
-          const int r = 2 * h + w, r2 = VALUE_WORDS == 2 ? r : 2 * h + 1, up = VALUE_WORDS == 2 ? 4 : 0;
-          a[0][r] = lo & LOW, a[1][r] = lo & NEXT, a[2][r] = (lo >> 8) & LOW, a[3][r] = (lo >> 8) & NEXT;
-          a[up][r2] = hi & LOW, a[up + 1][r2] = hi & NEXT, a[up + 2][r2] = (hi >> 8) & LOW, a[up + 3][r2] = (hi >> 8) & NEXT;
+          for (int e = 0; e < 2; ++e) {
+            const float y = ex2(x[h][e]);
+            // what is not seen may hold anything
+            const bool skip = MASKED && !seen[h][e];
+            sum[nt][e] += y;
+            if (!skip) middle[nt][e] = fmaf(y, vz[h], middle[nt][e]);
+            w[e] = skip ? 0.0f : y * fit[nt][e] * vs[h];
+          }
+          p[nt][h] = transposed(Pair<__half>::pack(w[0], w[1]));
         }
+      }
+      // values: lane (g, t) has elements D / 8 g on of tokens 2 t, 2 t + 1, 2 t + 8 and 2 t + 9 of each block
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int u = 0; u < 2; ++u) {
+        uint32_t v[4][VALUE_WORDS];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) mma16816(acc[nt][m], a[m][0], a[m][1], a[m][2], a[m][3], p[nt][0], p[nt][1]);
+        for (int x = 0; x < 4; ++x) {
+          const int row = (x & 2) * 4 + (x & 1) * 4 + t;
+          const int turn = D == 128 ? ((row >> 1) & 1) << 1 : 0;
+          lds<VALUE_WORDS>(v[x], at + F::CODE_BYTES + (u * BLOCK + row) * (D / 2) +
+                                     (D == 128 ? (((g >> 1) ^ turn) * 16 + (g & 1) * 8) : g * 4));
+        }
+        // pairs of tokens: elements 0 to 3 and 4 to 7 of a word
+        uint32_t lo[VALUE_WORDS][2], hi[VALUE_WORDS][2];
+#pragma unroll
+        for (int w = 0; w < VALUE_WORDS; ++w)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            lo[w][h] = __byte_perm(v[2 * h][w], v[2 * h + 1][w], 0x5410);
+            hi[w][h] = __byte_perm(v[2 * h][w], v[2 * h + 1][w], 0x7632);
+          }
+        // rows g and g + 8 of four products: of two words the first and the second, of one its halves
+        auto four = [&](int m, const uint32_t (&a)[2], const uint32_t (&b)[2]) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t p0 = p[nt][2 * u], p1 = p[nt][2 * u + 1];
+            mma16816(acc[nt][m], a[0] & LOW, b[0] & LOW, a[1] & LOW, b[1] & LOW, p0, p1);
+            mma16816(acc[nt][m + 1], a[0] & NEXT, b[0] & NEXT, a[1] & NEXT, b[1] & NEXT, p0, p1);
+            mma16816(acc[nt][m + 2], (a[0] >> 8) & LOW, (b[0] >> 8) & LOW, (a[1] >> 8) & LOW, (b[1] >> 8) & LOW, p0, p1);
+            mma16816(acc[nt][m + 3], (a[0] >> 8) & NEXT, (b[0] >> 8) & NEXT, (a[1] >> 8) & NEXT, (b[1] >> 8) & NEXT, p0, p1);
+          }
+        };
+        if (VALUE_WORDS == 2) {
+          four(0, lo[0], lo[VALUE_WORDS - 1]);
+          four(MT - 4, hi[0], hi[VALUE_WORDS - 1]);
+        } else {
+          four(0, lo[0], hi[0]);
+        }
+      }
     };
 
-    for (int j = s.first; j < s.last; ++j) {
+    for (int j = s.first + side; j < s.last; j += SIDES) {
       copies_wait<F::STAGES - 2>();
       __syncwarp();
       load(stage == 0 ? F::STAGES - 1 : stage - 1);  // the warp is done with the stage before
       const uint8_t* at = ring + stage * F::STAGE_BYTES;
-      const int slot = j * TILE + warp * CHUNK;
+      const int slot = j * TILE + place;
       if (slot + CHUNK <= s.clear && slot + CHUNK <= s.end)
         chunk(std::false_type(), at, slot);
       else if (slot < s.end)
@@ -524,7 +608,7 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
 }
 
 template <typename T, int D, int NT>
-cudaError_t attend(Plan& P, cudaStream_t stream) {
+cudaError_t attend(FewPlan& P, cudaStream_t stream) {
   using F = Few<D, NT>;
   constexpr int SMEM = F::RING_BYTES + static_cast<int>(sizeof(FewShared<D, NT>));
   static_assert(F::CTAS * (SMEM + 1024) <= 233472, "shared memory of an SM");
@@ -536,14 +620,19 @@ cudaError_t attend(Plan& P, cudaStream_t stream) {
 }
 
 template <typename T, int D>
-cudaError_t attend_rows(Plan& P, cudaStream_t stream) {
+cudaError_t attend_rows(FewPlan& P, cudaStream_t stream) {
   return P.rows <= 8 ? attend<T, D, 1>(P, stream) : attend<T, D, 2>(P, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_attend_few(const AttendLaunch& L, cudaStream_t stream) {
-  Plan P = plan_of(L);
+  FewPlan P;
+  static_cast<Plan&>(P) = plan_of(L);
+  P.token_bytes = L.kv.token_stride / 2;
+  P.page_bytes = L.kv.page_stride / 2;
+  P.scale_page_bytes = L.scales.page_stride * 2;
+  P.to_values = static_cast<const uint8_t*>(L.kv.v) - static_cast<const uint8_t*>(L.kv.k);
   P.row_tiles = 1;
   P.ws_rows = P.rows;
   if (L.kv.dtype == SPEC_TREE_BF16)
