@@ -1,115 +1,312 @@
 // Attention of a tree's nodes over a key-value cache in 4 bits
-// (spec_tree_kv4_attend): one CTA per row, its warps over the tokens.
-#include <math.h>
+// (spec_tree_kv4_attend), for calls of more rows than attend4_few.cu takes: six
+// warps unpack codes into the tiles that the products take, rounded to the model's
+// type, and the rest is as over a cache of 16 bits.
+//
+// A code becomes n - 8 and then s (n - 8) + (z + 8 s) in packed arithmetic: n - 8 is
+// exact, and with the middle z + 8 s, which is small, nearly all of the rounding is
+// that of the result.
+namespace st {
+namespace {
+constexpr bool CODES = true;
+}
+}  // namespace st
 
-#include "st_kernels.h"
-#include "st_kv.cuh"
+#include <algorithm>
+
+#include "st_attend_tile.cuh"
 
 namespace st {
 namespace {
 
-constexpr int THREADS = 128, WARPS = THREADS / 32;
+constexpr int UNIT = 16;                 // tokens that a warp unpacks at a time
+constexpr int UNITS = 2 * TILE / UNIT;   // of a tile: of keys first, then of values
+constexpr int UNPACKERS = 6;             // warps; no more than a tile has units of keys, so that each sees every tile
+constexpr int AHEAD = 4;                 // units of a warp in its ring
+static_assert(UNPACKERS <= UNITS / 2, "a warp that does not see a tile may miss two phases of its barriers");
 
-template <typename T, int D>
-__global__ void __launch_bounds__(THREADS) attend4_row_kernel(const AttendLaunch L, int page_shift) {
-  constexpr int E = D / 32;
-  __shared__ uint8_t seen[SPEC_TREE_MAX_NODES];
-  __shared__ float tops[WARPS], sums[WARPS], outs[WARPS][D];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+template <int D>
+struct Raw {
+  static constexpr int CODE_BYTES = UNIT * D / 2;
+  static constexpr int PAIRS = CODE_BYTES;             // scale and zero of each token
+  static constexpr int NOTE = PAIRS + UNIT * 4;        // where C.odd has the unit's tokens, -1: nowhere
+  static constexpr int BYTES = NOTE + 16;
+};
+
+__device__ __forceinline__ void copy_to_shared(uint32_t to, const void* from, bool there) {  // 16 bytes, or zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void copy4_to_shared(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
+}
+
+// Eight codes as s (n - 8) + m, in their order: byte k holds the k-th pair.
+__device__ __forceinline__ uint4 unpacked(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 m) {
+  const __nv_bfloat162 middle = __float2bfloat162_rn(-136.0f);
+  const uint32_t up = w >> 4;
+  uint32_t y[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {  // 128 + n
+    const uint32_t two = (__byte_perm(w, up, k | (4 + k) << 8) & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 x = __hfma2(__hadd2(Pair<__nv_bfloat16>::pair(two), middle), s, m);
+    y[k] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+__device__ __forceinline__ uint4 unpacked(uint32_t w, __half2 s, __half2 m) {
+  const __half2 one = __floats2half2_rn(1.0f, 0.0625f), middle = __floats2half2_rn(-1032.0f, -72.0f);
+  uint32_t y[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {  // 1024 + n, 1024 + 16 n
+    const uint32_t two = (__byte_perm(w, w, k | k << 8) & 0x00f0000fu) | 0x64006400u;
+    const __half2 x = __hfma2(__hfma2(Pair<__half>::pair(two), one, middle), s, m);
+    y[k] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+__device__ __forceinline__ __nv_bfloat162 twice(__nv_bfloat16, float x) { return __float2bfloat162_rn(x); }
+__device__ __forceinline__ __half2 twice(__half, float x) { return __float2half2_rn(x); }
+
+// One of UNPACKERS warps: every UNPACKERS-th unit, its codes, scales and zeros into the
+// warp's own ring (AHEAD - 1 units ahead), from there unpacked into the tiles' rings.
+template <typename T, int D, bool PAIR>
+__device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* k_ring, uint8_t* v_ring, uint8_t* raw, int which) {
+  using Y = Layout<D, PAIR>;
+  using R = Raw<D>;
+  constexpr int LANES = D / 32;       // for a token's codes
+  constexpr int TOKENS = 32 / LANES;  // of one step of loads
+  const spec_tree_kv_t& kv = P.L.kv;
+  const int lane = threadIdx.x % 32, token = lane / LANES, c = lane % LANES;
+  const uint64_t token_bytes = kv.token_stride / 2, page_bytes = kv.page_stride / 2, scale_page_bytes = P.L.scales.page_stride * 2;
+  const uint32_t mask = kv.page_size - 1;
+  raw += which * AHEAD * R::BYTES;
+  uint32_t* status = P.L.status;
+
+  // ---- loads
+  Walk<Y::HALVES> walk(C);
+  const Segment& s = walk.s;
+  uint32_t before = 0, segment = 0;  // tiles of the segments before, segments
+  bool more = walk.next(P);
+  uint32_t ask = which;  // the unit to load next
+  int page[2] = {-1, -1};  // of its first and last 8 tokens
+  auto tile_of = [&](uint32_t unit) { return s.first + static_cast<int>(unit / UNITS - before); };
+  auto look_up = [&] {  // on to the segment of `ask`, and its pages
+    while (more && tile_of(ask) >= s.last) {
+      before += s.last - s.first;
+      more = walk.next(P);
+      ++segment;
+    }
+    page[0] = page[1] = -1;
+    if (!more) return;
+    const int slot = tile_of(ask) * TILE + static_cast<int>(ask % (UNITS / 2)) * UNIT;
+    const int32_t* table = kv.page_table + static_cast<int64_t>(s.b) * kv.table_stride;
+    if (slot < s.end) page[0] = page[1] = table[slot >> P.page_shift];
+    if (kv.page_size < UNIT) page[1] = slot + 8 < s.end ? table[(slot + 8) >> P.page_shift] : -1;
+  };
+  look_up();
+  auto load = [&](int place) {
+    if (more) {
+      const int tile = tile_of(ask), slot = tile * TILE + static_cast<int>(ask % (UNITS / 2)) * UNIT, left = s.end - slot;
+      const bool value = ask % UNITS >= UNITS / 2;
+      const bool ok[2] = {page[0] >= 0 && page[0] < kv.n_pages, page[1] >= 0 && page[1] < kv.n_pages};
+      if ((!ok[0] && left > 0) || (!ok[1] && left > 8)) set_status(status, SPEC_TREE_S_PAGES);
+      const uint32_t to = smem_u32(raw + place * R::BYTES);
+      const uint8_t* codes = static_cast<const uint8_t*>(value ? kv.v : kv.k) +
+                             (P.L.layer * kv.layer_stride + s.head * kv.head_stride) / 2 + c * 16;
+#pragma unroll
+      for (int i = 0; i < UNIT / TOKENS; ++i) {
+        const int x = i * TOKENS + token, h = x / 8;
+        const bool there = (h ? ok[1] : ok[0]) && x < left;
+        copy_to_shared(to + lane * 16 + i * 512, codes + static_cast<uint32_t>(there ? (h ? page[1] : page[0]) : 0) * page_bytes +
+                                                     ((slot + x) & mask) * token_bytes, there);
+      }
+      if (lane < UNIT) {
+        const int h = lane / 8;
+        const bool there = (h ? ok[1] : ok[0]) && lane < left;
+        copy4_to_shared(to + R::PAIRS + lane * 4,
+                        static_cast<const uint8_t*>(P.L.scales.data) +
+                            (P.L.layer * P.L.scales.layer_stride + s.head * P.L.scales.head_stride) * 2 +
+                            static_cast<uint32_t>(there ? (h ? page[1] : page[0]) : 0) * scale_page_bytes +
+                            ((slot + lane) & mask) * 8 + (value ? 4 : 0), there);
+      }
+      const int first_masked = s.clear / TILE;
+      if (lane == 0)
+        *reinterpret_cast<int*>(raw + place * R::BYTES + R::NOTE) =
+            value && tile >= first_masked
+                ? (static_cast<int>(segment % ODD_BUFFERS) * MASKED_TILES + tile - first_masked) * (TILE / UNIT) + static_cast<int>(ask % (UNITS / 2))
+                : -1;
+      ask += UNPACKERS;
+      look_up();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int i = 0; i < AHEAD - 1; ++i) load(i);
+
+  // ---- tiles
+  const uint32_t units = static_cast<uint32_t>(C.count) * UNITS;
+  uint16_t* odd = reinterpret_cast<uint16_t*>(C.odd[0]);
+  const int row_lane = lane / 2, half = lane % 2;
+  uint32_t place = 0;
+  for (uint32_t unit = which; unit < units; unit += UNPACKERS) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 2) : "memory");
+    __syncwarp();
+    const uint32_t tile = unit / UNITS, group = unit % (UNITS / 2);
+    const bool value = unit % UNITS >= UNITS / 2;
+    const uint32_t slot = value ? tile % Y::VS : tile % Y::KS;
+    if (!warp_wait(value ? &C.v_empty[slot] : &C.k_empty[slot], ((value ? tile / Y::VS : tile / Y::KS) & 1) ^ 1, C, status)) break;
+    const uint8_t* from = raw + place * R::BYTES;
+    const float2 pair = Pair<T>::unpack(*reinterpret_cast<const uint32_t*>(from + R::PAIRS + row_lane * 4));
+    const int note = *reinterpret_cast<const int*>(from + R::NOTE);
+    float scale = pair.x, zero = pair.y;
+    if (note >= 0) {
+      // values that some rows do not see: those that are not finite become zeros and are noted
+      const bool bad = !isfinite(scale) || !isfinite(zero);
+      const uint32_t word = __ballot_sync(FULL, bad && half == 0);
+      if (bad) scale = zero = 0.0f;
+      uint32_t bits = 0;
+      if (__builtin_expect(word, 0)) {
+#pragma unroll
+        for (int x = 0; x < UNIT; ++x) bits |= ((word >> (2 * x)) & 1) << x;
+      }
+      if (lane == 0) odd[note] = static_cast<uint16_t>(bits);
+    }
+    const auto s2 = twice(T(), scale), m2 = twice(T(), fmaf(8.0f, scale, zero));
+    const int row = group * UNIT + row_lane;
+    uint8_t* to = (value ? v_ring : k_ring) + slot * Y::KV_BYTES + row * 128;
+    auto four = [&](const uint4 w, uint8_t* at, int chunk) {  // 32 codes, four pieces of 16 bytes
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(at + (((chunk + i) ^ (row % 8)) << 4)) = unpacked(x[i], s2, m2);
+    };
+    if (D == 128) {
+      // a lane has a panel's 64 elements of its token; neighbours begin at different halves, for the banks' sake
+      const uint8_t* codes = from + row_lane * 64 + half * 32;
+      const uint4 a = *reinterpret_cast<const uint4*>(codes + half * 16), b = *reinterpret_cast<const uint4*>(codes + (1 - half) * 16);
+      four(a, to + half * PANEL_BYTES, 4 * half);
+      four(b, to + half * PANEL_BYTES, 4 * (1 - half));
+    } else {
+      four(*reinterpret_cast<const uint4*>(from + row_lane * 32 + half * 16), to, 4 * half);
+    }
+    fence_proxy_async_smem();
+    warp_arrive(value ? &C.v_full[slot] : &C.k_full[slot]);
+    load(place == 0 ? AHEAD - 1 : place - 1);  // the unit before this one has been unpacked
+    place = place + 1 == AHEAD ? 0 : place + 1;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <typename T, int D, bool PAIR>
+__global__ void __launch_bounds__(THREADS, 1) attend4_kernel(const __grid_constant__ Plan P, const __grid_constant__ CUtensorMap mq) {
+  using Y = Layout<D, PAIR>;
+  extern __shared__ __align__(1024) uint8_t smem[];  // nothing static, so it starts on a swizzle group
+  uint8_t* k_ring = smem + Y::Q_BYTES;
+  uint8_t* v_ring = k_ring + Y::KS * Y::KV_BYTES;
+  uint8_t* raw = v_ring + Y::VS * Y::KV_BYTES;
+  Control& C = *reinterpret_cast<Control*>(raw + UNPACKERS * AHEAD * Raw<D>::BYTES);
+  const int warp = __shfl_sync(FULL, threadIdx.x / 32, 0), cta = blockIdx.x;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < MAX_SLOTS; ++i) {
+      mbar_init(&C.k_full[i], UNITS / 2);
+      mbar_init(&C.k_empty[i], 1);
+      mbar_init(&C.v_full[i], UNITS / 2);
+      mbar_init(&C.v_empty[i], 1);
+    }
+    mbar_init(&C.q_full, 1);
+    mbar_init(&C.q_empty, 1);
+    mbar_init(&C.drain, 1);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&C.s_full[h], 1);
+      mbar_init(&C.w_full[h][0], 4);
+      mbar_init(&C.w_full[h][1], 4);
+      mbar_init(&C.o_full[h], 1);
+    }
+    C.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == HELPERS) tmem_alloc(&C.tmem, COLUMNS);
+  if (threadIdx.x == THREADS - 1) prefetch_map(&mq);
   grid_dependency_wait();
   grid_dependents_launch();
-  const int head = blockIdx.x % L.n_q_heads, rest = blockIdx.x / L.n_q_heads;
-  const int i = rest % L.nodes.count, b = rest / L.nodes.count, n = L.nodes.begin + i;
-  const int kv_head = head / (L.n_q_heads / L.kv.n_kv_heads);
-  T* out = static_cast<T*>(L.out.data) + b * L.out.tree_stride + i * L.out.node_stride + head * L.out.head_stride;
-  int len = L.kv.seq_len[b], cnt = node_count(L.nodes, b);
-  const bool past = static_cast<int64_t>(len) + cnt > (static_cast<int64_t>(L.kv.max_pages) << page_shift);
-  if (len < 0 || past) {
-    if (threadIdx.x == 0) set_status(L.status, len < 0 ? SPEC_TREE_S_NODES : SPEC_TREE_S_PAGES);
-    cnt = 0;
-  }
-  if (n >= cnt) {
-    if (threadIdx.x < D) out[threadIdx.x] = T(0.0f);
-    return;
-  }
-  const int32_t* parent = L.nodes.parent ? L.nodes.parent + static_cast<int64_t>(b) * L.nodes.stride : nullptr;
-  if (parent) {
-    for (int x = threadIdx.x; x < SPEC_TREE_MAX_NODES; x += THREADS) seen[x] = 0;
-    __syncthreads();
-    if (threadIdx.x == 0)
-      for (int at = n; at >= 0;) {
-        seen[at] = 1;
-        const int up = parent[at];
-        if (up >= at) set_status(L.status, SPEC_TREE_S_NODES);
-        at = up < at ? up : -1;
-      }
-    __syncthreads();
-  }
-  const T* q = static_cast<const T*>(L.q.data) + b * L.q.tree_stride + i * L.q.node_stride + head * L.q.head_stride;
-  float x[E], o[E], top = -INFINITY, sum = 0.0f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = static_cast<float>(q[lane * E + e]), o[e] = 0.0f;
-  for (int t = warp; t <= len + n; t += WARPS) {
-    if (parent && t >= len && !seen[t - len]) continue;
-    const int64_t off = kv_slot_offset(L.kv, b, t, page_shift);
-    if (off < 0 && lane == 0) set_status(L.status, SPEC_TREE_S_PAGES);
-    uint32_t k = 0, v = 0;
-    float2 ks = make_float2(0.0f, 0.0f), vs = ks;
-    if (off >= 0) {
-      const int64_t at = (L.layer * L.kv.layer_stride + off + kv_head * L.kv.head_stride + lane * E) / 2;
-      const uint8_t* kb = static_cast<const uint8_t*>(L.kv.k) + at;
-      const uint8_t* vb = static_cast<const uint8_t*>(L.kv.v) + at;
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) k |= kb[e] << (8 * e), v |= vb[e] << (8 * e);
-      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const T*>(L.scales.data) + L.layer * L.scales.layer_stride +
-                                                      kv_scale_offset(L.kv, L.scales, b, t, page_shift) +
-                                                      kv_head * L.scales.head_stride);
-      ks = Pair<T>::unpack(w.x), vs = Pair<T>::unpack(w.y);
+  if (!P.may_piece || !find_piece<Y::HALVES>(P, C, C.tiles, cta)) find_range<Y::HALVES>(P, C, warp, cta);
+  if (threadIdx.x == 0 && P.may_piece) workspace_of(P).records[cta].parts = 0;
+  if (cta == 0)
+    for (int b = threadIdx.x; b < P.L.B; b += THREADS) {
+      int len, cnt;
+      if (const uint32_t bad = tree_of(P, b, len, cnt)) set_status(P.L.status, bad);
     }
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(x[e], fmaf(static_cast<float>((k >> (4 * e)) & 15u), ks.x, ks.y), s);
-    s = warp_sum(s) * L.scale;
-    const float next = s > top ? s : top;
-    if (next == -INFINITY) {
-      if (isnan(s)) sum = NAN;
-      continue;
-    }
-    const float keep = expf(top - next), w = expf(s - next);
-    top = next;
-    sum = fmaf(sum, keep, w);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = fmaf(o[e], keep, w * fmaf(static_cast<float>((v >> (4 * e)) & 15u), vs.x, vs.y));
-  }
-  if (lane == 0) tops[warp] = top, sums[warp] = sum;
-#pragma unroll
-  for (int e = 0; e < E; ++e) outs[warp][lane * E + e] = o[e];
+  tmem_fence_before();
   __syncthreads();
-  if (threadIdx.x >= D) return;
-  float all = -INFINITY, total = 0.0f, y = 0.0f;
-  for (int w = 0; w < WARPS; ++w) all = fmaxf(all, tops[w]);
-  for (int w = 0; w < WARPS; ++w) {
-    const float f = tops[w] == -INFINITY ? 0.0f : expf(tops[w] - all);
-    total += isnan(sums[w]) ? sums[w] : sums[w] * f;
-    y += outs[w][threadIdx.x] * f;
+  tmem_fence_after();
+
+  if (warp < HELPERS) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
+    softmax_role<T, D, PAIR>(P, C, cta, static_cast<int>(min64(gridDim.x, C.total)), warp / 4);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(HELPER_REGS));
+    if (warp == HELPERS) {
+      product_role<T, D, PAIR>(P, C, smem_u32(smem), smem_u32(k_ring), smem_u32(v_ring));
+      // products in flight end before their memory is given back, also where it
+      // is the softmax that has given up and no longer waits for them
+      if (elect()) mma_commit(&C.drain);
+      __syncwarp();
+      mbar_wait(&C.drain, 0);
+    } else if (warp == HELPERS + 1) {
+      side_role<T, D, PAIR>(P, &mq, C, smem_u32(smem), v_ring);
+    } else {
+      unpack_role<T, D, PAIR>(P, C, k_ring, v_ring, raw, warp - HELPERS - 2);
+    }
   }
-  out[threadIdx.x] = T(total == 0.0f ? 0.0f : y / total);
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == HELPERS) {
+    tmem_fence_after();
+    tmem_free(C.tmem, COLUMNS);
+  }
+}
+
+// -------------------------------------------------------------------- host ---
+
+template <typename T, int D, bool PAIR>
+cudaError_t attend(Plan& P, cudaStream_t stream) {
+  using Y = Layout<D, PAIR>;
+  constexpr int SMEM = Y::Q_BYTES + (Y::KS + Y::VS) * Y::KV_BYTES + UNPACKERS * AHEAD * Raw<D>::BYTES + static_cast<int>(sizeof(Control));
+  static_assert(SMEM <= 232448, "shared memory of one CTA");
+  static_assert(2 * (TILE + D) <= COLUMNS, "tensor memory");
+  static_assert(THREADS == (HELPERS + 2 + UNPACKERS) * 32, "roles");
+  const int item_rows = Y::HALVES * P.half_rows;
+  P.row_tiles = (P.rows + item_rows - 1) / item_rows;
+  P.ws_rows = std::min(P.rows, item_rows);
+  const int64_t items = static_cast<int64_t>(P.L.B) * P.row_tiles;
+  P.may_piece = items * P.L.kv.n_kv_heads <= P.L.num_sms && items <= MAX_PIECE_ITEMS;
+  CUtensorMap mq;
+  if (!query_map(&mq, P)) return cudaErrorInvalidValue;
+  cudaError_t err = prepare_kernel<attend4_kernel<T, D, PAIR>>(SMEM, LAUNCH_REGS);
+  if (err != cudaSuccess) return err;
+  err = launch_pdl(attend4_kernel<T, D, PAIR>, dim3(P.L.num_sms), dim3(THREADS), SMEM, stream, P, mq);
+  if (err != cudaSuccess || !P.may_piece) return err;
+  return launch_pdl(attend_join_kernel<T, D>, dim3(P.L.num_sms, JOIN_SLICES), dim3(JOIN_THREADS), 0, stream, P);
 }
 
 template <typename T, int D>
-cudaError_t attend(const AttendLaunch& L, cudaStream_t stream) {
-  return launch_pdl(attend4_row_kernel<T, D>, dim3(L.B * L.nodes.count * L.n_q_heads), dim3(THREADS), 0, stream, L,
-                    log2_of(L.kv.page_size));
+cudaError_t attend_rows(Plan& P, cudaStream_t stream) {
+  return P.rows > P.half_rows ? attend<T, D, false>(P, stream) : attend<T, D, true>(P, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_attend(const AttendLaunch& L, cudaStream_t stream) {
-  if (L.nodes.count * (L.n_q_heads / L.kv.n_kv_heads) <= SPEC_TREE_KV4_FEW_ROWS) return launch_kv4_attend_few(L, stream);
+  Plan P = plan_of(L);
+  if (P.rows <= SPEC_TREE_KV4_FEW_ROWS) return launch_kv4_attend_few(L, stream);
+  P.q_box = std::min(TILE / P.group, L.nodes.count);
+  P.join_inside = false;
   if (L.kv.dtype == SPEC_TREE_BF16)
-    return L.kv.head_dim == 128 ? attend<__nv_bfloat16, 128>(L, stream) : attend<__nv_bfloat16, 64>(L, stream);
-  return L.kv.head_dim == 128 ? attend<__half, 128>(L, stream) : attend<__half, 64>(L, stream);
+    return L.kv.head_dim == 128 ? attend_rows<__nv_bfloat16, 128>(P, stream) : attend_rows<__nv_bfloat16, 64>(P, stream);
+  return L.kv.head_dim == 128 ? attend_rows<__half, 128>(P, stream) : attend_rows<__half, 64>(P, stream);
 }
 
 }  // namespace st

@@ -614,7 +614,7 @@ cudaError_t attend(FewPlan& P, cudaStream_t stream) {
   static_assert(F::CTAS * (SMEM + 1024) <= 233472, "shared memory of an SM");
   P.slots = F::CTAS * P.L.num_sms;
   P.may_piece = static_cast<int64_t>(P.L.B) * P.L.kv.n_kv_heads <= P.slots && P.L.B <= MAX_PIECE_ITEMS;
-  const cudaError_t err = prepare_smem<attend4_few_kernel<T, D, NT>>(SMEM);
+  const cudaError_t err = prepare_kernel<attend4_few_kernel<T, D, NT>>(SMEM, 0);
   if (err != cudaSuccess) return err;
   return launch_pdl(attend4_few_kernel<T, D, NT>, dim3(P.slots), dim3(THREADS), SMEM, stream, P);
 }

@@ -6,6 +6,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "st_kernels.h"
 #include "st_kv.cuh"
@@ -15,6 +16,7 @@ namespace st {
 namespace {
 
 constexpr int TILE = 128;             // tokens of a tile
+constexpr int PANEL = 64;             // 16-bit elements of a 128-byte row
 constexpr float LAZY = 8.0f;          // log2 of what a weight may exceed its reference by
 constexpr int MAX_PIECE_ITEMS = 256;  // (tree, rows) of calls that may be dealt in pieces
 constexpr int JOIN_PARTS = 4;         // parts of an item joined at a time
@@ -174,6 +176,12 @@ __device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
   uint32_t v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
+}
+
+// One arrival for a whole warp, after what all its lanes did before.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
 
 // A barrier of some of the CTA's warps (converged: .aligned instructions of a
@@ -486,20 +494,71 @@ inline Plan plan_of(const AttendLaunch& L) {
   return P;
 }
 
-// Tells the current device, once, how much shared memory the kernel takes.
+// Tells the current device, once, how much shared memory the kernel takes, and
+// looks whether it has as many registers a thread as it was written for.
 template <auto KERNEL>
-cudaError_t prepare_smem(int bytes) {
+cudaError_t prepare_kernel(int bytes, int registers) {
   static std::atomic<uint64_t> prepared{0};
   int device = 0;
   cudaError_t err = cudaGetDevice(&device);
   if (err != cudaSuccess) return err;
   const uint64_t bit = device < 64 ? 1ull << device : 0;
   if (!(prepared.load(std::memory_order_relaxed) & bit)) {
+    cudaFuncAttributes has;
+    if ((err = cudaFuncGetAttributes(&has, KERNEL)) != cudaSuccess) return err;
+    if (has.numRegs < registers) return cudaErrorLaunchOutOfResources;
     err = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err != cudaSuccess) return err;
     prepared.fetch_or(bit, std::memory_order_relaxed);
   }
   return cudaSuccess;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiled encode_tiled() {
+  static EncodeTiled fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult res;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &res) == cudaSuccess &&
+        res == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiled>(p);
+  });
+  return fn;
+}
+
+// Boxes of a 4-dimensional array whose elements have `size` bytes; strides in elements.
+struct Boxes {
+  cuuint32_t n[4];
+};
+
+inline bool tiled_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base, const cuuint64_t (&dims)[4],
+               const int64_t (&strides)[3], const Boxes& boxes, CUtensorMapSwizzle swizzle) {
+  const EncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return false;
+  cuuint64_t bytes[3];
+  for (int i = 0; i < 3; ++i)  // the stride of a single entry means nothing
+    bytes[i] = dims[i + 1] == 1 ? 16 : static_cast<cuuint64_t>(strides[i]) * size;
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  return fn(map, type, 4, const_cast<void*>(base), dims, bytes, boxes.n, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+inline CUtensorMapDataType type_of(int dtype) {
+  return dtype == SPEC_TREE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+[[maybe_unused]] // Queries, [tree][node][head][element]: one key head's heads of q_box nodes.
+inline bool query_map(CUtensorMap* map, const Plan& P) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(P.L.kv.head_dim), static_cast<cuuint64_t>(P.L.n_q_heads),
+                              static_cast<cuuint64_t>(P.L.nodes.count), static_cast<cuuint64_t>(P.L.B)};
+  const int64_t strides[3] = {P.L.q.head_stride, P.L.q.node_stride, P.L.q.tree_stride};
+  return tiled_map(map, type_of(P.L.kv.dtype), 2, P.L.q.data, dims, strides,
+                   {PANEL, static_cast<cuuint32_t>(P.group), static_cast<cuuint32_t>(P.q_box), 1}, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
