@@ -19,26 +19,27 @@ constexpr bool CODES = true;
 namespace st {
 namespace {
 
-constexpr int UNIT = 16;                 // tokens that a warp unpacks at a time
-constexpr int UNITS = 2 * TILE / UNIT;   // of a tile: of keys first, then of values
-constexpr int UNPACKERS = 6;             // warps; no more than a tile has units of keys, so that each sees every tile
-constexpr int AHEAD = 4;                 // units of a warp in its ring
-static_assert(UNPACKERS <= UNITS / 2, "a warp that does not see a tile may miss two phases of its barriers");
+constexpr int UNIT = 16;             // tokens whose keys and values a warp unpacks at a time
+constexpr int UNITS = TILE / UNIT;   // of a tile
+constexpr int UNPACKERS = 6;         // warps; no more than a tile has units, so that each sees every tile
+static_assert(UNPACKERS <= UNITS, "a warp that does not see a tile may miss two phases of its barriers");
 
-template <int D>
+template <int D, bool PAIR>
 struct Raw {
   static constexpr int CODE_BYTES = UNIT * D / 2;
-  static constexpr int PAIRS = CODE_BYTES;             // scale and zero of each token
-  static constexpr int NOTE = PAIRS + UNIT * 4;        // where C.odd has the unit's tokens, -1: nowhere
+  static constexpr int SCALES = 2 * CODE_BYTES;      // four numbers for each token
+  static constexpr int NOTE = SCALES + UNIT * 8;     // where C.odd has the unit's tokens, -1: nowhere
   static constexpr int BYTES = NOTE + 16;
+  static constexpr int AHEAD = D == 128 ? 2 : 4;     // units of a warp in its ring
+  static constexpr int RING = AHEAD * BYTES;
 };
 
 __device__ __forceinline__ void copy_to_shared(uint32_t to, const void* from, bool there) {  // 16 bytes, or zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
 
-__device__ __forceinline__ void copy4_to_shared(uint32_t to, const void* from, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
+__device__ __forceinline__ void copy8_to_shared(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(there ? 8 : 0) : "memory");
 }
 
 // Eight codes as s (n - 8) + m, in their order: byte k holds the k-th pair.
@@ -71,80 +72,85 @@ __device__ __forceinline__ __nv_bfloat162 twice(__nv_bfloat16, float x) { return
 __device__ __forceinline__ __half2 twice(__half, float x) { return __float2half2_rn(x); }
 
 // One of UNPACKERS warps: every UNPACKERS-th unit, its codes, scales and zeros into the
-// warp's own ring (AHEAD - 1 units ahead), from there unpacked into the tiles' rings.
+// warp's own ring while the one before is unpacked into the tiles' rings.
 template <typename T, int D, bool PAIR>
 __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* k_ring, uint8_t* v_ring, uint8_t* raw, int which) {
   using Y = Layout<D, PAIR>;
-  using R = Raw<D>;
+  using R = Raw<D, PAIR>;
   constexpr int LANES = D / 32;       // for a token's codes
   constexpr int TOKENS = 32 / LANES;  // of one step of loads
   const spec_tree_kv_t& kv = P.L.kv;
   const int lane = threadIdx.x % 32, token = lane / LANES, c = lane % LANES;
   const uint64_t token_bytes = kv.token_stride / 2, page_bytes = kv.page_stride / 2, scale_page_bytes = P.L.scales.page_stride * 2;
   const uint32_t mask = kv.page_size - 1;
-  raw += which * AHEAD * R::BYTES;
+  raw += which * R::RING;
   uint32_t* status = P.L.status;
 
   // ---- loads
   Walk<Y::HALVES> walk(C);
   const Segment& s = walk.s;
   uint32_t before = 0, segment = 0;  // tiles of the segments before, segments
+  uint32_t ask = which;              // the unit to load next
   bool more = walk.next(P);
-  uint32_t ask = which;  // the unit to load next
-  int page[2] = {-1, -1};  // of its first and last 8 tokens
-  auto tile_of = [&](uint32_t unit) { return s.first + static_cast<int>(unit / UNITS - before); };
+  int page[2] = {-1, -1};            // of its first and last 8 tokens
+  const int64_t to_values = static_cast<const uint8_t*>(kv.v) - static_cast<const uint8_t*>(kv.k);
+  const uint8_t *codes, *scales;     // of this lane's token, entry 0 of page 0 of the segment's head
+  const int32_t* table;
+  auto enter = [&] {
+    codes = static_cast<const uint8_t*>(kv.k) + (P.L.layer * kv.layer_stride + s.head * kv.head_stride) / 2 + c * 16;
+    scales = static_cast<const uint8_t*>(P.L.scales.data) +
+             (P.L.layer * P.L.scales.layer_stride + s.head * P.L.scales.head_stride) * 2;
+    table = kv.page_table + static_cast<int64_t>(s.b) * kv.table_stride;
+  };
+  auto slot_of = [&] { return (s.first + static_cast<int>(ask / UNITS - before)) * TILE + static_cast<int>(ask % UNITS) * UNIT; };
   auto look_up = [&] {  // on to the segment of `ask`, and its pages
-    while (more && tile_of(ask) >= s.last) {
+    while (more && slot_of() >= s.last * TILE) {
       before += s.last - s.first;
       more = walk.next(P);
       ++segment;
+      enter();
     }
     page[0] = page[1] = -1;
     if (!more) return;
-    const int slot = tile_of(ask) * TILE + static_cast<int>(ask % (UNITS / 2)) * UNIT;
-    const int32_t* table = kv.page_table + static_cast<int64_t>(s.b) * kv.table_stride;
+    const int slot = slot_of();
     if (slot < s.end) page[0] = page[1] = table[slot >> P.page_shift];
     if (kv.page_size < UNIT) page[1] = slot + 8 < s.end ? table[(slot + 8) >> P.page_shift] : -1;
   };
+  enter();
   look_up();
   auto load = [&](int place) {
     if (more) {
-      const int tile = tile_of(ask), slot = tile * TILE + static_cast<int>(ask % (UNITS / 2)) * UNIT, left = s.end - slot;
-      const bool value = ask % UNITS >= UNITS / 2;
+      const int slot = slot_of(), left = s.end - slot;
       const bool ok[2] = {page[0] >= 0 && page[0] < kv.n_pages, page[1] >= 0 && page[1] < kv.n_pages};
       if ((!ok[0] && left > 0) || (!ok[1] && left > 8)) set_status(status, SPEC_TREE_S_PAGES);
       const uint32_t to = smem_u32(raw + place * R::BYTES);
-      const uint8_t* codes = static_cast<const uint8_t*>(value ? kv.v : kv.k) +
-                             (P.L.layer * kv.layer_stride + s.head * kv.head_stride) / 2 + c * 16;
 #pragma unroll
       for (int i = 0; i < UNIT / TOKENS; ++i) {
         const int x = i * TOKENS + token, h = x / 8;
         const bool there = (h ? ok[1] : ok[0]) && x < left;
-        copy_to_shared(to + lane * 16 + i * 512, codes + static_cast<uint32_t>(there ? (h ? page[1] : page[0]) : 0) * page_bytes +
-                                                     ((slot + x) & mask) * token_bytes, there);
+        const uint8_t* from = codes + static_cast<uint32_t>(there ? (h ? page[1] : page[0]) : 0) * page_bytes +
+                              ((slot + x) & mask) * token_bytes;
+        copy_to_shared(to + lane * 16 + i * 512, from, there);
+        copy_to_shared(to + R::CODE_BYTES + lane * 16 + i * 512, from + to_values, there);
       }
       if (lane < UNIT) {
         const int h = lane / 8;
         const bool there = (h ? ok[1] : ok[0]) && lane < left;
-        copy4_to_shared(to + R::PAIRS + lane * 4,
-                        static_cast<const uint8_t*>(P.L.scales.data) +
-                            (P.L.layer * P.L.scales.layer_stride + s.head * P.L.scales.head_stride) * 2 +
-                            static_cast<uint32_t>(there ? (h ? page[1] : page[0]) : 0) * scale_page_bytes +
-                            ((slot + lane) & mask) * 8 + (value ? 4 : 0), there);
+        copy8_to_shared(to + R::SCALES + lane * 8,
+                        scales + static_cast<uint32_t>(there ? (h ? page[1] : page[0]) : 0) * scale_page_bytes + ((slot + lane) & mask) * 8,
+                        there);
       }
-      const int first_masked = s.clear / TILE;
+      const int note = slot / TILE - s.clear / TILE;
       if (lane == 0)
         *reinterpret_cast<int*>(raw + place * R::BYTES + R::NOTE) =
-            value && tile >= first_masked
-                ? (static_cast<int>(segment % ODD_BUFFERS) * MASKED_TILES + tile - first_masked) * (TILE / UNIT) + static_cast<int>(ask % (UNITS / 2))
-                : -1;
+            note >= 0 ? (static_cast<int>(segment % ODD_BUFFERS) * MASKED_TILES + note) * UNITS + static_cast<int>(ask % UNITS) : -1;
       ask += UNPACKERS;
       look_up();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll 1
-  for (int i = 0; i < AHEAD - 1; ++i) load(i);
+  for (int i = 0; i < R::AHEAD - 1; ++i) load(i);
 
   // ---- tiles
   const uint32_t units = static_cast<uint32_t>(C.count) * UNITS;
@@ -152,21 +158,46 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
   const int row_lane = lane / 2, half = lane % 2;
   uint32_t place = 0;
   for (uint32_t unit = which; unit < units; unit += UNPACKERS) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 2) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(R::AHEAD - 2) : "memory");
     __syncwarp();
-    const uint32_t tile = unit / UNITS, group = unit % (UNITS / 2);
-    const bool value = unit % UNITS >= UNITS / 2;
-    const uint32_t slot = value ? tile % Y::VS : tile % Y::KS;
-    if (!warp_wait(value ? &C.v_empty[slot] : &C.k_empty[slot], ((value ? tile / Y::VS : tile / Y::KS) & 1) ^ 1, C, status)) break;
+    load(place == 0 ? R::AHEAD - 1 : place - 1);  // the unit before this one has been unpacked
+    const uint32_t tile = unit / UNITS;
+    const int row = static_cast<int>(unit % UNITS) * UNIT + row_lane;
     const uint8_t* from = raw + place * R::BYTES;
-    const float2 pair = Pair<T>::unpack(*reinterpret_cast<const uint32_t*>(from + R::PAIRS + row_lane * 4));
+    const uint2 four = *reinterpret_cast<const uint2*>(from + R::SCALES + row_lane * 8);
     const int note = *reinterpret_cast<const int*>(from + R::NOTE);
-    float scale = pair.x, zero = pair.y;
+    // 16 tokens of the tile at `to`, from their codes at `at`; a lane has a half of its token's
+    auto unpack = [&](uint8_t* to, const uint8_t* at, float scale, float zero) {
+      const auto s2 = twice(T(), scale), m2 = twice(T(), fmaf(8.0f, scale, zero));
+      auto pieces = [&](const uint4 w, uint8_t* panel, int chunk) {  // 32 codes, four pieces of 16 bytes
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(panel + (((chunk + i) ^ (row % 8)) << 4)) = unpacked(x[i], s2, m2);
+      };
+      to += row * 128;
+      if (D == 128) {
+        // a panel's 64 elements; neighbours begin at different halves, for the banks' sake
+        at += row_lane * 64 + half * 32;
+        const uint4 a = *reinterpret_cast<const uint4*>(at + half * 16), b = *reinterpret_cast<const uint4*>(at + (1 - half) * 16);
+        pieces(a, to + half * PANEL_BYTES, 4 * half);
+        pieces(b, to + half * PANEL_BYTES, 4 * (1 - half));
+      } else {
+        pieces(*reinterpret_cast<const uint4*>(at + row_lane * 32 + half * 16), to, 4 * half);
+      }
+      fence_proxy_async_smem();
+    };
+    const uint32_t ks = tile % Y::KS, vs = tile % Y::VS;
+    if (!warp_wait(&C.k_empty[ks], ((tile / Y::KS) & 1) ^ 1, C, status)) break;
+    float2 pair = Pair<T>::unpack(four.x);
+    unpack(k_ring + ks * Y::KV_BYTES, from, pair.x, pair.y);
+    warp_arrive(&C.k_full[ks]);
+    pair = Pair<T>::unpack(four.y);
+    if (!warp_wait(&C.v_empty[vs], ((tile / Y::VS) & 1) ^ 1, C, status)) break;
     if (note >= 0) {
       // values that some rows do not see: those that are not finite become zeros and are noted
-      const bool bad = !isfinite(scale) || !isfinite(zero);
+      const bool bad = !isfinite(pair.x) || !isfinite(pair.y);
       const uint32_t word = __ballot_sync(FULL, bad && half == 0);
-      if (bad) scale = zero = 0.0f;
+      if (bad) pair.x = pair.y = 0.0f;
       uint32_t bits = 0;
       if (__builtin_expect(word, 0)) {
 #pragma unroll
@@ -174,27 +205,9 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
       }
       if (lane == 0) odd[note] = static_cast<uint16_t>(bits);
     }
-    const auto s2 = twice(T(), scale), m2 = twice(T(), fmaf(8.0f, scale, zero));
-    const int row = group * UNIT + row_lane;
-    uint8_t* to = (value ? v_ring : k_ring) + slot * Y::KV_BYTES + row * 128;
-    auto four = [&](const uint4 w, uint8_t* at, int chunk) {  // 32 codes, four pieces of 16 bytes
-      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(at + (((chunk + i) ^ (row % 8)) << 4)) = unpacked(x[i], s2, m2);
-    };
-    if (D == 128) {
-      // a lane has a panel's 64 elements of its token; neighbours begin at different halves, for the banks' sake
-      const uint8_t* codes = from + row_lane * 64 + half * 32;
-      const uint4 a = *reinterpret_cast<const uint4*>(codes + half * 16), b = *reinterpret_cast<const uint4*>(codes + (1 - half) * 16);
-      four(a, to + half * PANEL_BYTES, 4 * half);
-      four(b, to + half * PANEL_BYTES, 4 * (1 - half));
-    } else {
-      four(*reinterpret_cast<const uint4*>(from + row_lane * 32 + half * 16), to, 4 * half);
-    }
-    fence_proxy_async_smem();
-    warp_arrive(value ? &C.v_full[slot] : &C.k_full[slot]);
-    load(place == 0 ? AHEAD - 1 : place - 1);  // the unit before this one has been unpacked
-    place = place + 1 == AHEAD ? 0 : place + 1;
+    unpack(v_ring + vs * Y::KV_BYTES, from + R::CODE_BYTES, pair.x, pair.y);
+    warp_arrive(&C.v_full[vs]);
+    place = place + 1 == R::AHEAD ? 0 : place + 1;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -206,13 +219,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend4_kernel(const __grid_consta
   uint8_t* k_ring = smem + Y::Q_BYTES;
   uint8_t* v_ring = k_ring + Y::KS * Y::KV_BYTES;
   uint8_t* raw = v_ring + Y::VS * Y::KV_BYTES;
-  Control& C = *reinterpret_cast<Control*>(raw + UNPACKERS * AHEAD * Raw<D>::BYTES);
+  Control& C = *reinterpret_cast<Control*>(raw + UNPACKERS * Raw<D, PAIR>::RING);
   const int warp = __shfl_sync(FULL, threadIdx.x / 32, 0), cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < MAX_SLOTS; ++i) {
-      mbar_init(&C.k_full[i], UNITS / 2);
+      mbar_init(&C.k_full[i], UNITS);
       mbar_init(&C.k_empty[i], 1);
-      mbar_init(&C.v_full[i], UNITS / 2);
+      mbar_init(&C.v_full[i], UNITS);
       mbar_init(&C.v_empty[i], 1);
     }
     mbar_init(&C.q_full, 1);
@@ -274,7 +287,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend4_kernel(const __grid_consta
 template <typename T, int D, bool PAIR>
 cudaError_t attend(Plan& P, cudaStream_t stream) {
   using Y = Layout<D, PAIR>;
-  constexpr int SMEM = Y::Q_BYTES + (Y::KS + Y::VS) * Y::KV_BYTES + UNPACKERS * AHEAD * Raw<D>::BYTES + static_cast<int>(sizeof(Control));
+  constexpr int SMEM = Y::Q_BYTES + (Y::KS + Y::VS) * Y::KV_BYTES + UNPACKERS * Raw<D, PAIR>::RING + static_cast<int>(sizeof(Control));
   static_assert(SMEM <= 232448, "shared memory of one CTA");
   static_assert(2 * (TILE + D) <= COLUMNS, "tensor memory");
   static_assert(THREADS == (HELPERS + 2 + UNPACKERS) * 32, "roles");
