@@ -108,8 +108,9 @@ struct Layout {
   // tiles that the rings of keys and of values hold: what 7 * 32 KB leave, or 6 beside
   // the rings of codes
   static constexpr int SLOTS = ((CODES ? 6 : 7) * 32768 - Q_BYTES) / KV_BYTES;
-  static constexpr int KS = (SLOTS + 1) / 2 < MAX_SLOTS ? (SLOTS + 1) / 2 : MAX_SLOTS;
-  static constexpr int VS = SLOTS / 2 < MAX_SLOTS ? SLOTS / 2 : MAX_SLOTS;
+  static constexpr int MORE = (SLOTS + 1) / 2 < MAX_SLOTS ? (SLOTS + 1) / 2 : MAX_SLOTS;
+  static constexpr int LESS = SLOTS / 2 < MAX_SLOTS ? SLOTS / 2 : MAX_SLOTS;
+  static constexpr int KS = CODES ? LESS : MORE, VS = CODES ? MORE : LESS;
 };
 
 struct Control : Deal<THREADS / 32> {
