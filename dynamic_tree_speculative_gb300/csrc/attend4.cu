@@ -68,6 +68,32 @@ __device__ __forceinline__ uint4 unpacked(uint32_t w, __half2 s, __half2 m) {
   return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
+// The same in the order that takes fewest operations: codes j and j + 4 in word j (output_column).
+__device__ __forceinline__ uint4 unpacked_pairs(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 m) {
+  const __nv_bfloat162 middle = __float2bfloat162_rn(-136.0f);
+  uint32_t y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // 128 + n
+    const uint32_t two = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 x = __hfma2(__hadd2(Pair<__nv_bfloat16>::pair(two), middle), s, m);
+    y[j] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+__device__ __forceinline__ uint4 unpacked_pairs(uint32_t w, __half2 s, __half2 m) {
+  const __half2 low = __float2half2_rn(-1032.0f), next = __float2half2_rn(-72.0f), sixteenth = __float2half2_rn(0.0625f);
+  uint32_t y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // 1024 + n, or 1024 + 16 n
+    const uint32_t v = j < 2 ? w : w >> 8;
+    const __half2 two = Pair<__half>::pair((v & (j % 2 ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u);
+    const __half2 x = __hfma2(j % 2 ? __hfma2(two, sixteenth, next) : __hadd2(two, low), s, m);
+    y[j] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+
 __device__ __forceinline__ __nv_bfloat162 twice(__nv_bfloat16, float x) { return __float2bfloat162_rn(x); }
 __device__ __forceinline__ __half2 twice(__half, float x) { return __float2half2_rn(x); }
 
@@ -167,12 +193,14 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
     const uint2 four = *reinterpret_cast<const uint2*>(from + R::SCALES + row_lane * 8);
     const int note = *reinterpret_cast<const int*>(from + R::NOTE);
     // 16 tokens of the tile at `to`, from their codes at `at`; a lane has a half of its token's
-    auto unpack = [&](uint8_t* to, const uint8_t* at, float scale, float zero) {
+    auto unpack = [&](auto values, uint8_t* to, const uint8_t* at, float scale, float zero) {
       const auto s2 = twice(T(), scale), m2 = twice(T(), fmaf(8.0f, scale, zero));
       auto pieces = [&](const uint4 w, uint8_t* panel, int chunk) {  // 32 codes, four pieces of 16 bytes
         const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(panel + (((chunk + i) ^ (row % 8)) << 4)) = unpacked(x[i], s2, m2);
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(panel + (((chunk + i) ^ (row % 8)) << 4)) =
+              decltype(values)::value ? unpacked_pairs(x[i], s2, m2) : unpacked(x[i], s2, m2);
       };
       to += row * 128;
       if (D == 128) {
@@ -189,7 +217,7 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
     const uint32_t ks = tile % Y::KS, vs = tile % Y::VS;
     if (!warp_wait(&C.k_empty[ks], ((tile / Y::KS) & 1) ^ 1, C, status)) break;
     float2 pair = Pair<T>::unpack(four.x);
-    unpack(k_ring + ks * Y::KV_BYTES, from, pair.x, pair.y);
+    unpack(std::false_type(), k_ring + ks * Y::KV_BYTES, from, pair.x, pair.y);
     warp_arrive(&C.k_full[ks]);
     pair = Pair<T>::unpack(four.y);
     if (!warp_wait(&C.v_empty[vs], ((tile / Y::VS) & 1) ^ 1, C, status)) break;
@@ -205,7 +233,7 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
       }
       if (lane == 0) odd[note] = static_cast<uint16_t>(bits);
     }
-    unpack(v_ring + vs * Y::KV_BYTES, from + R::CODE_BYTES, pair.x, pair.y);
+    unpack(std::true_type(), v_ring + vs * Y::KV_BYTES, from + R::CODE_BYTES, pair.x, pair.y);
     warp_arrive(&C.v_full[vs]);
     place = place + 1 == R::AHEAD ? 0 : place + 1;
   }

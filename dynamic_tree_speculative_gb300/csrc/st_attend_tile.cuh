@@ -528,6 +528,12 @@ __device__ __noinline__ void settle(const Plan& P, const Segment& s, const uint3
   }
 }
 
+// The accumulator's column of element x (below 32): values made of codes come in
+// pairs of elements four apart, which costs nothing to undo here.
+__device__ __forceinline__ constexpr int output_column(int x) {
+  return CODES ? (x & ~7) + ((x & 3) << 1) + ((x >> 2) & 1) : x;
+}
+
 // Whether the row's node sees one of the tokens of the segment that `odd` names.
 __device__ __noinline__ bool sees_odd(const Plan& P, const Segment& s, const uint32_t* odd, int node) {
   const int first_masked = s.clear / TILE;
@@ -776,10 +782,10 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
             for (int q = 0; q < 8; ++q) y[q] = __ldcg(theirs + q * P.ws_rows);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-              o[q * 4] = __float_as_uint(fmaf(y[q].x, f, __uint_as_float(o[q * 4])));
-              o[q * 4 + 1] = __float_as_uint(fmaf(y[q].y, f, __uint_as_float(o[q * 4 + 1])));
-              o[q * 4 + 2] = __float_as_uint(fmaf(y[q].z, f, __uint_as_float(o[q * 4 + 2])));
-              o[q * 4 + 3] = __float_as_uint(fmaf(y[q].w, f, __uint_as_float(o[q * 4 + 3])));
+              o[output_column(q * 4)] = __float_as_uint(fmaf(y[q].x, f, __uint_as_float(o[output_column(q * 4)])));
+              o[output_column(q * 4 + 1)] = __float_as_uint(fmaf(y[q].y, f, __uint_as_float(o[output_column(q * 4 + 1)])));
+              o[output_column(q * 4 + 2)] = __float_as_uint(fmaf(y[q].z, f, __uint_as_float(o[output_column(q * 4 + 2)])));
+              o[output_column(q * 4 + 3)] = __float_as_uint(fmaf(y[q].w, f, __uint_as_float(o[output_column(q * 4 + 3)])));
             }
           }
         }
@@ -788,15 +794,15 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
           if (live) {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              partial[(c * 8 + q) * P.ws_rows] = make_float4(__uint_as_float(o[q * 4]), __uint_as_float(o[q * 4 + 1]),
-                                                             __uint_as_float(o[q * 4 + 2]), __uint_as_float(o[q * 4 + 3]));
+              partial[(c * 8 + q) * P.ws_rows] = make_float4(__uint_as_float(o[output_column(q * 4)]), __uint_as_float(o[output_column(q * 4 + 1)]),
+                                                             __uint_as_float(o[output_column(q * 4 + 2)]), __uint_as_float(o[output_column(q * 4 + 3)]));
           }
         } else if (in_call) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = some ? __uint_as_float(o[q * 8 + e]) * inv : 0.0f;
+            for (int e = 0; e < 8; ++e) y[e] = some ? __uint_as_float(o[output_column(q * 8 + e)]) * inv : 0.0f;
             *reinterpret_cast<uint4*>(out + c * 32 + q * 8) = pack8<T>(y);
           }
         }
