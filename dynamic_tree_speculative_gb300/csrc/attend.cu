@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp < HELPERS) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
-    softmax_role<T, D, PAIR>(P, C, cta, static_cast<int>(min64(gridDim.x, C.total)), warp / 4);
+    softmax_role<T, D, PAIR>(P, C, smem, cta, static_cast<int>(min64(gridDim.x, C.total)), warp / 4);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(HELPER_REGS));
     if (warp == HELPERS) {

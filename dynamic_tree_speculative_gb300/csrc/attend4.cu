@@ -1,11 +1,7 @@
 // Attention of a tree's nodes over a key-value cache in 4 bits
 // (spec_tree_kv4_attend), for calls of more rows than attend4_few.cu takes: six
-// warps unpack codes into the tiles that the products take, rounded to the model's
-// type, and the rest is as over a cache of 16 bits.
-//
-// A code becomes n - 8 and then s (n - 8) + (z + 8 s) in packed arithmetic: n - 8 is
-// exact, and with the middle z + 8 s, which is small, nearly all of the rounding is
-// that of the result.
+// warps unpack codes into the tiles that the products take, and the rest is as over a
+// cache of 16 bits.
 namespace st {
 namespace {
 constexpr bool CODES = true;
@@ -19,19 +15,15 @@ constexpr bool CODES = true;
 namespace st {
 namespace {
 
-constexpr int UNIT = 16;             // tokens whose keys and values a warp unpacks at a time
-constexpr int UNITS = TILE / UNIT;   // of a tile
 constexpr int UNPACKERS = 6;         // warps; no more than a tile has units, so that each sees every tile
 static_assert(UNPACKERS <= UNITS, "a warp that does not see a tile may miss two phases of its barriers");
 
-template <int D, bool PAIR>
+template <int D>
 struct Raw {
   static constexpr int CODE_BYTES = UNIT * D / 2;
   static constexpr int SCALES = 2 * CODE_BYTES;      // four numbers for each token
   static constexpr int NOTE = SCALES + UNIT * 8;     // where C.odd has the unit's tokens, -1: nowhere
   static constexpr int BYTES = NOTE + 16;
-  static constexpr int AHEAD = D == 128 ? 2 : 4;     // units of a warp in its ring
-  static constexpr int RING = AHEAD * BYTES;
 };
 
 __device__ __forceinline__ void copy_to_shared(uint32_t to, const void* from, bool there) {  // 16 bytes, or zeros
@@ -42,74 +34,34 @@ __device__ __forceinline__ void copy8_to_shared(uint32_t to, const void* from, b
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(there ? 8 : 0) : "memory");
 }
 
-// Eight codes as s (n - 8) + m, in their order: byte k holds the k-th pair.
-__device__ __forceinline__ uint4 unpacked(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 m) {
-  const __nv_bfloat162 middle = __float2bfloat162_rn(-136.0f);
-  const uint32_t up = w >> 4;
+// Eight codes as s n + z, f16, j and j + 4 in word j.  A code in the lowest four bits of
+// 1024 is 1024 + n, in the next four 1024 + 16 n; n is exact, and s n + z rounded once.
+__device__ __forceinline__ uint4 unpacked(uint32_t w, __half2 s, __half2 z) {
+  const __half2 low = __float2half2_rn(-1024.0f), next = __float2half2_rn(-64.0f), sixteenth = __float2half2_rn(0.0625f);
   uint32_t y[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {  // 128 + n
-    const uint32_t two = (__byte_perm(w, up, k | (4 + k) << 8) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 x = __hfma2(__hadd2(Pair<__nv_bfloat16>::pair(two), middle), s, m);
-    y[k] = *reinterpret_cast<const uint32_t*>(&x);
-  }
-  return make_uint4(y[0], y[1], y[2], y[3]);
-}
-
-__device__ __forceinline__ uint4 unpacked(uint32_t w, __half2 s, __half2 m) {
-  const __half2 one = __floats2half2_rn(1.0f, 0.0625f), middle = __floats2half2_rn(-1032.0f, -72.0f);
-  uint32_t y[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {  // 1024 + n, 1024 + 16 n
-    const uint32_t two = (__byte_perm(w, w, k | k << 8) & 0x00f0000fu) | 0x64006400u;
-    const __half2 x = __hfma2(__hfma2(Pair<__half>::pair(two), one, middle), s, m);
-    y[k] = *reinterpret_cast<const uint32_t*>(&x);
-  }
-  return make_uint4(y[0], y[1], y[2], y[3]);
-}
-
-// The same in the order that takes fewest operations: codes j and j + 4 in word j (output_column).
-__device__ __forceinline__ uint4 unpacked_pairs(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 m) {
-  const __nv_bfloat162 middle = __float2bfloat162_rn(-136.0f);
-  uint32_t y[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {  // 128 + n
-    const uint32_t two = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 x = __hfma2(__hadd2(Pair<__nv_bfloat16>::pair(two), middle), s, m);
-    y[j] = *reinterpret_cast<const uint32_t*>(&x);
-  }
-  return make_uint4(y[0], y[1], y[2], y[3]);
-}
-
-__device__ __forceinline__ uint4 unpacked_pairs(uint32_t w, __half2 s, __half2 m) {
-  const __half2 low = __float2half2_rn(-1032.0f), next = __float2half2_rn(-72.0f), sixteenth = __float2half2_rn(0.0625f);
-  uint32_t y[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {  // 1024 + n, or 1024 + 16 n
+  for (int j = 0; j < 4; ++j) {
     const uint32_t v = j < 2 ? w : w >> 8;
     const __half2 two = Pair<__half>::pair((v & (j % 2 ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u);
-    const __half2 x = __hfma2(j % 2 ? __hfma2(two, sixteenth, next) : __hadd2(two, low), s, m);
+    const __half2 x = __hfma2(j % 2 ? __hfma2(two, sixteenth, next) : __hadd2(two, low), s, z);
     y[j] = *reinterpret_cast<const uint32_t*>(&x);
   }
   return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-__device__ __forceinline__ __nv_bfloat162 twice(__nv_bfloat16, float x) { return __float2bfloat162_rn(x); }
-__device__ __forceinline__ __half2 twice(__half, float x) { return __float2half2_rn(x); }
-
-// One of UNPACKERS warps: every UNPACKERS-th unit, its codes, scales and zeros into the
-// warp's own ring while the one before is unpacked into the tiles' rings.
+// One of UNPACKERS warps: every UNPACKERS-th unit, its codes, scales and zeros into shared
+// memory of the warp's own while the one before is unpacked into the tiles' rings.
 template <typename T, int D, bool PAIR>
 __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* k_ring, uint8_t* v_ring, uint8_t* raw, int which) {
   using Y = Layout<D, PAIR>;
-  using R = Raw<D, PAIR>;
+  using R = Raw<D>;
   constexpr int LANES = D / 32;       // for a token's codes
   constexpr int TOKENS = 32 / LANES;  // of one step of loads
   const spec_tree_kv_t& kv = P.L.kv;
   const int lane = threadIdx.x % 32, token = lane / LANES, c = lane % LANES;
   const uint64_t token_bytes = kv.token_stride / 2, page_bytes = kv.page_stride / 2, scale_page_bytes = P.L.scales.page_stride * 2;
   const uint32_t mask = kv.page_size - 1;
-  raw += which * R::RING;
+  raw += which * R::BYTES;
   uint32_t* status = P.L.status;
 
   // ---- loads
@@ -144,12 +96,12 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
   };
   enter();
   look_up();
-  auto load = [&](int place) {
+  auto load = [&] {
     if (more) {
       const int slot = slot_of(), left = s.end - slot;
       const bool ok[2] = {page[0] >= 0 && page[0] < kv.n_pages, page[1] >= 0 && page[1] < kv.n_pages};
       if ((!ok[0] && left > 0) || (!ok[1] && left > 8)) set_status(status, SPEC_TREE_S_PAGES);
-      const uint32_t to = smem_u32(raw + place * R::BYTES);
+      const uint32_t to = smem_u32(raw);
 #pragma unroll
       for (int i = 0; i < UNIT / TOKENS; ++i) {
         const int x = i * TOKENS + token, h = x / 8;
@@ -168,64 +120,56 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
       }
       const int note = slot / TILE - s.clear / TILE;
       if (lane == 0)
-        *reinterpret_cast<int*>(raw + place * R::BYTES + R::NOTE) =
+        *reinterpret_cast<int*>(raw + R::NOTE) =
             note >= 0 ? (static_cast<int>(segment % ODD_BUFFERS) * MASKED_TILES + note) * UNITS + static_cast<int>(ask % UNITS) : -1;
       ask += UNPACKERS;
       look_up();
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll 1
-  for (int i = 0; i < R::AHEAD - 1; ++i) load(i);
+  load();
 
   // ---- tiles
   const uint32_t units = static_cast<uint32_t>(C.count) * UNITS;
   uint16_t* odd = reinterpret_cast<uint16_t*>(C.odd[0]);
   const int row_lane = lane / 2, half = lane % 2;
-  uint32_t place = 0;
   for (uint32_t unit = which; unit < units; unit += UNPACKERS) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(R::AHEAD - 2) : "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
-    load(place == 0 ? R::AHEAD - 1 : place - 1);  // the unit before this one has been unpacked
-    const uint32_t tile = unit / UNITS;
-    const int row = static_cast<int>(unit % UNITS) * UNIT + row_lane;
-    const uint8_t* from = raw + place * R::BYTES;
-    const uint2 four = *reinterpret_cast<const uint2*>(from + R::SCALES + row_lane * 8);
-    const int note = *reinterpret_cast<const int*>(from + R::NOTE);
-    // 16 tokens of the tile at `to`, from their codes at `at`; a lane has a half of its token's
-    auto unpack = [&](auto values, uint8_t* to, const uint8_t* at, float scale, float zero) {
-      const auto s2 = twice(T(), scale), m2 = twice(T(), fmaf(8.0f, scale, zero));
-      auto pieces = [&](const uint4 w, uint8_t* panel, int chunk) {  // 32 codes, four pieces of 16 bytes
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    // a lane's token, and half of its codes: of 128 a panel's 64 elements, with neighbours beginning at different
+    // halves, for the banks' sake
+    const uint2 four = *reinterpret_cast<const uint2*>(raw + R::SCALES + row_lane * 8);
+    const int note = *reinterpret_cast<const int*>(raw + R::NOTE);
+    uint4 key_words[D / 64], value_words[D / 64];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(panel + (((chunk + i) ^ (row % 8)) << 4)) =
-              decltype(values)::value ? unpacked_pairs(x[i], s2, m2) : unpacked(x[i], s2, m2);
-      };
-      to += row * 128;
-      if (D == 128) {
-        // a panel's 64 elements; neighbours begin at different halves, for the banks' sake
-        at += row_lane * 64 + half * 32;
-        const uint4 a = *reinterpret_cast<const uint4*>(at + half * 16), b = *reinterpret_cast<const uint4*>(at + (1 - half) * 16);
-        pieces(a, to + half * PANEL_BYTES, 4 * half);
-        pieces(b, to + half * PANEL_BYTES, 4 * (1 - half));
-      } else {
-        pieces(*reinterpret_cast<const uint4*>(at + row_lane * 32 + half * 16), to, 4 * half);
+    for (int x = 0; x < D / 64; ++x) {
+      const int at = row_lane * (D / 2) + half * (D / 4) + (D == 128 ? (x ^ half) * 16 : 0);
+      key_words[x] = *reinterpret_cast<const uint4*>(raw + at);
+      value_words[x] = *reinterpret_cast<const uint4*>(raw + R::CODE_BYTES + at);
+    }
+    __syncwarp();
+    load();  // the next unit, while this one is unpacked
+    const uint32_t tile = unit / UNITS, in_tile = unit % UNITS;
+    const int row = static_cast<int>(in_tile) * UNIT + row_lane;
+    auto unpack = [&](uint8_t* to, const uint4 (&words)[D / 64], float2 pair, float down) {
+      const __half2 scale = __float2half2_rn(pair.x * down), zero = __float2half2_rn(pair.y * down);
+      to += row * 128 + (D == 128 ? half * PANEL_BYTES : 0);
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x) {
+        const uint32_t w[4] = {words[x].x, words[x].y, words[x].z, words[x].w};
+        const int chunk = 4 * (D == 128 ? x ^ half : half);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(to + (((chunk + i) ^ (row % 8)) << 4)) = unpacked(w[i], scale, zero);
       }
       fence_proxy_async_smem();
     };
     const uint32_t ks = tile % Y::KS, vs = tile % Y::VS;
     if (!warp_wait(&C.k_empty[ks], ((tile / Y::KS) & 1) ^ 1, C, status)) break;
-    float2 pair = Pair<T>::unpack(four.x);
-    unpack(std::false_type(), k_ring + ks * Y::KV_BYTES, from, pair.x, pair.y);
-    warp_arrive(&C.k_full[ks]);
-    pair = Pair<T>::unpack(four.y);
-    if (!warp_wait(&C.v_empty[vs], ((tile / Y::VS) & 1) ^ 1, C, status)) break;
+    float2 key = Pair<T>::unpack(four.x), value = Pair<T>::unpack(four.y);
     if (note >= 0) {
-      // values that some rows do not see: those that are not finite become zeros and are noted
-      const bool bad = !isfinite(pair.x) || !isfinite(pair.y);
+      // values that some rows do not see: those that are not finite are noted and become zeros
+      const bool bad = !isfinite(value.x) || !isfinite(value.y);
       const uint32_t word = __ballot_sync(FULL, bad && half == 0);
-      if (bad) pair.x = pair.y = 0.0f;
+      if (bad) value.x = value.y = 0.0f;
       uint32_t bits = 0;
       if (__builtin_expect(word, 0)) {
 #pragma unroll
@@ -233,9 +177,20 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
       }
       if (lane == 0) odd[note] = static_cast<uint16_t>(bits);
     }
-    unpack(std::true_type(), v_ring + vs * Y::KV_BYTES, from + R::CODE_BYTES, pair.x, pair.y);
+    // the unit's powers of two: a token's lanes have a key and a value
+    const float2 mine = half == 0 ? key : value;
+    float largest = fmaxf(fabsf(mine.y), fabsf(fmaf(15.0f, mine.x, mine.y)));
+#pragma unroll
+    for (int o = 2; o < 32; o *= 2) largest = fmaxf(largest, __shfl_xor_sync(FULL, largest, o));
+    const int e = power_above(largest), ek = __shfl_sync(FULL, e, 0), ev = __shfl_sync(FULL, e, 1);
+    // The last tile that had this place is done with: the warp has waited for the values before this tile's, and so for
+    // products that came after its weights.
+    if (lane == 0) C.units[tile % UNIT_BUFFERS][in_tile] = make_float4(P.scale2 * power2(ek), static_cast<float>(ev), power2(-ev), 0.0f);
+    unpack(k_ring + ks * Y::KV_BYTES, key_words, key, power2(-ek));
+    warp_arrive(&C.k_full[ks]);
+    if (!warp_wait(&C.v_empty[vs], ((tile / Y::VS) & 1) ^ 1, C, status)) break;
+    unpack(v_ring + vs * Y::KV_BYTES, value_words, value, power2(-ev));
     warp_arrive(&C.v_full[vs]);
-    place = place + 1 == R::AHEAD ? 0 : place + 1;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -247,7 +202,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend4_kernel(const __grid_consta
   uint8_t* k_ring = smem + Y::Q_BYTES;
   uint8_t* v_ring = k_ring + Y::KS * Y::KV_BYTES;
   uint8_t* raw = v_ring + Y::VS * Y::KV_BYTES;
-  Control& C = *reinterpret_cast<Control*>(raw + UNPACKERS * Raw<D, PAIR>::RING);
+  Control& C = *reinterpret_cast<Control*>(raw + UNPACKERS * Raw<D>::BYTES);
   const int warp = __shfl_sync(FULL, threadIdx.x / 32, 0), cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < MAX_SLOTS; ++i) {
@@ -258,6 +213,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend4_kernel(const __grid_consta
     }
     mbar_init(&C.q_full, 1);
     mbar_init(&C.q_empty, 1);
+    mbar_init(&C.q_ready, HELPERS);
     mbar_init(&C.drain, 1);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&C.s_full[h], 1);
@@ -285,7 +241,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend4_kernel(const __grid_consta
 
   if (warp < HELPERS) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
-    softmax_role<T, D, PAIR>(P, C, cta, static_cast<int>(min64(gridDim.x, C.total)), warp / 4);
+    softmax_role<T, D, PAIR>(P, C, smem, cta, static_cast<int>(min64(gridDim.x, C.total)), warp / 4);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(HELPER_REGS));
     if (warp == HELPERS) {
@@ -315,7 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend4_kernel(const __grid_consta
 template <typename T, int D, bool PAIR>
 cudaError_t attend(Plan& P, cudaStream_t stream) {
   using Y = Layout<D, PAIR>;
-  constexpr int SMEM = Y::Q_BYTES + (Y::KS + Y::VS) * Y::KV_BYTES + UNPACKERS * Raw<D, PAIR>::RING + static_cast<int>(sizeof(Control));
+  constexpr int SMEM = Y::Q_BYTES + (Y::KS + Y::VS) * Y::KV_BYTES + UNPACKERS * Raw<D>::BYTES + static_cast<int>(sizeof(Control));
   static_assert(SMEM <= 232448, "shared memory of one CTA");
   static_assert(2 * (TILE + D) <= COLUMNS, "tensor memory");
   static_assert(THREADS == (HELPERS + 2 + UNPACKERS) * 32, "roles");

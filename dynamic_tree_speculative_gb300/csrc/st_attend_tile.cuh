@@ -42,6 +42,14 @@
 // set, so weights stay below 2^8 (f16: all weights carry another 2^7, so that
 // small ones keep their bits) and the sums are the same up to rounding.
 //
+// Codes.  Keys and values become f16 numbers, and queries too, for any model: with the
+// 8 bits of bf16 for keys, values and weights, outputs were 3 times as far from the exact ones as
+// their own rounding (and with codes multiplied as they are, scales and zeros applied to each score
+// and weight in the softmax, a tree of 64 took 439 us).  Powers of two keep them in
+// range: one for a row of queries; for the keys and for the values of each 16 tokens, which go
+// back in with the scores, the values' into the exponent of the weights; the weights' reference
+// so follows scores times values.
+//
 // Tokens a row does not see get S = -inf.  Their values enter the product
 // with weight zero, so in tiles that not every row sees whole, infinities and
 // NaN among the values are replaced by zero in shared memory first.
@@ -74,12 +82,13 @@ namespace st {
 namespace {
 
 constexpr int PANEL_BYTES = TILE * 128;         // 128 rows of 64 elements
-constexpr int MAX_SLOTS = 5;                    // of a ring
+constexpr int MAX_SLOTS = CODES ? 3 : 5;        // of a ring
 constexpr int MASKED_TILES = SPEC_TREE_MAX_NODES / TILE + 2;
 // Segments whose notes on values are held.  A side warp waits for the products of the
 // segment before; unpacking warps are ahead of them by a ring of values, whose last
 // tile's product means that the softmax is done with the segment before that tile's.
-constexpr int ODD_BUFFERS = CODES ? MAX_SLOTS + 1 : 3;
+constexpr int ODD_BUFFERS = CODES ? MAX_SLOTS + 1 : 3, UNIT_BUFFERS = CODES ? MAX_SLOTS + 1 : 1;
+constexpr int UNIT = 16, UNITS = TILE / UNIT;   // tokens that are unpacked together, and have one factor
 // Two softmax warpgroups and one of helpers, or two: codes are unpacked by six warps.
 constexpr int THREADS = (CODES ? 4 : 3) * TILE;
 // A softmax thread holds a row of 128 scores in registers: of those that each thread
@@ -120,6 +129,10 @@ struct Control : Deal<THREADS / 32> {
   int abort;
   uint32_t odd[ODD_BUFFERS][MASKED_TILES * (TILE / 32)];  // tokens with a value that is not finite, by segment
   uint8_t up[2][SPEC_TREE_MAX_NODES];           // node minus parent, by segment modulo 2; 0: none, 255: more
+  // codes, for each unit of a tile, by tile: what its products with the keys are to be
+  // multiplied by; e and 2^-e, its values being multiplied by the latter
+  float4 units[UNIT_BUFFERS][UNITS];
+  uint64_t q_ready;  // codes: queries have been put in order
   union {
     float2 pair[TILE];         // the odd tiles' (reference, sum)
     int tiles[MAX_PIECE_ITEMS];  // setup: tiles of (tree, rows)
@@ -227,11 +240,12 @@ __device__ __forceinline__ void load_role(const Plan& P, const CUtensorMap* map,
 template <typename T, int D, bool PAIR>
 __device__ __forceinline__ void product_role(const Plan& P, Control& C, uint32_t q_smem, uint32_t k_smem, uint32_t v_smem) {
   using Y = Layout<D, PAIR>;
-  constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+  constexpr bool BF = std::is_same<T, __nv_bfloat16>::value && !CODES;
   constexpr uint32_t ID_S = mma_descriptor(BF, TILE, false), ID_O = mma_descriptor(BF, D, true);
   constexpr int KV16 = Y::KV_BYTES / 16, PANEL16 = PANEL_BYTES / 16;  // descriptors count 16 bytes
   const uint32_t tmem = uniform(C.tmem), q_low = uniform(smem_descriptor_low(q_smem, 0));
   const uint32_t k_low = smem_descriptor_low(k_smem, 0), v_low = smem_descriptor_low(v_smem, PANEL_BYTES);
+  uint64_t* queries = CODES ? &C.q_ready : &C.q_full;
   const uint32_t id_s = uniform(P.negative ? ID_S | MMA_NEGATE_A : ID_S);
   uint32_t* status = P.L.status;
   Walk<Y::HALVES> walk(C);
@@ -304,7 +318,7 @@ __device__ __forceinline__ void product_role(const Plan& P, Control& C, uint32_t
 
   while (walk.next(P)) {
     const int count = s.last - s.first;
-    if (!warp_wait(&C.q_full, segment & 1, C, status) || !keys(n)) return;
+    if (!warp_wait(queries, segment & 1, C, status) || !keys(n)) return;
     tmem_fence_after();
 #pragma unroll 1
     for (int h = 0; h < 2 && (!PAIR || h < count); ++h) {
@@ -534,6 +548,13 @@ __device__ __forceinline__ constexpr int output_column(int x) {
   return CODES ? (x & ~7) + ((x & 3) << 1) + ((x >> 2) & 1) : x;
 }
 
+__device__ __forceinline__ float power2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// The least e with x <= 2^e, from -80 to 126.
+__device__ __forceinline__ int power_above(float x) {
+  return min(static_cast<int>((__float_as_uint(fmaxf(x, power2(-80))) + 0x007fffffu) >> 23) - 127, 126);
+}
+
 // Whether the row's node sees one of the tokens of the segment that `odd` names.
 __device__ __noinline__ bool sees_odd(const Plan& P, const Segment& s, const uint32_t* odd, int node) {
   const int first_masked = s.clear / TILE;
@@ -550,10 +571,11 @@ __device__ __noinline__ bool sees_odd(const Plan& P, const Segment& s, const uin
 // 128 threads, one row each: weights, the running reference and sum, and the
 // output.
 template <typename T, int D, bool PAIR>
-__device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta, int ctas, int half) {
+__device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t* q_smem, int cta, int ctas, int half) {
   using Y = Layout<D, PAIR>;
   constexpr int EACH = PAIR ? 2 : 1;  // a half takes every tile, or every other one
-  constexpr float SHIFT = std::is_same<T, __half>::value ? 7.0f : 0.0f;
+  using W = std::conditional_t<CODES, __half, T>;  // weights
+  constexpr float SHIFT = std::is_same<W, __half>::value ? 7.0f : 0.0f;
   const int t = threadIdx.x % TILE, warp = t / 32, lane = t % 32;
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
   const uint32_t tm_s = C.tmem + half * TILE + lanes, tm_o = C.tmem + 2 * TILE + half * D + lanes;
@@ -561,8 +583,9 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
   Walk<Y::HALVES> walk(C);
   const Segment& s = walk.s;
   uint32_t tile = 0, segment = 0, ends = 0;  // tiles of this half, segments, segments with a tile of this half so far
+  uint32_t before = 0;  // tiles of the segments before
   bool ok = true;  // uniform over the warp; a warp that has given up still meets the others at barriers
-  for (; walk.next(P); ++segment) {
+  for (; walk.next(P); before += s.last - s.first, ++segment) {
     const int local = (PAIR ? 0 : half * P.half_rows) + t, row = s.row0 + local;
     const bool in_call = t < P.half_rows && row < P.rows;
     const int i = node_of_row(P, row), g = row - i * P.group;
@@ -571,6 +594,41 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
     const bool warp_live = __any_sync(FULL, live);
     const int first_masked = s.clear / TILE;  // tiles from here on are not seen whole by every row
     float ref = -INFINITY, sum = 0.0f;
+    // codes: the row's query as f16 numbers, up to 2^14, in the order in which keys are unpacked
+    float factor = 1.0f;
+    if (CODES) {
+      ok = ok && warp_wait(&C.q_full, segment & 1, C, status);
+      if (ok && (!PAIR || half == 0)) {
+        uint8_t* own = q_smem + (PAIR ? 0 : half) * Y::KV_BYTES + t * 128;
+        float largest = 0.0f;
+        auto piece = [&](int c) { return reinterpret_cast<uint4*>(own + c / 8 * PANEL_BYTES + ((c ^ t) % 8) * 16); };
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          float q[8];
+          unpack8<T>(*piece(c), q);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) largest = fmaxf(largest, fabsf(q[e]));
+        }
+        const int e = power_above(largest);
+        const float up = power2(14 - e);
+        factor = power2(e - 14);
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          float q[8];
+          unpack8<T>(*piece(c), q);
+          const uint32_t w[4] = {Pair<__half>::pack(q[0] * up, q[4] * up), Pair<__half>::pack(q[1] * up, q[5] * up),
+                                 Pair<__half>::pack(q[2] * up, q[6] * up), Pair<__half>::pack(q[3] * up, q[7] * up)};
+          *piece(c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (PAIR) C.pair[t].x = factor;
+        fence_proxy_async_smem();
+      }
+      warp_arrive(&C.q_ready);
+      if (PAIR && half == 1) {
+        ok = ok && warp_wait(&C.q_ready, segment & 1, C, status);
+        factor = C.pair[t].x;
+      }
+    }
 
     for (int j = s.first + (PAIR ? half : 0); j < s.last; j += EACH, ++tile) {
       const int base = j * TILE;
@@ -612,14 +670,31 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
 #pragma unroll
         for (int c = 0; c < TILE / 32; ++c) tmem_ld32(tm_s + c * 32, x + c * 32);
         tmem_wait_ld();
+        // codes: relative to the reference so far, times the values' powers of two
+        const float4* units = C.units[(before + j - s.first) % UNIT_BUFFERS];
+        const float now = ref == -INFINITY ? 0.0f : ref - SHIFT;
+        if (CODES) {
+#pragma unroll
+          for (int u = 0; u < UNITS; ++u) {
+            const float4 unit = units[u];
+            const float up = fmaxf(unit.x * factor, 1e-37f);  // a zero would make NaN of the -inf of what is not seen
+            const F2 by(up, up), less(unit.y - now, unit.y - now);
+#pragma unroll
+            for (int c = u * UNIT; c < (u + 1) * UNIT; c += 2) {
+              float a, b;
+              fma2(F2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), by, less).get(a, b);
+              x[c] = __float_as_uint(a), x[c + 1] = __float_as_uint(b);
+            }
+          }
+        }
         float top8[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) top8[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
 #pragma unroll
         for (int c = 16; c < TILE; c += 2)
           top8[c / 2 % 8] = max3(top8[c / 2 % 8], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-        const float top = P.scale2 * fmaxf(max3(max3(top8[0], top8[1], top8[2]), top8[3], top8[4]),
-                                           max3(top8[5], top8[6], top8[7]));
+        float top = fmaxf(max3(max3(top8[0], top8[1], top8[2]), top8[3], top8[4]), max3(top8[5], top8[6], top8[7]));
+        top = CODES ? top + now : P.scale2 * top;
         const bool grow = live && top > ref + LAZY;
         if (j < s.first + EACH) {
           ref = top;
@@ -639,16 +714,35 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
         }
         const float sub = ref == -INFINITY ? 0.0f : ref - SHIFT;
         const F2 scale2(P.scale2, P.scale2), shift2(-sub, -sub);
+        if (CODES && __any_sync(FULL, sub != now)) {
+          const F2 moved(now - sub, now - sub);
+#pragma unroll
+          for (int c = 0; c < TILE; c += 2) {
+            float a, b;
+            add2(F2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), moved).get(a, b);
+            x[c] = __float_as_uint(a), x[c + 1] = __float_as_uint(b);
+          }
+        }
         F2 part[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) part[c] = F2(0.0f, 0.0f);
         auto weigh = [&](int c) {
           float a, b;
-          fma2(F2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, shift2).get(a, b);
+          if (CODES)
+            a = __uint_as_float(x[c]), b = __uint_as_float(x[c + 1]);
+          else
+            fma2(F2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, shift2).get(a, b);
           a = ex2(a);
           b = ex2(b);
           part[c / 2 % 4] = add2(part[c / 2 % 4], F2(a, b));
-          x[c / 2] = Pair<T>::pack(a, b);
+          x[c / 2] = Pair<W>::pack(a, b);
+          if (CODES && c % UNIT == UNIT - 2) {
+            // a unit's weights, without its values' power of two
+            add2(add2(part[0], part[1]), add2(part[2], part[3])).get(a, b);
+            sum = fmaf(a + b, units[c / UNIT].z, sum);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) part[i] = F2(0.0f, 0.0f);
+          }
         };
 #pragma unroll
         for (int c = 0; c < EARLY; c += 2) weigh(c);
@@ -661,9 +755,11 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, int cta,
         tmem_st32(tm_s + EARLY / 2, x + EARLY / 2);
         tmem_wait_st();
         tmem_fence_before();
-        float a, b;
-        add2(add2(part[0], part[1]), add2(part[2], part[3])).get(a, b);
-        sum += a + b;
+        if (!CODES) {
+          float a, b;
+          add2(add2(part[0], part[1]), add2(part[2], part[3])).get(a, b);
+          sum += a + b;
+        }
       } else {
         warp_arrive(&C.w_full[half][0]);
       }

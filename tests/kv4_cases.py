@@ -29,23 +29,24 @@ def steps(c, pool4, scale, which):
     return s, z + 8 * s
 
 
-def attend_bound(dtype, out, k_abs, q_k, v_abs, mean_v, steps_v, sum_v, D, tokens, few):
+def attend_bound(dtype, out, k_abs, q_k, floor_k, floor_v, mean_v, steps_v, D, tokens, few):
     """|error| of an attention output over values of 4 bits; all terms are sums over what a row sees.
 
     few rows: codes n are exact, a score is s (q . n) + z sum q in float32 (k_abs: the largest scale * sum |q| (15 s + |z|)),
     D + 16 roundings 2^-23 of it; the weights times the values' scales are rounded to f16's 11 bits, half a step 2^-11 of
     sum p 15 s (steps_v), those 2^-29 below the largest to its least step (2^-39 of the largest each); products of up to
     sum p 15 s + |z| are summed in float32.
-    more rows: keys k = s (n - 8) + (z + 8 s) are rounded to dtype, half a step h of |k| and of |z + 8 s| (q_k: the largest
-    scale * sum |q| (|k| + |z + 8 s|)), D + 8 roundings of the products; the weights are rounded to dtype (h of sum p |v|),
-    the values to dtype too (mean_v: sum p (|v| + |z + 8 s|), h of it).
+    more rows: keys and values are rounded to f16's 11 bits, half a step 2^-11 of |k| (q_k: the largest scale * sum |q| |k|)
+    and of |v| (mean_v), and to 2^-25 of the largest element of 16 tokens (floor_k: the same sum with the largest element of
+    all; floor_v: that of the values), D + 8 roundings of the products; the weights, times a power of two, to 2^-11.
     Both: an error e in the scores is a factor exp(2 e) between weights; sums over the tokens and the exponential
-    cost (tokens + 16) 2^-23; f16 weights below 2^-14 lose at most 2^-25 each; then one rounding to dtype."""
+    cost (tokens + 16) 2^-23; then one rounding to dtype."""
     h = kv_cases.half_step(dtype)
     if few:
         delta = np.expm1(2 * (D + 16) * 2.0 ** -23 * k_abs[..., None]) + (tokens + 32) * 2.0 ** -23
         before = delta * mean_v + 2.0 ** -11 * (1 + delta) * steps_v + (tokens + 16) * 2.0 ** -23 * (steps_v + mean_v)
     else:
-        delta = np.expm1(2 * (h * q_k + (D + 8) * 2.0 ** -23 * k_abs)[..., None]) + h + (tokens + 16) * 2.0 ** -23
-        before = delta * (1 + h) * mean_v + 2 * h * mean_v + (2.0 ** -25 * sum_v if dtype == torch.float16 else 0.0)
+        delta = np.expm1(2 * (2.0 ** -11 * q_k + 2.0 ** -25 * floor_k + (D + 8) * 2.0 ** -23 * k_abs)[..., None])
+        delta = delta + 2.0 ** -11 + (tokens + 16) * 2.0 ** -23
+        before = delta * (1 + 2.0 ** -11) * mean_v + 2.0 ** -11 * mean_v + 2.0 ** -24 * floor_v
     return before + h * (np.abs(out) + before) + (2.0 ** -25 if dtype == torch.float16 else 2.0 ** -133)

@@ -59,16 +59,18 @@ def _expected(c, q, codes, scale, layer=0):
     call = lambda qq, k, v: O.attend(qq, k, v, c.table.numpy(), c.seq_len.numpy(), parents, c.counts, c.begin, scale)  # noqa: E731
     (ks, km), (vs, vm) = (tuple(x[layer] for x in kv4_cases.steps(c, None, sc, w)) for w in (0, 1))
     qn = q.double().numpy()
-    out, mean_v, _, sum_v = call(qn, kp, vp)
+    out, mean_v, _, _ = call(qn, kp, vp)
     wide = lambda x: np.repeat(x[..., None], D, -1)  # noqa: E731
     # sums over the tokens with the outputs' own weights: |v| + |middle| + |zero|, and 15 steps
     mean_m = call(qn, kp, wide(np.abs(vm) + np.abs(vm - 8 * vs)))[0]
     steps_v = call(qn, kp, wide(15 * np.abs(vs)))[0]
     # the largest scale * sum |q| x over what a row sees
-    q_k = call(np.abs(qn), np.abs(kp) + wide(np.abs(km)), vp)[2]
+    q_k = call(np.abs(qn), np.abs(kp), vp)[2]
+    floor_k = call(np.abs(qn), np.full_like(kp, np.nanmax(np.abs(np.where(np.isfinite(kp), kp, 0)))), vp)[2]
+    floor_v = np.nanmax(np.abs(np.where(np.isfinite(vp), vp, 0)))
     k_abs = call(np.abs(qn), wide(15 * np.abs(ks) + np.abs(km - 8 * ks)), vp)[2]
     tokens = int(c.seq_len.max()) + c.begin + c.N
-    return out, kv4_cases.attend_bound(c.dtype, out, k_abs, q_k, None, mean_v + mean_m, steps_v, sum_v, D, tokens, few)
+    return out, kv4_cases.attend_bound(c.dtype, out, k_abs, q_k, floor_k, floor_v, mean_v + mean_m, steps_v, D, tokens, few)
 
 
 def _check_attend(c, q, scale=None, layer=0, layout="head"):
@@ -77,10 +79,11 @@ def _check_attend(c, q, scale=None, layer=0, layout="head"):
     want, bound = _expected(c, q, codes, q.shape[3] ** -0.5 if scale is None else scale, layer)
     err = np.abs(got.double().numpy() - want)
     assert status == 0 and (err <= bound).all(), (status, float(np.nanmax(err / bound)), int((~(err <= bound)).sum()))
-    # all roundings together, in the 2-norm: those of the output and of the weights (or the weights times scales) are
-    # independent and at most half a step each, those of keys and values too where they are rounded: some half steps
+    # all roundings together, in the 2-norm: the output's half step h at most, and 2^-11 each of the weights, keys (times the
+    # scores' spread, up to four) and values, of outputs that are at least a hundredth of the values
     if np.linalg.norm(want) > 0 and scale is None:
-        assert np.linalg.norm(err) <= 4 * 2.0 ** -8 * max(np.linalg.norm(want), 0.1 * np.sqrt(want.size))
+        h = kv_cases.half_step(c.dtype)
+        assert np.linalg.norm(err) <= (h + 6 * 2.0 ** -11) * max(np.linalg.norm(want), 0.1 * np.sqrt(want.size))
 
 
 # --------------------------------------------------------------- attention ---
