@@ -670,31 +670,29 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
 #pragma unroll
         for (int c = 0; c < TILE / 32; ++c) tmem_ld32(tm_s + c * 32, x + c * 32);
         tmem_wait_ld();
-        // codes: relative to the reference so far, times the values' powers of two
+        float top;
         const float4* units = C.units[(before + j - s.first) % UNIT_BUFFERS];
-        const float now = ref == -INFINITY ? 0.0f : ref - SHIFT;
         if (CODES) {
+          top = -INFINITY;
 #pragma unroll
           for (int u = 0; u < UNITS; ++u) {
             const float4 unit = units[u];
             const float up = fmaxf(unit.x * factor, 1e-37f);  // a zero would make NaN of the -inf of what is not seen
-            const F2 by(up, up), less(unit.y - now, unit.y - now);
+            float most = fmaxf(__uint_as_float(x[u * UNIT]), __uint_as_float(x[u * UNIT + 1]));
 #pragma unroll
-            for (int c = u * UNIT; c < (u + 1) * UNIT; c += 2) {
-              float a, b;
-              fma2(F2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), by, less).get(a, b);
-              x[c] = __float_as_uint(a), x[c + 1] = __float_as_uint(b);
-            }
+            for (int c = 2; c < UNIT; c += 2)
+              most = max3(most, __uint_as_float(x[u * UNIT + c]), __uint_as_float(x[u * UNIT + c + 1]));
+            top = fmaxf(top, fmaf(most, up, unit.y));
           }
+        } else {
+          float top8[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) top8[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+#pragma unroll
+          for (int c = 16; c < TILE; c += 2)
+            top8[c / 2 % 8] = max3(top8[c / 2 % 8], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+          top = P.scale2 * fmaxf(max3(max3(top8[0], top8[1], top8[2]), top8[3], top8[4]), max3(top8[5], top8[6], top8[7]));
         }
-        float top8[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) top8[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
-#pragma unroll
-        for (int c = 16; c < TILE; c += 2)
-          top8[c / 2 % 8] = max3(top8[c / 2 % 8], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-        float top = fmaxf(max3(max3(top8[0], top8[1], top8[2]), top8[3], top8[4]), max3(top8[5], top8[6], top8[7]));
-        top = CODES ? top + now : P.scale2 * top;
         const bool grow = live && top > ref + LAZY;
         if (j < s.first + EACH) {
           ref = top;
@@ -714,24 +712,18 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
         }
         const float sub = ref == -INFINITY ? 0.0f : ref - SHIFT;
         const F2 scale2(P.scale2, P.scale2), shift2(-sub, -sub);
-        if (CODES && __any_sync(FULL, sub != now)) {
-          const F2 moved(now - sub, now - sub);
-#pragma unroll
-          for (int c = 0; c < TILE; c += 2) {
-            float a, b;
-            add2(F2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), moved).get(a, b);
-            x[c] = __float_as_uint(a), x[c + 1] = __float_as_uint(b);
-          }
-        }
+        F2 by = scale2, plus = shift2;
         F2 part[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) part[c] = F2(0.0f, 0.0f);
         auto weigh = [&](int c) {
           float a, b;
-          if (CODES)
-            a = __uint_as_float(x[c]), b = __uint_as_float(x[c + 1]);
-          else
-            fma2(F2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, shift2).get(a, b);
+          if (CODES && c % UNIT == 0) {  // read again: kept, they would cost the registers that there are not
+            const float4 unit = units[c / UNIT];
+            a = fmaxf(unit.x * factor, 1e-37f), b = unit.y - sub;
+            by = F2(a, a), plus = F2(b, b);
+          }
+          fma2(F2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), by, plus).get(a, b);
           a = ex2(a);
           b = ex2(b);
           part[c / 2 % 4] = add2(part[c / 2 % 4], F2(a, b));
