@@ -2,6 +2,12 @@
 // (spec_tree_kv4_attend), for calls of more rows than attend4_few.cu takes: six
 // warps unpack codes into the tiles that the products take, and the rest is as over a
 // cache of 16 bits.
+//
+// Trees of 61 nodes after 4500 tokens, 64 sequences, take 252 us and a chunk of 2048
+// tokens after 52 takes 120; with the arithmetic of unpacking left out 215 and 104 remained.
+// Unpacking is bound by the integer pipe (5 operations for
+// 8 codes, and 2 of f16 for each pair) and by shared memory (each 16-bit number is
+// written once and read by each half of the rows), which the softmax's loads share.
 namespace st {
 namespace {
 constexpr bool CODES = true;
@@ -15,20 +21,21 @@ constexpr bool CODES = true;
 namespace st {
 namespace {
 
-constexpr int UNPACKERS = 6;         // warps; no more than a tile has units, so that each sees every tile
+constexpr int UNIT = 16, UNITS = TILE / UNIT;  // tokens that a warp unpacks together
+constexpr int UNPACKERS = 6;                   // warps; no more than a tile has units, so that each sees every tile
 static_assert(UNPACKERS <= UNITS, "a warp that does not see a tile may miss two phases of its barriers");
 
 template <int D>
 struct Raw {
   static constexpr int CODE_BYTES = UNIT * D / 2;
-  static constexpr int SCALES = 2 * CODE_BYTES;      // four numbers for each token
-  static constexpr int NOTE = SCALES + UNIT * 8;     // where C.odd has the unit's tokens, -1: nowhere
-  static constexpr int BYTES = NOTE + 16;
+  static constexpr int BYTES = 2 * CODE_BYTES;
 };
 
 __device__ __forceinline__ void copy_to_shared(uint32_t to, const void* from, bool there) {  // 16 bytes, or zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
+
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 __device__ __forceinline__ void copy8_to_shared(uint32_t to, const void* from, bool there) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(there ? 8 : 0) : "memory");
@@ -49,8 +56,107 @@ __device__ __forceinline__ uint4 unpacked(uint32_t w, __half2 s, __half2 z) {
   return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-// One of UNPACKERS warps: every UNPACKERS-th unit, its codes, scales and zeros into shared
-// memory of the warp's own while the one before is unpacked into the tiles' rings.
+// One warp: the tiles' scales and zeros, LEAD tiles ahead of their powers of two, which
+// are the keys' and values' next above the largest of the tile's 128 tokens; which values
+// are not finite, where some rows may not see them, and zeros in their place; queries and
+// parents.
+template <typename T, int D, bool PAIR>
+__device__ __forceinline__ void scale_role(const Plan& P, const CUtensorMap* mq, Control& C, uint32_t q_smem) {
+  constexpr int LEAD = 2, EACH = TILE / 32;  // tokens of a lane; pages have 8 or more
+  static_assert(EACH == 4, "a word of notes for 8 lanes");
+  // Tiles of a segment that come before its queries are waited for, which are free once the
+  // segment before is done with: that needs nothing of the segment itself as long as
+  // the slot of the last of their loads is one of the segment before.
+  constexpr int FIRST = SCALE_SLOTS - LEAD - 1;
+  static_assert(FIRST >= 1, "slots");
+  const spec_tree_kv_t& kv = P.L.kv;
+  const int lane = threadIdx.x % 32;
+  uint32_t* status = P.L.status;
+
+  Walk<Layout<D, PAIR>::HALVES> ahead(C), walk(C);
+  bool more = ahead.next(P);
+  int to_load = ahead.s.first, page = -1;
+  uint32_t loads = 0;
+  auto look_up = [&] {
+    const int slot = to_load * TILE + lane * EACH;
+    page = more && slot < ahead.s.end ? kv.page_table[static_cast<int64_t>(ahead.s.b) * kv.table_stride + (slot >> P.page_shift)] : -1;
+  };
+  auto load = [&] {
+    if (!more) return true;
+    if (!warp_wait(&C.scale_empty[loads % SCALE_SLOTS], ((loads / SCALE_SLOTS) & 1) ^ 1, C, status)) return false;
+    const int slot = to_load * TILE + lane * EACH;
+    const bool ok = page >= 0 && page < kv.n_pages;
+    if (!ok && slot < ahead.s.end) set_status(status, SPEC_TREE_S_PAGES);
+    const uint8_t* from = static_cast<const uint8_t*>(P.L.scales.data) +
+                          (P.L.layer * P.L.scales.layer_stride + ahead.s.head * P.L.scales.head_stride +
+                           (ok ? page : 0) * P.L.scales.page_stride) * 2 + (slot & (kv.page_size - 1)) * 8;
+    const uint32_t to = smem_u32(&C.scales[loads % SCALE_SLOTS][lane * EACH]);
+#pragma unroll
+    for (int x = 0; x < EACH; ++x) copy8_to_shared(to + x * 8, from + x * 8, ok && slot + x < ahead.s.end);
+    ++loads;
+    if (++to_load == ahead.s.last) {
+      more = ahead.next(P);
+      to_load = ahead.s.first;
+    }
+    look_up();
+    return true;
+  };
+  look_up();
+#pragma unroll 1
+  for (int x = 0; x < LEAD; ++x) {
+    load();
+    commit_copies();
+  }
+
+  uint32_t segment = 0, n = 0, asked = 0;  // segments, tiles, segments whose queries have been asked for so far
+  const Segment& s = walk.s;
+  bool ok = true;
+  for (; ok && walk.next(P); ++segment) {
+    for (int j = s.first; ok; ++j, ++n) {
+      if (asked == segment && (segment == 0 || j == min(s.first + FIRST, s.last))) {
+        ok = ask_queries<D, PAIR>(P, mq, C, q_smem, s, segment);
+        asked += ok;
+      }
+      if (!ok || j == s.last) break;
+      ok = load();
+      commit_copies();
+      if (!ok) break;
+      asm volatile("cp.async.wait_group %0;" ::"n"(LEAD) : "memory");
+      uint2* mine = &C.scales[n % SCALE_SLOTS][lane * EACH];
+      float key = 0.0f, value = 0.0f;
+      uint32_t bad = 0;
+      const bool masked = j >= s.clear / TILE;
+#pragma unroll
+      for (int x = 0; x < EACH; ++x) {
+        const uint2 four = mine[x];
+        const float2 k = Pair<T>::unpack(four.x);
+        const float2 v = Pair<T>::unpack(four.y);
+        const float most_k = fmaxf(fabsf(k.y), fabsf(fmaf(15.0f, k.x, k.y)));
+        const float most_v = fmaxf(fabsf(v.y), fabsf(fmaf(15.0f, v.x, v.y)));
+        if (isfinite(most_k)) key = fmaxf(key, most_k);
+        if (isfinite(most_v)) value = fmaxf(value, most_v);
+        if (masked && !(isfinite(v.x) && isfinite(v.y))) {
+          bad |= 1u << x;
+          mine[x].y = 0;
+        }
+      }
+      if (masked) {
+        const uint32_t word = __reduce_or_sync(0xffu << (lane / 8 * 8), bad << (lane % 8 * EACH));
+        if (lane % 8 == 0) C.odd[segment % ODD_BUFFERS][(j - s.clear / TILE) * (TILE / 32) + lane / 8] = word;
+      }
+      const int ek = power_above(__uint_as_float(__reduce_max_sync(FULL, __float_as_uint(key))));
+      const int ev = power_above(__uint_as_float(__reduce_max_sync(FULL, __float_as_uint(value))));
+      if (lane == 0)
+        C.powers[n % POWER_SLOTS] = make_float4(P.scale2 * power2(ek), static_cast<float>(ev), power2(-ev), power2(-ek));
+      warp_arrive(&C.scale_full[n % SCALE_SLOTS]);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (asked > 0) mbar_wait(&C.q_full, (asked - 1) & 1);  // queries in flight land before the CTA ends
+}
+
+// One of UNPACKERS warps: every UNPACKERS-th unit, its codes into shared memory of the
+// warp's own while the one before is unpacked into the tiles' rings.
 template <typename T, int D, bool PAIR>
 __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* k_ring, uint8_t* v_ring, uint8_t* raw, int which) {
   using Y = Layout<D, PAIR>;
@@ -59,7 +165,7 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
   constexpr int TOKENS = 32 / LANES;  // of one step of loads
   const spec_tree_kv_t& kv = P.L.kv;
   const int lane = threadIdx.x % 32, token = lane / LANES, c = lane % LANES;
-  const uint64_t token_bytes = kv.token_stride / 2, page_bytes = kv.page_stride / 2, scale_page_bytes = P.L.scales.page_stride * 2;
+  const uint64_t token_bytes = kv.token_stride / 2, page_bytes = kv.page_stride / 2;
   const uint32_t mask = kv.page_size - 1;
   raw += which * R::BYTES;
   uint32_t* status = P.L.status;
@@ -67,17 +173,15 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
   // ---- loads
   Walk<Y::HALVES> walk(C);
   const Segment& s = walk.s;
-  uint32_t before = 0, segment = 0;  // tiles of the segments before, segments
+  uint32_t before = 0;               // tiles of the segments before
   uint32_t ask = which;              // the unit to load next
   bool more = walk.next(P);
   int page[2] = {-1, -1};            // of its first and last 8 tokens
   const int64_t to_values = static_cast<const uint8_t*>(kv.v) - static_cast<const uint8_t*>(kv.k);
-  const uint8_t *codes, *scales;     // of this lane's token, entry 0 of page 0 of the segment's head
+  const uint8_t* codes;              // of this lane's token, entry 0 of page 0 of the segment's head
   const int32_t* table;
   auto enter = [&] {
     codes = static_cast<const uint8_t*>(kv.k) + (P.L.layer * kv.layer_stride + s.head * kv.head_stride) / 2 + c * 16;
-    scales = static_cast<const uint8_t*>(P.L.scales.data) +
-             (P.L.layer * P.L.scales.layer_stride + s.head * P.L.scales.head_stride) * 2;
     table = kv.page_table + static_cast<int64_t>(s.b) * kv.table_stride;
   };
   auto slot_of = [&] { return (s.first + static_cast<int>(ask / UNITS - before)) * TILE + static_cast<int>(ask % UNITS) * UNIT; };
@@ -85,7 +189,6 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
     while (more && slot_of() >= s.last * TILE) {
       before += s.last - s.first;
       more = walk.next(P);
-      ++segment;
       enter();
     }
     page[0] = page[1] = -1;
@@ -100,7 +203,6 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
     if (more) {
       const int slot = slot_of(), left = s.end - slot;
       const bool ok[2] = {page[0] >= 0 && page[0] < kv.n_pages, page[1] >= 0 && page[1] < kv.n_pages};
-      if ((!ok[0] && left > 0) || (!ok[1] && left > 8)) set_status(status, SPEC_TREE_S_PAGES);
       const uint32_t to = smem_u32(raw);
 #pragma unroll
       for (int i = 0; i < UNIT / TOKENS; ++i) {
@@ -111,17 +213,6 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
         copy_to_shared(to + lane * 16 + i * 512, from, there);
         copy_to_shared(to + R::CODE_BYTES + lane * 16 + i * 512, from + to_values, there);
       }
-      if (lane < UNIT) {
-        const int h = lane / 8;
-        const bool there = (h ? ok[1] : ok[0]) && lane < left;
-        copy8_to_shared(to + R::SCALES + lane * 8,
-                        scales + static_cast<uint32_t>(there ? (h ? page[1] : page[0]) : 0) * scale_page_bytes + ((slot + lane) & mask) * 8,
-                        there);
-      }
-      const int note = slot / TILE - s.clear / TILE;
-      if (lane == 0)
-        *reinterpret_cast<int*>(raw + R::NOTE) =
-            note >= 0 ? (static_cast<int>(segment % ODD_BUFFERS) * MASKED_TILES + note) * UNITS + static_cast<int>(ask % UNITS) : -1;
       ask += UNPACKERS;
       look_up();
     }
@@ -130,15 +221,12 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
 
   // ---- tiles
   const uint32_t units = static_cast<uint32_t>(C.count) * UNITS;
-  uint16_t* odd = reinterpret_cast<uint16_t*>(C.odd[0]);
   const int row_lane = lane / 2, half = lane % 2;
   for (uint32_t unit = which; unit < units; unit += UNPACKERS) {
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     // a lane's token, and half of its codes: of 128 a panel's 64 elements, with neighbours beginning at different
     // halves, for the banks' sake
-    const uint2 four = *reinterpret_cast<const uint2*>(raw + R::SCALES + row_lane * 8);
-    const int note = *reinterpret_cast<const int*>(raw + R::NOTE);
     uint4 key_words[D / 64], value_words[D / 64];
 #pragma unroll
     for (int x = 0; x < D / 64; ++x) {
@@ -163,34 +251,17 @@ __device__ __forceinline__ void unpack_role(const Plan& P, Control& C, uint8_t* 
       fence_proxy_async_smem();
     };
     const uint32_t ks = tile % Y::KS, vs = tile % Y::VS;
+    const uint32_t slot = tile % SCALE_SLOTS;
+    if (!warp_wait(&C.scale_full[slot], (tile / SCALE_SLOTS) & 1, C, status)) break;
+    const uint2 four = C.scales[slot][row];
+    const float4 powers = C.powers[tile % POWER_SLOTS];
     if (!warp_wait(&C.k_empty[ks], ((tile / Y::KS) & 1) ^ 1, C, status)) break;
-    float2 key = Pair<T>::unpack(four.x), value = Pair<T>::unpack(four.y);
-    if (note >= 0) {
-      // values that some rows do not see: those that are not finite are noted and become zeros
-      const bool bad = !isfinite(value.x) || !isfinite(value.y);
-      const uint32_t word = __ballot_sync(FULL, bad && half == 0);
-      if (bad) value.x = value.y = 0.0f;
-      uint32_t bits = 0;
-      if (__builtin_expect(word, 0)) {
-#pragma unroll
-        for (int x = 0; x < UNIT; ++x) bits |= ((word >> (2 * x)) & 1) << x;
-      }
-      if (lane == 0) odd[note] = static_cast<uint16_t>(bits);
-    }
-    // the unit's powers of two: a token's lanes have a key and a value
-    const float2 mine = half == 0 ? key : value;
-    float largest = fmaxf(fabsf(mine.y), fabsf(fmaf(15.0f, mine.x, mine.y)));
-#pragma unroll
-    for (int o = 2; o < 32; o *= 2) largest = fmaxf(largest, __shfl_xor_sync(FULL, largest, o));
-    const int e = power_above(largest), ek = __shfl_sync(FULL, e, 0), ev = __shfl_sync(FULL, e, 1);
-    // The last tile that had this place is done with: the warp has waited for the values before this tile's, and so for
-    // products that came after its weights.
-    if (lane == 0) C.units[tile % UNIT_BUFFERS][in_tile] = make_float4(P.scale2 * power2(ek), static_cast<float>(ev), power2(-ev), 0.0f);
-    unpack(k_ring + ks * Y::KV_BYTES, key_words, key, power2(-ek));
+    unpack(k_ring + ks * Y::KV_BYTES, key_words, Pair<T>::unpack(four.x), powers.w);
     warp_arrive(&C.k_full[ks]);
     if (!warp_wait(&C.v_empty[vs], ((tile / Y::VS) & 1) ^ 1, C, status)) break;
-    unpack(v_ring + vs * Y::KV_BYTES, value_words, value, power2(-ev));
+    unpack(v_ring + vs * Y::KV_BYTES, value_words, Pair<T>::unpack(four.y), powers.z);
     warp_arrive(&C.v_full[vs]);
+    warp_arrive(&C.scale_empty[slot]);  // so late, as the notes and the powers of the tiles behind it rest on it
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -210,6 +281,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend4_kernel(const __grid_consta
       mbar_init(&C.k_empty[i], 1);
       mbar_init(&C.v_full[i], UNITS);
       mbar_init(&C.v_empty[i], 1);
+    }
+    for (int i = 0; i < SCALE_SLOTS; ++i) {
+      mbar_init(&C.scale_full[i], 1);
+      mbar_init(&C.scale_empty[i], UNITS);
     }
     mbar_init(&C.q_full, 1);
     mbar_init(&C.q_empty, 1);
@@ -252,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend4_kernel(const __grid_consta
       __syncwarp();
       mbar_wait(&C.drain, 0);
     } else if (warp == HELPERS + 1) {
-      side_role<T, D, PAIR>(P, &mq, C, smem_u32(smem), v_ring);
+      scale_role<T, D, PAIR>(P, &mq, C, smem_u32(smem));
     } else {
       unpack_role<T, D, PAIR>(P, C, k_ring, v_ring, raw, warp - HELPERS - 2);
     }

@@ -46,9 +46,10 @@
 // 8 bits of bf16 for keys, values and weights, outputs were 3 times as far from the exact ones as
 // their own rounding (and with codes multiplied as they are, scales and zeros applied to each score
 // and weight in the softmax, a tree of 64 took 439 us).  Powers of two keep them in
-// range: one for a row of queries; for the keys and for the values of each 16 tokens, which go
+// range: one for a row of queries; for the keys and for the values of each tile, which go
 // back in with the scores, the values' into the exponent of the weights; the weights' reference
-// so follows scores times values.
+// so follows scores times values.  (Powers of two for 16 tokens cost 8 times the operations
+// beside the weights: a tree of 61 nodes after 4500 tokens, 64 sequences, 287 us instead of 252.)
 //
 // Tokens a row does not see get S = -inf.  Their values enter the product
 // with weight zero, so in tiles that not every row sees whole, infinities and
@@ -84,11 +85,14 @@ namespace {
 constexpr int PANEL_BYTES = TILE * 128;         // 128 rows of 64 elements
 constexpr int MAX_SLOTS = CODES ? 3 : 5;        // of a ring
 constexpr int MASKED_TILES = SPEC_TREE_MAX_NODES / TILE + 2;
-// Segments whose notes on values are held.  A side warp waits for the products of the
-// segment before; unpacking warps are ahead of them by a ring of values, whose last
-// tile's product means that the softmax is done with the segment before that tile's.
-constexpr int ODD_BUFFERS = CODES ? MAX_SLOTS + 1 : 3, UNIT_BUFFERS = CODES ? MAX_SLOTS + 1 : 1;
-constexpr int UNIT = 16, UNITS = TILE / UNIT;   // tokens that are unpacked together, and have one factor
+// Codes: tiles whose scales and zeros are held for the unpacking warps, and whose powers
+// of two for the softmax, which is a ring of values behind those.
+constexpr int SCALE_SLOTS = CODES ? 6 : 1, POWER_SLOTS = CODES ? SCALE_SLOTS + MAX_SLOTS + 1 : 1;
+// Segments whose notes on values are held.  A side warp of values waits for the products
+// of the segment before.  One of scales is ahead by what is held of them and by a ring
+// of values; a tile's product with the values means that the softmax is done with the
+// segments before that tile's.
+constexpr int ODD_BUFFERS = CODES ? POWER_SLOTS + 1 : 3;
 // Two softmax warpgroups and one of helpers, or two: codes are unpacked by six warps.
 constexpr int THREADS = (CODES ? 4 : 3) * TILE;
 // A softmax thread holds a row of 128 scores in registers: of those that each thread
@@ -129,9 +133,11 @@ struct Control : Deal<THREADS / 32> {
   int abort;
   uint32_t odd[ODD_BUFFERS][MASKED_TILES * (TILE / 32)];  // tokens with a value that is not finite, by segment
   uint8_t up[2][SPEC_TREE_MAX_NODES];           // node minus parent, by segment modulo 2; 0: none, 255: more
-  // codes, for each unit of a tile, by tile: what its products with the keys are to be
-  // multiplied by; e and 2^-e, its values being multiplied by the latter
-  float4 units[UNIT_BUFFERS][UNITS];
+  uint2 scales[CODES ? SCALE_SLOTS : 1][CODES ? TILE : 1];  // codes: a token's four numbers
+  // codes, by tile: what its products with the keys are to be multiplied by; e and 2^-e, its values being multiplied by
+  // the latter; what its keys are
+  float4 powers[POWER_SLOTS];
+  uint64_t scale_full[SCALE_SLOTS], scale_empty[SCALE_SLOTS];
   uint64_t q_ready;  // codes: queries have been put in order
   union {
     float2 pair[TILE];         // the odd tiles' (reference, sum)
@@ -376,8 +382,37 @@ __device__ __forceinline__ bool any_odd(const uint4* row, int rotate) {
   return isnan(__low2float(acc)) || isnan(__high2float(acc));
 }
 
-// One warp, ahead of the softmax: an item's queries and its nodes' parents into
-// shared memory, and, unless they are made of codes, the values of tiles that not every row sees whole: those
+// A warp: an item's queries and its nodes' parents into shared memory.
+template <int D, bool PAIR>
+__device__ __forceinline__ bool ask_queries(const Plan& P, const CUtensorMap* mq, Control& C, uint32_t q_smem, const Segment& s,
+                                            uint32_t segment) {
+  using Y = Layout<D, PAIR>;
+  if (!warp_wait(&C.q_empty, (segment & 1) ^ 1, C, P.L.status)) return false;
+  const int node = node_of_row(P, s.row0);
+  if (elect()) {
+    mbar_expect_more(&C.q_full, Y::HALVES * Y::PANELS * P.q_box * P.group * 128);
+#pragma unroll
+    for (int h = 0; h < Y::HALVES; ++h)
+#pragma unroll
+      for (int p = 0; p < Y::PANELS; ++p)
+        tile_g2s(q_smem + h * Y::KV_BYTES + p * PANEL_BYTES, mq, p * PANEL, s.head * P.group, node + h * P.q_box, s.b,
+                 &C.q_full);
+  }
+  __syncwarp();
+  if (P.L.nodes.parent) {
+    const int32_t* parent = P.L.nodes.parent + static_cast<int64_t>(s.b) * P.L.nodes.stride;
+#pragma unroll 2
+    for (int x = threadIdx.x % 32; x < s.cnt; x += 32) {
+      const int up = parent[x];
+      C.up[segment % 2][x] = static_cast<uint8_t>(up < 0 || up >= x ? 0 : min(x - up, 255));
+      if (up >= x) set_status(P.L.status, SPEC_TREE_S_NODES);
+    }
+  }
+  warp_arrive(&C.q_full);
+  return true;
+}
+
+// One warp, ahead of the softmax: queries and parents, and the values of tiles that not every row sees whole: those
 // past the item's end and those that are not finite become zeros.  It passes
 // every slot of the values' ring, so that its waits keep to the ring's phases.
 template <typename T, int D, bool PAIR>
@@ -391,31 +426,9 @@ __device__ __forceinline__ void side_role(const Plan& P, const CUtensorMap* mq, 
   uint32_t segment = 0, n = 0, asked = 0;  // segments, tiles, segments whose queries have been asked for so far
   bool ok = true;
   for (; ok && walk.next(P); ++segment) {
-    ok = warp_wait(&C.q_empty, (segment & 1) ^ 1, C, status);
+    ok = ask_queries<D, PAIR>(P, mq, C, q_smem, s, segment);
     if (!ok) break;
-    const int node = node_of_row(P, s.row0);
-    if (elect()) {
-      mbar_expect_more(&C.q_full, Y::HALVES * Y::PANELS * P.q_box * P.group * 128);
-#pragma unroll
-      for (int h = 0; h < Y::HALVES; ++h)
-#pragma unroll
-        for (int p = 0; p < Y::PANELS; ++p)
-          tile_g2s(q_smem + h * Y::KV_BYTES + p * PANEL_BYTES, mq, p * PANEL, s.head * P.group, node + h * P.q_box, s.b,
-                   &C.q_full);
-    }
-    __syncwarp();
-    if (P.L.nodes.parent) {
-      const int32_t* parent = P.L.nodes.parent + static_cast<int64_t>(s.b) * P.L.nodes.stride;
-#pragma unroll 2
-      for (int x = lane; x < s.cnt; x += 32) {
-        const int up = parent[x];
-        C.up[segment % 2][x] = static_cast<uint8_t>(up < 0 || up >= x ? 0 : min(x - up, 255));
-        if (up >= x) set_status(status, SPEC_TREE_S_NODES);
-      }
-    }
-    warp_arrive(&C.q_full);
     asked = segment + 1;
-    if (CODES) continue;
 
     const int first_masked = s.clear / TILE;
     for (int j = s.first; j < s.last; ++j, ++n) {
@@ -671,28 +684,17 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
         for (int c = 0; c < TILE / 32; ++c) tmem_ld32(tm_s + c * 32, x + c * 32);
         tmem_wait_ld();
         float top;
-        const float4* units = C.units[(before + j - s.first) % UNIT_BUFFERS];
-        if (CODES) {
-          top = -INFINITY;
+        const float4 power = C.powers[CODES ? (before + j - s.first) % POWER_SLOTS : 0];
+        // a zero would make NaN of the -inf of what is not seen
+        const float scale = CODES ? fmaxf(power.x * factor, 1e-37f) : P.scale2;
+        float top8[8];
 #pragma unroll
-          for (int u = 0; u < UNITS; ++u) {
-            const float4 unit = units[u];
-            const float up = fmaxf(unit.x * factor, 1e-37f);  // a zero would make NaN of the -inf of what is not seen
-            float most = fmaxf(__uint_as_float(x[u * UNIT]), __uint_as_float(x[u * UNIT + 1]));
+        for (int c = 0; c < 8; ++c) top8[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
 #pragma unroll
-            for (int c = 2; c < UNIT; c += 2)
-              most = max3(most, __uint_as_float(x[u * UNIT + c]), __uint_as_float(x[u * UNIT + c + 1]));
-            top = fmaxf(top, fmaf(most, up, unit.y));
-          }
-        } else {
-          float top8[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) top8[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
-#pragma unroll
-          for (int c = 16; c < TILE; c += 2)
-            top8[c / 2 % 8] = max3(top8[c / 2 % 8], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-          top = P.scale2 * fmaxf(max3(max3(top8[0], top8[1], top8[2]), top8[3], top8[4]), max3(top8[5], top8[6], top8[7]));
-        }
+        for (int c = 16; c < TILE; c += 2)
+          top8[c / 2 % 8] = max3(top8[c / 2 % 8], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+        top = scale * fmaxf(max3(max3(top8[0], top8[1], top8[2]), top8[3], top8[4]), max3(top8[5], top8[6], top8[7]));
+        if (CODES) top += power.y;
         const bool grow = live && top > ref + LAZY;
         if (j < s.first + EACH) {
           ref = top;
@@ -711,30 +713,18 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
           }
         }
         const float sub = ref == -INFINITY ? 0.0f : ref - SHIFT;
-        const F2 scale2(P.scale2, P.scale2), shift2(-sub, -sub);
-        F2 by = scale2, plus = shift2;
+        const float shift = CODES ? power.y - sub : -sub;
+        const F2 scale2(scale, scale), shift2(shift, shift);
         F2 part[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) part[c] = F2(0.0f, 0.0f);
         auto weigh = [&](int c) {
           float a, b;
-          if (CODES && c % UNIT == 0) {  // read again: kept, they would cost the registers that there are not
-            const float4 unit = units[c / UNIT];
-            a = fmaxf(unit.x * factor, 1e-37f), b = unit.y - sub;
-            by = F2(a, a), plus = F2(b, b);
-          }
-          fma2(F2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), by, plus).get(a, b);
+          fma2(F2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), scale2, shift2).get(a, b);
           a = ex2(a);
           b = ex2(b);
           part[c / 2 % 4] = add2(part[c / 2 % 4], F2(a, b));
           x[c / 2] = Pair<W>::pack(a, b);
-          if (CODES && c % UNIT == UNIT - 2) {
-            // a unit's weights, without its values' power of two
-            add2(add2(part[0], part[1]), add2(part[2], part[3])).get(a, b);
-            sum = fmaf(a + b, units[c / UNIT].z, sum);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) part[i] = F2(0.0f, 0.0f);
-          }
         };
 #pragma unroll
         for (int c = 0; c < EARLY; c += 2) weigh(c);
@@ -747,11 +737,9 @@ __device__ __forceinline__ void softmax_role(const Plan& P, Control& C, uint8_t*
         tmem_st32(tm_s + EARLY / 2, x + EARLY / 2);
         tmem_wait_st();
         tmem_fence_before();
-        if (!CODES) {
-          float a, b;
-          add2(add2(part[0], part[1]), add2(part[2], part[3])).get(a, b);
-          sum += a + b;
-        }
+        float a, b;
+        add2(add2(part[0], part[1]), add2(part[2], part[3])).get(a, b);
+        sum = CODES ? fmaf(a + b, power.z, sum) : sum + (a + b);
       } else {
         warp_arrive(&C.w_full[half][0]);
       }

@@ -37,7 +37,7 @@ def attend_bound(dtype, out, k_abs, q_k, floor_k, floor_v, mean_v, steps_v, D, t
     sum p 15 s (steps_v), those 2^-29 below the largest to its least step (2^-39 of the largest each); products of up to
     sum p 15 s + |z| are summed in float32.
     more rows: keys and values are rounded to f16's 11 bits, half a step 2^-11 of |k| (q_k: the largest scale * sum |q| |k|)
-    and of |v| (mean_v), and to 2^-25 of the largest element of 16 tokens (floor_k: the same sum with the largest element of
+    and of |v| (mean_v), and to 2^-25 of the largest element of a tile of 128 tokens (floor_k: the same sum with the largest element of
     all; floor_v: that of the values), D + 8 roundings of the products; the weights, times a power of two, to 2^-11.
     Both: an error e in the scores is a factor exp(2 e) between weights; sums over the tokens and the exponential
     cost (tokens + 16) 2^-23; then one rounding to dtype."""
