@@ -13,9 +13,9 @@
 // bounded it.)
 //
 // So queries and weights are f16 too, whatever the model's type.  Queries carry a
-// power of two that brings the call's largest element near f16's; weights times
-// values' scales one for each row, which goes down as larger scales come: both
-// keep at least f16's 11 bits down to 2^-29 of the largest.
+// power of two for each row, which brings its largest element near f16's; weights times
+// values' scales one too, which goes down as larger scales come: both
+// keep at least f16's 11 bits down to 2^-28 of the largest.
 //
 // Products are mma.sync, tokens (of keys) or elements (of values) in the rows and
 // the call's rows in the columns, so that 8 rows fill a product: the codes go
@@ -290,47 +290,45 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
     uint32_t q[NT][2 * KEY_WORDS][2];
     float sum_q[NT][2];  // of rows 2 t and 2 t + 1
     int node[NT][2];     // theirs, among those of the call
-    float scale_q;       // what a score's codes are multiplied by beside their scale
+    float scale_q[NT][2];  // what their scores' codes are multiplied by beside their scale
     {
-      uint4 raw[NT][KEY_WORDS];
-      float largest = 0.0f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int row = nt * 8 + g, i = node_of_row(P, row);
         const T* from = static_cast<const T*>(P.L.q.data) + s.b * P.L.q.tree_stride + i * P.L.q.node_stride +
                         (static_cast<int64_t>(s.head) * P.group + row - i * P.group) * P.L.q.head_stride + t * 8 * KEY_WORDS;
-        float sum = 0.0f;
+        uint4 raw[KEY_WORDS];
+        float sum = 0.0f, largest = 0.0f;
 #pragma unroll
         for (int w = 0; w < KEY_WORDS; ++w) {
-          raw[nt][w] = row < P.rows ? *reinterpret_cast<const uint4*>(from + 8 * w) : make_uint4(0, 0, 0, 0);
+          raw[w] = row < P.rows ? *reinterpret_cast<const uint4*>(from + 8 * w) : make_uint4(0, 0, 0, 0);
           float e[8];
-          unpack8<T>(raw[nt][w], e);
+          unpack8<T>(raw[w], e);
 #pragma unroll
           for (int d = 0; d < 8; ++d) sum += e[d], largest = fmaxf(largest, fabsf(e[d]));
         }
-        sum += __shfl_xor_sync(FULL, sum, 1);
-        sum += __shfl_xor_sync(FULL, sum, 2);
+#pragma unroll
+        for (int o = 1; o < 4; o *= 2) {
+          sum += __shfl_xor_sync(FULL, sum, o);
+          largest = fmaxf(largest, __shfl_xor_sync(FULL, largest, o));
+        }
+        const int exponent = min(exponent_above(largest), 126);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           sum_q[nt][e] = __shfl_sync(FULL, sum, (2 * t + e) * 4) * scale2;
+          scale_q[nt][e] = scale2 * power2(__shfl_sync(FULL, exponent, (2 * t + e) * 4) - 14) * 16777216.0f;
           node[nt][e] = node_of_row(P, nt * 8 + 2 * t + e);
         }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o /= 2) largest = fmaxf(largest, __shfl_xor_sync(FULL, largest, o));
-      const int e = min(exponent_above(largest), 126);
-      const float up = power2(14 - e), up16 = power2(10 - e);
-      scale_q = scale2 * power2(e - 14) * 16777216.0f;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        const float up = power2(14 - exponent), up16 = power2(10 - exponent);
 #pragma unroll
         for (int w = 0; w < KEY_WORDS; ++w) {
           float x[8];
-          unpack8<T>(raw[nt][w], x);
+          unpack8<T>(raw[w], x);
 #pragma unroll
           for (int d = 0; d < 4; ++d)
             q[nt][2 * w + d / 2][d % 2] = Pair<__half>::pack(x[d] * (d % 2 ? up16 : up), x[d + 4] * (d % 2 ? up16 : up));
         }
+      }
     }
     float acc[NT][MT][4];               // outputs of elements x rows
     float sum[NT][2], middle[NT][2];    // of this lane's tokens: weights, weights times zeros
@@ -355,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
       for (int h = 0; h < 4; ++h) {
         const uint2 w = *reinterpret_cast<const uint2*>(at + 2 * F::CODE_BYTES + (g + 8 * h) * 8);
         const float2 a = Pair<T>::unpack(w.x), b = Pair<T>::unpack(w.y);
-        ks[h] = a.x * scale_q, kz[h] = a.y, vs[h] = b.x, vz[h] = b.y;
+        ks[h] = a.x, kz[h] = a.y, vs[h] = b.x, vz[h] = b.y;
       }
       float dot[NT][2][4];
 #pragma unroll
@@ -384,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, Few<D, NT>::CTAS) attend4_few_kernel(
         float x[4][2];
         bool seen[4][2];
         auto score = [&](int h, int e, float less) {
-          return fmaf(ks[h], dot[nt][h / 2][h % 2 * 2 + e], fmaf(kz[h], sum_q[nt][e], -less));
+          return fmaf(ks[h] * scale_q[nt][e], dot[nt][h / 2][h % 2 * 2 + e], fmaf(kz[h], sum_q[nt][e], -less));
         };
 #pragma unroll
         for (int h = 0; h < 4; ++h)
