@@ -57,7 +57,7 @@ __device__ __forceinline__ uint4 unpacked(uint32_t w, __half2 s, __half2 z) {
 }
 
 // One warp: the tiles' scales and zeros, LEAD tiles ahead of their powers of two, which
-// are the keys' and values' next above the largest of the tile's 128 tokens; which values
+// bring the largest element of the tile's 128 tokens, of keys and of values, near f16's; which values
 // are not finite, where some rows may not see them, and zeros in their place; queries and
 // parents.
 template <typename T, int D, bool PAIR>
@@ -144,8 +144,9 @@ __device__ __forceinline__ void scale_role(const Plan& P, const CUtensorMap* mq,
         const uint32_t word = __reduce_or_sync(0xffu << (lane / 8 * 8), bad << (lane % 8 * EACH));
         if (lane % 8 == 0) C.odd[segment % ODD_BUFFERS][(j - s.clear / TILE) * (TILE / 32) + lane / 8] = word;
       }
-      const int ek = power_above(__uint_as_float(__reduce_max_sync(FULL, __float_as_uint(key))));
-      const int ev = power_above(__uint_as_float(__reduce_max_sync(FULL, __float_as_uint(value))));
+      // up to 2^14, which f16 holds with room for the roundings: what is 2^-28 as large keeps its 11 bits
+      const int ek = -14 + power_above(__uint_as_float(__reduce_max_sync(FULL, __float_as_uint(key))));
+      const int ev = -14 + power_above(__uint_as_float(__reduce_max_sync(FULL, __float_as_uint(value))));
       if (lane == 0)
         C.powers[n % POWER_SLOTS] = make_float4(P.scale2 * power2(ek), static_cast<float>(ev), power2(-ev), power2(-ek));
       warp_arrive(&C.scale_full[n % SCALE_SLOTS]);

@@ -565,7 +565,7 @@ __device__ __forceinline__ float power2(int e) { return __uint_as_float(static_c
 
 // The least e with x <= 2^e, from -80 to 126.
 __device__ __forceinline__ int power_above(float x) {
-  return min(static_cast<int>((__float_as_uint(fmaxf(x, power2(-80))) + 0x007fffffu) >> 23) - 127, 126);
+  return min(static_cast<int>((__float_as_uint(fmaxf(x, power2(-66))) + 0x007fffffu) >> 23) - 127, 126);
 }
 
 // Whether the row's node sees one of the tokens of the segment that `odd` names.

@@ -627,7 +627,7 @@ int spec_tree_kv4_append(int B, const spec_tree_kv4_t* kv, int layer, const spec
  * powers of two) are rounded to f16's 11 bits, whatever kv.dtype.  Calls of up to
  * SPEC_TREE_KV4_FEW_ROWS rows (nodes times query heads per key head) multiply the
  * codes as they are and apply scales and zeros in float32.  Calls of more rows
- * round keys and values to 11 bits, and to 2^-25 of the largest element of the 128
+ * round keys and values to 11 bits, and to 2^-34 of the largest element of the 128
  * tokens (from a multiple of 128 on) that theirs is one of.  A key or value that
  * stands for NaN makes NaN of every row that sees it, whatever its weight, and has
  * no influence on the others.

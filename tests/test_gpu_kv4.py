@@ -215,6 +215,41 @@ def test_unseen_nodes_have_no_influence(Hq, N):
                     assert torch.equal(got[b, n], clean[b, n]), (what, value, b, n)
 
 
+@pytest.mark.parametrize("Hq,N,D", [(8, 4, 128), (2, 9, 64), (4, 4, 64), (8, 61, 128), (8, 8, 64), (2, 40, 128)])
+@pytest.mark.parametrize("value", [INF, NAN, 3e38, -1e30])
+def test_rows_have_no_influence_on_each_other(Hq, N, D, value):
+    """What one node's queries hold leaves the others' outputs as they are, bit by bit."""
+    c = kv_cases.make(131, [37, 150, 700], N, 2, D, 16, stale=NAN)
+    q = _queries(132, c, Hq)
+    clean, _ = _run_attend(c, q)
+    for node in (0, N - 1):
+        hit = q.clone()
+        hit[:, node] = value
+        got, status = _run_attend(c, hit)
+        keep = [n for n in range(N) if n != node]
+        assert status == 0 and torch.equal(got[:, keep], clean[:, keep])
+
+
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("Hq,N", [(8, 4), (8, 61)])
+def test_a_large_unseen_vector_costs_no_precision(Hq, N, what):
+    """A node's key or value 2^14 times the others', of up to 2^2: its neighbours are rounded to 2^-34 of it at most, 2^-18, which
+    is under an eighth of their own half step 2^-11 of what is 2^-4 or larger, and the others' part in a mean is small."""
+    c = kv_cases.make(133, [37, 150], N, 2, 128, 16, stale=NAN)
+    q = _queries(134, c, Hq)
+    codes = kv4_cases.quantised(c)
+    want, bound = _expected(c, q, codes, 128 ** -0.5)
+    hit = N - 1
+    x = getattr(c, what).clone()
+    for b in range(2):
+        s = int(c.seq_len[b]) + hit
+        x[0, int(c.table[b, s // 16]), s % 16] *= 2.0 ** 14
+    got, status = _run_attend(kv_cases.dataclasses.replace(c, **{what: x}), q)
+    keep = [n for n in range(N) if n != hit]
+    err = np.abs(got.double().numpy() - want)[:, keep]
+    assert status == 0 and (err <= 1.125 * bound[:, keep]).all()
+
+
 @pytest.mark.parametrize("N,lens", [(1, [300]), (1, [6000]), (40, [300]), (40, [6000]), (150, [200])])
 def test_nan_counts_whatever_its_weight(N, lens):
     """One element of one token's value that is not finite makes its vector NaN, and with it every row that sees it,
