@@ -14,7 +14,11 @@ would around real ones:
   commit        spec_tree_kv_commit moves the accepted path's keys and values
                 behind the committed tokens; the drafter appends them as a chain
 
-    python examples/tree_decode.py [--rounds 12] [--batch 4]
+With --bits 4 both models keep their keys and values in 4 bits (the spec_tree_kv4_*
+calls), in pages that a pool hands out as sequences grow and takes back from the
+nodes that were not accepted (spec_tree_kv_reserve, spec_tree_kv_release).
+
+    python examples/tree_decode.py [--rounds 12] [--batch 4] [--bits 4]
 """
 from __future__ import annotations
 
@@ -32,7 +36,7 @@ class Model:
     """A pre-norm transformer of random weights over a paged cache: grouped heads, normalised queries and keys."""
 
     def __init__(self, seed, B, context, vocab, layers, width=256, heads=8, kv_heads=2, head_dim=64, page=16,
-                 max_nodes=64, embedding=None, device="cuda"):
+                 max_nodes=64, embedding=None, device="cuda", bits=16):
         g = torch.Generator(device=device).manual_seed(seed)
 
         def mat(*shape):
@@ -45,40 +49,55 @@ class Model:
                             qw=torch.ones(head_dim, device=device).bfloat16() * 2,
                             kw=torch.ones(head_dim, device=device).bfloat16()) for _ in range(layers)]
         pages = -(-context // page)
-        shape = (layers, B * pages, page, kv_heads, head_dim)
-        # a real server hands out pages as sequences grow; here each sequence owns a shuffled set
-        table = torch.randperm(B * pages, generator=torch.Generator().manual_seed(seed)).int().view(B, pages)
-        self.cache = F.KVCache(torch.zeros(shape, dtype=torch.bfloat16, device=device),
-                               torch.zeros(shape, dtype=torch.bfloat16, device=device), table.to(device),
-                               torch.zeros(B, dtype=torch.int32, device=device))
+        lengths = torch.zeros(B, dtype=torch.int32, device=device)
+        if bits == 4:
+            self.pool = F.PagePool(B * pages, page, B, pages, device=device)
+            self.cache = F.KVCache4.zeros(layers, B * pages, page, kv_heads, head_dim, self.pool.page_table, lengths)
+            self.append, self.attend, self.commit = F.spec_tree_kv4_append, F.spec_tree_kv4_attend, F.spec_tree_kv4_commit
+        else:
+            self.pool = None
+            shape = (layers, B * pages, page, kv_heads, head_dim)
+            # without a pool, each sequence owns a shuffled set of pages from the start
+            table = torch.randperm(B * pages, generator=torch.Generator().manual_seed(seed)).int().view(B, pages)
+            self.cache = F.KVCache(torch.zeros(shape, dtype=torch.bfloat16, device=device),
+                                   torch.zeros(shape, dtype=torch.bfloat16, device=device), table.to(device), lengths)
+            self.append, self.attend, self.commit = F.spec_tree_kv_append, F.spec_tree_attend, F.spec_tree_kv_commit
         self.rope = F.rope_table(context, head_dim, 10000.0, device)
         self.workspace = F.AttendWorkspace(B, max_nodes, heads, kv_heads, head_dim, device)
 
     def step(self, tokens, status, tree=None, begin=0):
         """Logits [B][N][vocab] of nodes begin .. begin + N - 1, whose entries are appended to the cache."""
         B, N = tokens.shape
+        if self.pool:
+            F.spec_tree_kv_reserve(self.pool, self.cache.seq_len, begin + N, status)
         x = self.embedding[tokens.clamp_min(0).long()].float()
         norm = lambda y: (y * torch.rsqrt((y * y).mean(-1, keepdim=True) + 1e-6)).bfloat16()  # noqa: E731
         for layer, w in enumerate(self.blocks):
             qkv = (norm(x) @ w["qkv"].T).view(B, N, self.heads + 2 * self.kv_heads, self.head_dim)
             q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], dim=2)
-            F.spec_tree_kv_append(self.cache, layer, q, k, v, q, self.rope, status, tree=tree, node_begin=begin,
-                                  q_weight=w["qw"], k_weight=w["kw"])
+            self.append(self.cache, layer, q, k, v, q, self.rope, status, tree=tree, node_begin=begin, q_weight=w["qw"],
+                        k_weight=w["kw"])
             out = torch.empty((B, N, self.heads, self.head_dim), dtype=q.dtype, device=q.device)
-            F.spec_tree_attend(self.cache, layer, q, out, self.workspace, status, tree=tree, node_begin=begin)
+            self.attend(self.cache, layer, q, out, self.workspace, status, tree=tree, node_begin=begin)
             x = x + (out.view(B, N, -1) @ w["out"].T).float()
             x = x + (torch.nn.functional.silu(norm(x) @ w["up"].T) @ w["down"].T).float()
         return norm(x) @ self.embedding.T * self.embedding.shape[1] ** -0.5
 
+    def keep(self, lengths, status):
+        """The cache's lengths from now on; pages behind them go back to the pool."""
+        self.cache.set_lengths(lengths)
+        if self.pool:
+            F.spec_tree_kv_release(self.pool, lengths, status)
 
-def decode(B=4, rounds=12, vocab=4096, prompt_len=40, seed=0, K=4, W=4, depth=4, R=20, layers=2):
+
+def decode(B=4, rounds=12, vocab=4096, prompt_len=40, seed=0, K=4, W=4, depth=4, R=20, layers=2, bits=16):
     """(target, tokens, accepted): the target model, each sequence's tokens (the last one is not cached yet) and
     the accept lengths of every round."""
     params = F.Params(K=K, m=1, W=W, depth=depth, R=R, temperature=1.0, support=64)
     context = prompt_len + rounds * (depth + 1) + R + 1
     max_nodes = max(R + 1, 1 + (depth - 1) * W, prompt_len)
-    target = Model(seed, B, context, vocab, layers, max_nodes=max_nodes)
-    drafter = Model(seed + 1, B, context, vocab, 1, max_nodes=max_nodes, embedding=target.embedding)
+    target = Model(seed, B, context, vocab, layers, max_nodes=max_nodes, bits=bits)
+    drafter = Model(seed + 1, B, context, vocab, 1, max_nodes=max_nodes, embedding=target.embedding, bits=bits)
     dev = "cuda"
     g = torch.Generator(device=dev).manual_seed(seed + 2)
     uniform = lambda *shape: torch.rand(shape, generator=g, device=dev)  # noqa: E731
@@ -95,8 +114,8 @@ def decode(B=4, rounds=12, vocab=4096, prompt_len=40, seed=0, K=4, W=4, depth=4,
     tokens, accepted = [row.tolist() for row in prompt], []
 
     for _ in range(rounds):
-        target.cache.set_lengths(lengths)
-        drafter.cache.set_lengths(lengths)
+        target.keep(lengths, status)
+        drafter.keep(lengths, status)
         # drafting: nodes in the order they are expanded, layer l's at 1 + (l - 1) W
         nodes = 1 + (depth - 1) * W
         parent = torch.full((B, nodes), -1, dtype=torch.int32, device=dev)
@@ -120,7 +139,7 @@ def decode(B=4, rounds=12, vocab=4096, prompt_len=40, seed=0, K=4, W=4, depth=4,
         F.spec_tree_verify(params, vocab, logits.contiguous(), tree, uniform(B, depth, K), uniform(B), out.accept_len,
                            out.out_tok, out.out_node, out.margins, status)
         # commit: the target's entries are moved, the drafter makes its own from the accepted tokens
-        F.spec_tree_kv_commit(target.cache, out.accept_len, out.out_node, new_len, status)
+        target.commit(target.cache, out.accept_len, out.out_node, new_len, status)
         chain = torch.cat([root[:, None], out.out_tok[:, :depth]], 1)
         drafter.step(chain, status, F.NodeArrays(n_nodes=out.accept_len + 1))
         lengths, new_len = new_len, lengths
@@ -128,10 +147,10 @@ def decode(B=4, rounds=12, vocab=4096, prompt_len=40, seed=0, K=4, W=4, depth=4,
         for b, (n, row) in enumerate(zip(out.accept_len.tolist(), out.out_tok.tolist())):
             tokens[b] += row[:n + 1]
         accepted.append(out.accept_len.tolist())
+    target.keep(lengths, status)
     torch.cuda.synchronize()
     if int(status.item()):
         raise RuntimeError(f"status {int(status.item())}")
-    target.cache.set_lengths(lengths)
     return target, tokens, accepted
 
 
@@ -139,8 +158,9 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--rounds", type=int, default=12)
     ap.add_argument("--batch", type=int, default=4)
+    ap.add_argument("--bits", type=int, default=16, choices=(16, 4), help="of the caches' keys and values")
     args = ap.parse_args()
-    _, tokens, accepted = decode(B=args.batch, rounds=args.rounds)
+    _, tokens, accepted = decode(B=args.batch, rounds=args.rounds, bits=args.bits)
     total = sum(map(sum, accepted))
     print(f"{args.batch} sequences, {args.rounds} target passes: {total / args.batch / args.rounds:.2f} tokens accepted "
           f"per tree, {len(tokens[0])} tokens in the first sequence")

@@ -782,3 +782,42 @@ def test_a_step_in_a_graph():
         assert torch.equal(plain["pool"].page_table, graphed["pool"].page_table)
         assert torch.equal(plain["cache"].k, graphed["cache"].k) and torch.equal(plain["cache"].scale, graphed["cache"].scale)
         assert (plain["pool"].held == (plain["lens"] + page - 1) // page).all()
+
+
+# ------------------------------------------------------------- all together ---
+
+def test_a_loop_of_drafting_verification_and_commit():
+    """Rounds over caches in 4 bits, with pages from a pool: the first layer's entries of the committed tokens are those of a
+    plain pass over them, up to half a step of each side's codes, two roundings to bf16 in the layer and one as they are read
+    back (half a step, 2^-8, each); every page belongs to one sequence or is free."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import tree_decode
+    target, tokens, accepted = tree_decode.decode(B=3, rounds=8, bits=4)
+    assert max(map(max, accepted)) > 0
+    lengths = target.cache.seq_len.tolist()
+    assert lengths == [len(t) - 1 for t in tokens]
+    pool, free = target.pool, int(target.pool.n_free.item())
+    assert pool.held.tolist() == [-(-n // pool.page_size) for n in lengths]
+    mine = [target.pool.page_table[b, :n].tolist() for b, n in enumerate(pool.held.tolist())]
+    assert sorted(sum(mine, []) + pool.free[:free].tolist()) == list(range(pool.n_pages))
+    status = _status()
+
+    def entries(model, b, n):
+        out = [torch.empty((3, max(lengths), 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        counts = torch.zeros(3, dtype=torch.int32, device="cuda")
+        counts[b] = n  # the others may be shorter, without pages so far
+        B.spec_tree_kv4_read(model.cache, 0, *out, status, counts=counts)
+        slots = torch.arange(n, device="cuda")
+        pages = model.cache.page_table[b].long()[slots // pool.page_size]
+        steps = model.cache.scale[0, pages, :, slots % pool.page_size].double()
+        return [(x[b, :n].double(), steps[..., 2 * i, None]) for i, x in enumerate(out)]
+
+    for b, row in enumerate(tokens):
+        plain = tree_decode.Model(0, 3, target.rope.shape[0], 4096, 2, max_nodes=256, bits=4)
+        plain.step(torch.tensor([row[:-1]] * 3, device="cuda"), status)
+        for (a, sa), (c, sc) in zip(entries(target, b, lengths[b]), entries(plain, b, lengths[b])):
+            largest = torch.maximum(a.abs(), c.abs()).amax(-1, keepdim=True)
+            assert bool(((a - c).abs() <= (sa + sc) / 2 + 6 * 2.0 ** -8 * largest).all())
+    assert int(status.item()) == 0
