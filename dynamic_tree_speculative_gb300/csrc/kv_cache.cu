@@ -49,7 +49,7 @@ __device__ __forceinline__ float round_down(__half, float x) { return __half2flo
 // are their codes, and each lane gets (scale, zero).  The range over 15 and the
 // quotients are float32's, correctly rounded, so that ties fall as they are
 // defined to: of vectors of 16-bit numbers a few in a thousand elements lie
-// exactly between two codes.
+// exactly between two codes.  (By divisions 64 trees took 37 us instead of 27.)
 template <typename T, int LANES>
 __device__ __forceinline__ uint32_t quantise(const uint4 (&u)[2], uint32_t (&w)[2]) {
   const uint32_t in[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
@@ -67,14 +67,25 @@ __device__ __forceinline__ uint32_t quantise(const uint4 (&u)[2], uint32_t (&w)[
   const float s = round_down(T(), __fdiv_rn(range, 15.0f));
   // 1.5 * 2^23 + n holds n in its lowest bits, n rounded to the nearest even
   constexpr float MAGIC = 12582912.0f;
+  // A quotient rounded to the nearest as a division gives it, for all elements from one
+  // reciprocal (Markstein's correction): q is within 1.5 units of its last place of
+  // y / s, the remainder y - s q is exact, and q + remainder / s is off by 2^-23 of a
+  // unit before it is rounded.  y / s, of 24 bits over 11, is never half way between two
+  // numbers of 24 bits nor nearer to that than 2^-13 of a unit.  f keeps it in range.
+  const float f = s < 0x1p-60f ? 0x1p64f : s > 0x1p60f ? 0x1p-64f : 1.0f;
+  const float divisor = s * f, inverse = __frcp_rn(divisor), below = -(z * f);
+  auto code = [&](float x) {
+    const float y = fmaf(x, f, below), q = y * inverse;
+    return __float_as_uint(fminf(fmaf(fmaf(-divisor, q, y), inverse, q), 15.0f) + MAGIC);
+  };
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t sum = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 x = Pair<T>::unpack(in[4 * h + e]);
-      sum += __float_as_uint(fminf(__fdiv_rn(x.x - z, s), 15.0f) + MAGIC) << (8 * e);
-      sum += __float_as_uint(fminf(__fdiv_rn(x.y - z, s), 15.0f) + MAGIC) << (8 * e + 4);
+      sum += code(x.x) << (8 * e);
+      sum += code(x.y) << (8 * e + 4);
     }
     uint32_t magics = 0;  // the bits of MAGIC, shifted and added up alike
 #pragma unroll

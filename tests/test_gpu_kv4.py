@@ -470,12 +470,15 @@ def _vectors(seed, shape, dtype):
 
 
 def _check_append(seed, lens, N, Hq, Hkv, D, page, dtype="bf16", tree=True, begin=0, counts=None, norm=False, rot=None,
-                  interleaved=False, layout="head", layers=1, layer=0, in_place=False):
+                  interleaved=False, layout="head", layers=1, layer=0, in_place=False, powers=None):
     """Keys, values and queries are to the bit what the append into a 16-bit cache makes of them, quantised."""
     rot = D if rot is None else rot
     c = kv_cases.make(seed, lens, N, Hkv, D, page, dtype, tree=tree, begin=begin, counts=counts, layers=layers)
     q = _queries(seed, c, Hq)
     k, v = (_vectors(seed + i, (len(lens), N, Hkv, D), c.dtype) for i in (1, 2))
+    if powers is not None:  # a power of two for each token
+        gain = 2.0 ** torch.tensor(powers)[torch.arange(N) % len(powers)].double()[None, :, None, None]
+        k, v = ((x.double() * gain).to(c.dtype) for x in (k, v))
     g = torch.Generator().manual_seed(seed)
     qw, kw = [(1 + 0.2 * torch.randn(D, generator=g)).to(c.dtype).cuda() if norm else None for _ in range(2)]
     rope = B.rope_table(max(lens) + begin + N, rot, 10000.0) if rot else None
@@ -516,6 +519,18 @@ def test_append(dtype, D, rot, interleaved):
 ])
 def test_append_shapes(kw):
     _check_append(61, **kw)
+
+
+@pytest.mark.parametrize("dtype,powers", [("bf16", [-136, -131, -127, -124, -100, -64, -60, -57, -30, 30, 57, 62, 64, 100, 121]),
+                                          ("f16", [-24, -20, -17, -14, -10, 5, 11, 13])])
+def test_append_vectors_of_any_size(dtype, powers):
+    """Down to the types' least steps and up to their largest numbers; nothing is turned, which would round."""
+    _check_append(62, [9, 300], 45, 4, 2, 128, 16, dtype, rot=0, powers=powers)
+
+
+def test_append_many_vectors_of_many_ranges():
+    """Quotients are those of a division, whatever the step: 100000 vectors."""
+    _check_append(63, [0] * 20, 250, 1, 10, 64, 16, "bf16", rot=0, powers=[0])
 
 
 def test_append_reports_what_it_cannot_place():
