@@ -740,7 +740,7 @@ def spec_tree_kv4_read(cache: KVCache4, layer: int, k: torch.Tensor, v: torch.Te
 class PagePool:
     """The pages of a cache of B sequences (the spec_tree_pages_t of the C ABI): `page_table` [B][max_pages] is the
     cache's, `held` [B] counts each sequence's pages, the first n_free[0] of `free` are nobody's.  All int32 on one
-    device, made here (every page free, the lowest handed out first) or given."""
+    device, made here (every page free, the lowest handed out first) or given.  One call on a pool at a time."""
 
     def __init__(self, n_pages: int, page_size: int, B: int, max_pages: int, page_table: Optional[torch.Tensor] = None,
                  held: Optional[torch.Tensor] = None, free: Optional[torch.Tensor] = None,

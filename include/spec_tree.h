@@ -670,7 +670,8 @@ int spec_tree_kv4_read(int B, const spec_tree_kv4_t* kv, int layer, const int32_
  *   scratch:    [B + 1] int32, zero before the first call that uses it; every
  *               call leaves what the next one needs.
  * To begin: held all 0, free_pages any order of all pages, n_free n_pages.
- * Every page is in one place: one row's held part, or the free part.
+ * Every page is in one place: one row's held part, or the free part.  One call
+ * on a pool at a time, on one stream or on streams that wait for one another.
  */
 typedef struct spec_tree_pages_t {
   int32_t* page_table;
