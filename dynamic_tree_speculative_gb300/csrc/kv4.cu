@@ -13,7 +13,8 @@ constexpr int READ_THREADS = 128;
 // One thread per 16 bytes of a slot's codes, or per head's four scales and
 // zeros, in one layer; as in the cache of 16 bits it walks the path in ascending
 // order, COMMIT_BATCH steps at a time, loading a batch before storing it: step j
-// reads slot path[j] >= j, which only a step after j may write.
+// reads slot path[j] >= j, which only a step after j may write.  One path of one layer
+// takes 2.6 us, 16 of 32 layers 3.3 (1.7 MB): three dependent loads and a launch.
 template <typename W>
 __device__ __forceinline__ void move_path(uint8_t* base, const int64_t* src, const int64_t* dst, int steps, int shift) {
   for (int j0 = 0; j0 < steps; j0 += COMMIT_BATCH) {
@@ -80,7 +81,8 @@ __global__ void __launch_bounds__(COMMIT_THREADS) kv4_commit_kernel(const Commit
 }
 
 // One warp takes 256 / D vectors of keys, then of values, at a time: a lane four
-// bytes (8 codes) of one, which it writes as 16.
+// bytes (8 codes) of one, which it writes as 16.  3904 entries of 8 heads of 128 (20 MB):
+// 6.5 us, against 3.0 at the memory's rate; lookups before the loads are the rest.
 template <typename T, int D>
 __global__ void __launch_bounds__(READ_THREADS) kv4_read_kernel(const ReadLaunch L, int64_t vectors, int page_shift) {
   constexpr int LANES = D / 8;

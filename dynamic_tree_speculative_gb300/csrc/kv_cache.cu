@@ -49,7 +49,9 @@ __device__ __forceinline__ float round_down(__half, float x) { return __half2flo
 // are their codes, and each lane gets (scale, zero).  The range over 15 and the
 // quotients are float32's, correctly rounded, so that ties fall as they are
 // defined to: of vectors of 16-bit numbers a few in a thousand elements lie
-// exactly between two codes.  (By divisions 64 trees took 37 us instead of 27.)
+// exactly between two codes.  (By divisions 64 trees
+// of 61 nodes of 48 heads of 128, appended and read back, took 37 us instead of 27; the append
+// alone takes 17.8, into 16 bits 15.6.)
 template <typename T, int LANES>
 __device__ __forceinline__ uint32_t quantise(const uint4 (&u)[2], uint32_t (&w)[2]) {
   const uint32_t in[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};

@@ -441,6 +441,48 @@ def test_bad_parents_and_lengths_are_reported(N):
     assert status == B.S_NODES and (got[0] == 0).all()
 
 
+@pytest.mark.parametrize("Hq,Hkv,N", [(3, 1, 50), (128, 1, 3), (128, 1, 1), (64, 1, 9), (48, 16, 7), (48, 16, 1), (100, 1, 4),
+                                      (6, 6, 150), (16, 16, 16)])
+def test_group_sizes(Hq, Hkv, N):
+    c = kv_cases.make(149, [60, 140], N, Hkv, 64, 16, counts=[N, max(1, N - 2)], stale=NAN)
+    _check_attend(c, _queries(151, c, Hq))
+
+
+def test_chunk_of_a_group_that_does_not_divide_128():
+    c = kv_cases.make(152, [75, 300], 90, 1, 128, 32, tree=False, stale=NAN)
+    _check_attend(c, _queries(153, c, 7))
+
+
+@pytest.mark.parametrize("Hq,N", [(4, 3), (4, 40)])
+def test_f16_vectors_up_to_the_largest_number(Hq, N):
+    c = kv_cases.make(154, [50, 200], N, 2, 64, 16, "f16", stale=NAN)
+    v = (c.v.float() * 65504.0).clamp(-65504.0, 65504.0).to(c.dtype)
+    k = (c.k.float() * 8192.0).clamp(-65504.0, 65504.0).to(c.dtype)
+    c = kv_cases.dataclasses.replace(c, k=torch.where(torch.isfinite(c.k), k, c.k), v=torch.where(torch.isfinite(c.v), v, c.v))
+    _check_attend(c, _queries(155, c, Hq, 1.5 / 1024.0), scale=1.0 / 8)
+
+
+@pytest.mark.parametrize("N", [1, 30])
+def test_two_calls_at_once(N):
+    """Two streams, a workspace and a status word each: the bits of one call after the other."""
+    cases = [kv_cases.make(156 + i, [3000 + 700 * i, 90], N, 2, 128, 16, tree=N > 1) for i in range(2)]
+    qs = [_queries(160 + i, c, 8) for i, c in enumerate(cases)]
+    want = [_run_attend(c, q)[0] for c, q in zip(cases, qs)]
+    caches, nodes, qd = [_cache4(c) for c in cases], [_nodes(c) for c in cases], [q.cuda() for q in qs]
+    outs = [torch.full_like(q, NAN) for q in qd]
+    wss = [B.AttendWorkspace(2, N, 8, 2, 128) for _ in cases]
+    status = [_status() for _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                B.spec_tree_kv4_attend(caches[i], 0, qd[i], outs[i], wss[i], status[i], tree=nodes[i], stream=stream)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert int(status[i].item()) == 0 and torch.equal(outs[i].cpu(), want[i])
+
+
 # ------------------------------------------------------------------ append ---
 
 def _vectors(seed, shape, dtype):
