@@ -31,8 +31,9 @@ struct Raw {
   static constexpr int BYTES = 2 * CODE_BYTES;
 };
 
-__device__ __forceinline__ void copy_to_shared(uint32_t to, const void* from, bool there) {  // 16 bytes, or zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+// 16 bytes, or zeros; the L2 fetches no more than 64 around them, which may be another head's.
+__device__ __forceinline__ void copy_to_shared(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
 
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }

@@ -33,7 +33,7 @@
 // us at the measured bandwidth): 72 us, 57 with the products left out and 62 with the
 // loads left out: 614 instructions a warp for 32 tokens of a key head, the issue slots 47 %
 // and the integer pipe 41 % busy.  Without the rings (loads to registers as they were
-// wanted) 95.  Two tokens over 131071 64 us with heads outermost, 95 with tokens, whose
+// wanted) 95.  Two tokens over 131071 64 us with heads outermost, 66 with tokens, whose
 // runs are 64 bytes.  16 rows instead of 4 take 116 us; 20, by attend4.cu, 182.
 #include <type_traits>
 
@@ -130,12 +130,15 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {  // an 8 x 8 matrix
   return y;
 }
 
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {  // 16 bytes into shared memory
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+// 16 bytes into shared memory.  The L2 is to fetch 64 bytes around them, not the 128 that
+// it does by itself: with heads inside tokens, the rest is of another head.  Two tokens
+// over 131071: 94 -> 66 us; with heads outermost 64 either way.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 
 __device__ __forceinline__ void copy16_or_zeros(uint32_t to, const void* from, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
 
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
